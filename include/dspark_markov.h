@@ -281,6 +281,129 @@ dspark_status_t dspark_markov_apply_block_lm_head(const void* hidden_states, dsp
                                                   int64_t r, float* corrected_logits, void* workspace,
                                                   size_t workspace_bytes, void* stream);
 
+/* Rows of 8-bit integers with one scale each (the operands of the 8-bit
+ * vocabulary head; the head's rows once, when they are loaded):
+ *     scale[n] = max_i |x[n, i]| / 127,
+ *     q[n, i]  = clamp(rint(x[n, i] / scale[n]), -127, 127),
+ * both quotients in fp32, ties to even.  A row whose scale is zero gets zeros;
+ * a row that holds an infinity or NaN gets it as its scale, and zeros.
+ *   x      device, [rows, d], dtype (F32 or BF16).
+ *   q      device, [rows, d] int8 output; scale device, [rows] fp32 output.
+ * rows, d >= 0; d == 0 gives zero scales.  Outputs must not overlap x or
+ * each other. */
+dspark_status_t dspark_markov_quantize_rows(const void* x, dspark_dtype_t dtype, int64_t rows, int64_t d, int8_t* q,
+                                            float* scale, void* stream);
+
+/* The vocabulary head in 8-bit integers: the hidden states are quantised row
+ * by row as above (a scale for each token) and multiplied with the head's
+ * quantised rows (a scale for each vocabulary channel),
+ *     logits[n, v] = round_O( (scale[n] * head_scale[v]) * sum_i q[n, i] head_q[v, i] ),
+ * the sum exact in 32-bit integers, its conversion and the two products in
+ * fp32, one rounding to the output dtype.  It gives the base logits of the
+ * calls above (the bf16 head with the bias in the same kernel is
+ * dspark_markov_apply_block_lm_head).
+ *   hidden_states  device, [B, M, d], hidden_dtype (F32 or BF16).
+ *   head_q         device, [V, d] int8; head_scale device, [V] fp32.
+ *   logits         device, [B, M, V] output, logits_dtype; must not overlap
+ *                  an input.
+ * Any d from 1 to 131072 (the integer sum's range; above: DSPARK_ERR_UNSUPPORTED), any V and alignment;
+ * heads with d a multiple of 16 and a 16-byte aligned head_q are read fastest.
+ * B*M*V == 0 is a successful no-op.  The workspace must hold
+ * dspark_markov_lm_head_int8_workspace_bytes(...) bytes (no zero fill needed). */
+size_t dspark_markov_lm_head_int8_workspace_bytes(int64_t B, int64_t M, int64_t d);
+
+dspark_status_t dspark_markov_lm_head_int8(const void* hidden_states, dspark_dtype_t hidden_dtype, int64_t d,
+                                           const int8_t* head_q, const float* head_scale, int64_t B, int64_t M,
+                                           int64_t V, void* logits, dspark_dtype_t logits_dtype, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Rules on logits: penalties for repeated tokens, biases and grammar masks.
+ * All pointers are device memory; a null pointer turns its rule off.  With c
+ * the number of times token v stands among the counted outputs of row b, and
+ * "seen" whether it stands among any of its counted tokens,
+ *     x = logits[b, k, v]
+ *     seen:   x = x > 0 ? x / repetition_penalty[b] : x * repetition_penalty[b]
+ *     c > 0:  x = x - (frequency_penalty[b] * c + presence_penalty[b])
+ *     x = x + logit_bias[b, v]
+ *     token_mask bit 0: x = -inf (whatever stood there, NaN included)
+ * in fp32, rounded once to the logits' dtype.
+ *   history         [B] rows of history_len int64 ids, history_stride elements
+ *                   apart: the tokens of row b so far, prompt first.  Ids
+ *                   outside [0, V) are ignored.
+ *   lengths         [B] int64: how many of them count (clamped to
+ *                   [0, history_len]); null: all.  What lies behind is not read.
+ *   prompt_lengths  [B] int64: how many of those are the prompt's, which only
+ *                   the repetition penalty sees; null: none.
+ *   repetition_penalty, frequency_penalty, presence_penalty   [B] fp32.
+ *   logit_bias      [B] rows of V elements of bias_dtype (F32 or BF16),
+ *                   bias_stride elements apart; 0: one row for all.
+ *   token_mask      32 tokens a word, token v in bit v % 32 of word v / 32,
+ *                   set when allowed; the words of row (b, k) start at
+ *                   b * mask_stride_b + k * mask_stride_m (0: shared).  Bits
+ *                   past V are ignored. */
+typedef struct dspark_logit_rules {
+  const int64_t* history;
+  int64_t history_len;
+  int64_t history_stride;
+  const int64_t* lengths;
+  const int64_t* prompt_lengths;
+  const float* repetition_penalty;
+  const float* frequency_penalty;
+  const float* presence_penalty;
+  const void* logit_bias;
+  int64_t bias_stride;
+  dspark_dtype_t bias_dtype;
+  const uint32_t* token_mask;
+  int64_t mask_stride_b;
+  int64_t mask_stride_m;
+} dspark_logit_rules_t;
+
+/* The rules on given logits [B, M, V] (teacher-forced, or a single position
+ * with M = 1).
+ *   token_ids  [B, M] int64 or null: the predecessors of
+ *              dspark_markov_apply_block.  At position k the block's tokens
+ *              token_ids[b, 1 .. k] count as outputs besides the history
+ *              (token_ids[b, 0] is the history's last token).
+ *   processed  [B, M, V] output; may equal logits (in place); any other
+ *              overlap with an input is invalid.
+ * B*M*V == 0 is a successful no-op. */
+dspark_status_t dspark_markov_process_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* token_ids,
+                                            const dspark_logit_rules_t* rules, int64_t B, int64_t M, int64_t V,
+                                            void* processed, void* stream);
+
+/* Gradient of the rules with respect to the logits (the penalties, biases and
+ * masks are constants): grad_logits = grad_processed times 0 where masked
+ * (whatever stood there), else 1 / repetition_penalty[b] (logit > 0) or
+ * repetition_penalty[b] (logit <= 0 or NaN) where seen, else 1; in fp32,
+ * rounded once to the logits' dtype, which both gradients have.
+ *   grad_logits  [B, M, V] output; may equal grad_processed; any other overlap
+ *                with an input is invalid. */
+dspark_status_t dspark_markov_process_block_backward(const void* grad_processed, const void* logits,
+                                                     dspark_dtype_t logits_dtype, const int64_t* token_ids,
+                                                     const dspark_logit_rules_t* rules, int64_t B, int64_t M, int64_t V,
+                                                     void* grad_logits, void* stream);
+
+/* dspark_markov_sample_block under the rules: position k of row b draws from
+ * the processed corrected logits, and the tokens drawn before it count as
+ * outputs besides the history (which ends with first_prev).  Scores, noise and
+ * offsets as in dspark_markov_sample_block.  A row with nothing above -inf to
+ * draw from gets token -1; its next position then has an id outside [0, V) as
+ * predecessor, so no bias.  M = 1 is the single-token form.
+ *   processed_logits  device, [B, M, V] output (the processed rows); must not
+ *                     overlap an input.
+ * V up to 2^30.  The workspace must hold
+ * dspark_markov_processed_workspace_bytes(...) bytes, zero-filled once. */
+size_t dspark_markov_processed_workspace_bytes(int64_t B, int64_t M, int64_t V, int64_t r);
+
+dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, dspark_dtype_t logits_dtype,
+                                                     const int64_t* first_prev_token_ids, const void* w1,
+                                                     const void* w2, dspark_dtype_t weight_dtype,
+                                                     const dspark_logit_rules_t* rules, int64_t B, int64_t M,
+                                                     int64_t V, int64_t r, double temperature, uint64_t seed,
+                                                     int64_t position_offset, int64_t batch_offset,
+                                                     int64_t* sampled_tokens, void* processed_logits, void* workspace,
+                                                     size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then returns in *bad_rows the number of rows whose
  * predecessor id was outside [0, V) in the calls made with this workspace
  * since the last read, and clears the count.  Returns DSPARK_ERR_DEVICE when

@@ -18,6 +18,13 @@ The gated head (the pages' GatedMarkovHead) has the same two operations,
 ``apply_block_logits_gated`` and ``sample_block_tokens_gated``, which also
 take the backbone hidden states and the gate_proj weight and bias.
 
+For serving, ``lm_head_logits_int8`` computes base logits with the vocabulary
+head held in 8-bit integers (``quantize_rows`` makes them), and
+``process_block_logits`` applies a request's penalties for repeated tokens,
+biases and grammar masks to logits, ``sample_block_tokens_processed`` within
+the left-to-right draft; ``process_block_logits_backward`` is the rules'
+gradient.
+
 Tensors must live on the current HIP device.  ``w1`` is the Embedding
 weight [V, r]; ``w2`` is the Linear(r, V) weight [V, r].  This module only
 marshals arguments (dtype tags, pointers, sizes, the current stream) and
@@ -34,7 +41,9 @@ import torch
 from . import _lib
 
 __all__ = ["apply_block_logits", "sample_block_tokens", "apply_block_logits_gated",
-           "sample_block_tokens_gated", "apply_block_logits_backward", "apply_block_logits_lm_head", "Workspace",
+           "sample_block_tokens_gated", "apply_block_logits_backward", "apply_block_logits_lm_head",
+           "quantize_rows", "lm_head_logits_int8", "process_block_logits", "process_block_logits_backward",
+           "sample_block_tokens_processed", "Workspace",
            "read_device_error", "workspace_bytes"]
 
 
@@ -65,17 +74,23 @@ def workspace_bytes(B: int, M: int, V: int, r: int, sample: bool, hidden: int | 
 class Workspace:
     """Device workspace for a family of calls of at most the given sizes
     (``hidden``: the hidden size of gated calls; ``backward``: sized for the
-    backward as well).
+    backward as well; ``int8_hidden``: the hidden size of 8-bit head calls;
+    ``processed``: sized for sampling under logit rules as well).
 
     Zero-filled once at creation; the library leaves it ready for the next
     call.  Calls sharing one workspace must be ordered on one stream."""
 
     def __init__(self, B: int, M: int, V: int, r: int, sample: bool, device=None,
-                 hidden: int | None = None, backward: bool = False):
+                 hidden: int | None = None, backward: bool = False, int8_hidden: int | None = None,
+                 processed: bool = False):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.nbytes = max(workspace_bytes(B, M, V, r, sample, hidden), 256)
         if backward:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_backward_workspace_bytes(B, M, V, r)))
+        if int8_hidden is not None:
+            self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(B, M, int8_hidden)))
+        if processed:
+            self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_processed_workspace_bytes(B, M, V, r)))
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
         _lib.check(_lib.load().dspark_markov_workspace_init(
             _ptr(self.buffer), self.nbytes, _stream_handle(device)), "workspace_init")
@@ -409,3 +424,271 @@ def apply_block_logits_backward(grad_corrected: torch.Tensor, token_ids: torch.T
         workspace.ptr, workspace.nbytes, _stream_handle(dev))
     _lib.check(st, "apply_block_logits_backward")
     return gw1, gw2
+
+
+def quantize_rows(x: torch.Tensor, *, out: torch.Tensor | None = None, scale_out: torch.Tensor | None = None):
+    """Rows of 8-bit integers with one fp32 scale each: x [..., d] gives
+    ``(q [..., d] int8, scale [...])`` with scale = max|x| / 127 and
+    q = clamp(rint(x / scale), -127, 127).  A row of zeros has scale 0; a row
+    with an infinity or NaN has it as its scale (and zeros), so that what is
+    computed from the row shows it."""
+    if x.dim() < 1:
+        raise ValueError("x must be [..., d]")
+    _check_device(x.device, None, out=out, scale_out=scale_out)
+    tag = _dtype_tag(x)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+    elif out.shape != x.shape or out.dtype != torch.int8 or not out.is_contiguous():
+        raise ValueError("out must be a contiguous int8 tensor shaped like x")
+    if scale_out is None:
+        scale_out = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    elif scale_out.shape != x.shape[:-1] or scale_out.dtype != torch.float32 or not scale_out.is_contiguous():
+        raise ValueError(f"scale_out must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])}")
+    xc = x.contiguous()
+    with torch.cuda.device(x.device):
+        st = _lib.load().dspark_markov_quantize_rows(_ptr(xc), tag, scale_out.numel(), x.shape[-1], _ptr(out),
+                                                     _ptr(scale_out), _stream_handle(x.device))
+    _lib.check(st, "quantize_rows")
+    return out, scale_out
+
+
+def lm_head_logits_int8(hidden_states: torch.Tensor, head_q: torch.Tensor, head_scale: torch.Tensor, *,
+                        out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                        workspace: Workspace | None = None) -> torch.Tensor:
+    """Base logits [..., V] of hidden_states [..., d] through a vocabulary head
+    held in 8-bit integers: head_q [V, d] and head_scale [V] as quantize_rows
+    gives them for the head's Linear weight.  The hidden states are quantised
+    row by row in the call (one scale for each token), the products summed
+    exactly in 32-bit integers.  ``out_dtype``: float32 (default) or bfloat16."""
+    if hidden_states.dim() < 1:
+        raise ValueError("hidden_states must be [..., d]")
+    d = hidden_states.shape[-1]
+    if head_q.dim() != 2 or head_q.shape[1] != d or head_q.dtype != torch.int8:
+        raise ValueError(f"head_q must be int8 [V, {d}], got {head_q.dtype} {tuple(head_q.shape)}")
+    V = head_q.shape[0]
+    if tuple(head_scale.shape) != (V,) or head_scale.dtype != torch.float32:
+        raise ValueError(f"head_scale must be float32 [{V}], got {head_scale.dtype} {tuple(head_scale.shape)}")
+    dev = hidden_states.device
+    _check_device(dev, workspace, head_q=head_q, head_scale=head_scale, out=out)
+    tag = _dtype_tag(hidden_states)
+    shape = tuple(hidden_states.shape[:-1]) + (V,)
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != out_dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {out_dtype} tensor of shape {shape}")
+    out_tag = _dtype_tag(out)
+    if out.numel() == 0:
+        return out
+    rows = out.numel() // V
+    h, hq, hs = hidden_states.contiguous(), head_q.contiguous(), head_scale.contiguous()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            nbytes = int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(rows, 1, d))
+            buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+        else:
+            nbytes, buffer = workspace.nbytes, workspace.buffer
+        st = _lib.load().dspark_markov_lm_head_int8(_ptr(h), tag, d, _ptr(hq), _ptr(hs), rows, 1, V, _ptr(out), out_tag,
+                                                    _ptr(buffer), nbytes, _stream_handle(dev))
+    _lib.check(st, "lm_head_logits_int8")
+    return out
+
+
+def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, frequency_penalty, presence_penalty,
+                 logit_bias, token_mask):
+    """The rules as dspark_logit_rules_t, and the tensors it points into."""
+    keep = []
+
+    def per_request(t, name, dtype):
+        if t is None:
+            return None
+        if tuple(t.shape) != (B,):
+            raise ValueError(f"{name} must be [{B}], got {tuple(t.shape)}")
+        if t.is_floating_point() != dtype.is_floating_point:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        keep.append(t.to(dtype).contiguous())
+        return _ptr(keep[-1])
+
+    r = _lib.LogitRules()
+    if history is None and (lengths is not None or prompt_lengths is not None):
+        raise ValueError("lengths and prompt_lengths need a history")
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != B or history.is_floating_point():
+            raise ValueError(f"history must be integer ids [{B}, L], got {history.dtype} {tuple(history.shape)}")
+        h = history.to(torch.int64)
+        if h.shape[1] > 1 and h.stride(1) != 1 or B > 1 and h.stride(0) < h.shape[1]:
+            h = h.contiguous()
+        keep.append(h)
+        r.history, r.history_len, r.history_stride = _ptr(h), h.shape[1], h.stride(0) if B > 1 else h.shape[1]
+        r.lengths = per_request(lengths, "lengths", torch.int64)
+        r.prompt_lengths = per_request(prompt_lengths, "prompt_lengths", torch.int64)
+    r.repetition_penalty = per_request(repetition_penalty, "repetition_penalty", torch.float32)
+    r.frequency_penalty = per_request(frequency_penalty, "frequency_penalty", torch.float32)
+    r.presence_penalty = per_request(presence_penalty, "presence_penalty", torch.float32)
+    if logit_bias is not None:
+        if tuple(logit_bias.shape) not in ((V,), (1, V), (B, V)):
+            raise ValueError(f"logit_bias must be [{V}] or [{B}, {V}], got {tuple(logit_bias.shape)}")
+        r.bias_dtype = _dtype_tag(logit_bias)
+        bias = logit_bias.contiguous()
+        keep.append(bias)
+        r.logit_bias, r.bias_stride = _ptr(bias), V if bias.dim() == 2 and bias.shape[0] > 1 else 0
+    if token_mask is not None:
+        W = (V + 31) // 32
+        if token_mask.dtype != torch.int32:
+            raise TypeError(f"token_mask must be int32 words of 32 tokens, got {token_mask.dtype}")
+        mask = token_mask[:, None] if token_mask.dim() == 2 else token_mask
+        if mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] not in (1, M) or mask.shape[2] != W:
+            raise ValueError(f"token_mask must be [{B}, {W}] or [{B}, {M}, {W}] (or 1 in place of either size), "
+                             f"got {tuple(token_mask.shape)}")
+        if W > 1 and mask.stride(2) != 1 or any(s < 0 for s in mask.stride()):
+            mask = mask.contiguous()
+        keep.append(mask)
+        r.token_mask = _ptr(mask)
+        r.mask_stride_b = mask.stride(0) if mask.shape[0] > 1 else 0
+        r.mask_stride_m = mask.stride(1) if mask.shape[1] > 1 else 0
+    for name, t in (("history", history), ("lengths", lengths), ("prompt_lengths", prompt_lengths),
+                    ("repetition_penalty", repetition_penalty), ("frequency_penalty", frequency_penalty),
+                    ("presence_penalty", presence_penalty), ("logit_bias", logit_bias), ("token_mask", token_mask)):
+        _check_device(dev, None, **{name: t})
+    return r, keep
+
+
+def _block(logits, token_ids, what):
+    if logits.dim() != 3:
+        raise ValueError(f"{what} must be [B, M, V]")
+    if token_ids is not None and (tuple(token_ids.shape) != tuple(logits.shape[:2]) or token_ids.is_floating_point()):
+        raise ValueError(f"token_ids must be integer ids of shape {tuple(logits.shape[:2])}")
+    return logits.shape
+
+
+def process_block_logits(logits: torch.Tensor, *, token_ids: torch.Tensor | None = None,
+                         history: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                         prompt_lengths: torch.Tensor | None = None, repetition_penalty: torch.Tensor | None = None,
+                         frequency_penalty: torch.Tensor | None = None, presence_penalty: torch.Tensor | None = None,
+                         logit_bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and grammar masks on logits
+    [B, M, V] (M = 1: a single token each).  For a token that stands in the
+    request's counted tokens x becomes x / repetition_penalty (x > 0) or
+    x * repetition_penalty; for one that stands c times among its outputs
+    frequency_penalty * c + presence_penalty is taken off; then the bias is
+    added; a masked token is -inf.  fp32 arithmetic, one rounding.
+
+    ``history`` [B, L]: each request's tokens, prompt first; ``lengths`` [B]
+    how many count (default: all; what lies behind is not read; ids outside
+    the vocabulary are ignored), ``prompt_lengths`` [B] how many of them are
+    the prompt's (default: none), which only the repetition penalty sees.
+    ``token_ids`` [B, M]: the predecessors of apply_block_logits; at position k
+    the tokens token_ids[:, 1 .. k] count as outputs too (the first is the
+    history's last).  The penalties are [B]; ``logit_bias`` [V] or [B, V];
+    ``token_mask`` int32 words of 32 tokens, [B, W] or [B, M, W] (either size
+    may be 1), bit set: allowed.  Rules not given are off.  ``out`` may be
+    ``logits`` itself (in place)."""
+    B, M, V = _block(logits, token_ids, "logits")
+    dev = logits.device
+    _check_device(dev, None, token_ids=token_ids, out=out)
+    tag = _dtype_tag(logits)
+    rules, keep = _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, frequency_penalty,
+                               presence_penalty, logit_bias, token_mask)
+    x = logits.contiguous()
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor shaped and typed like logits")
+    ids = None if token_ids is None else token_ids.to(torch.int64).contiguous()
+    with torch.cuda.device(dev):
+        st = _lib.load().dspark_markov_process_block(_ptr(x), tag, _ptr(ids), rules, B, M, V, _ptr(out),
+                                                     _stream_handle(dev))
+    _lib.check(st, "process_block_logits")
+    return out
+
+
+def process_block_logits_backward(grad_processed: torch.Tensor, logits: torch.Tensor, *,
+                                  token_ids: torch.Tensor | None = None, history: torch.Tensor | None = None,
+                                  lengths: torch.Tensor | None = None, prompt_lengths: torch.Tensor | None = None,
+                                  repetition_penalty: torch.Tensor | None = None,
+                                  token_mask: torch.Tensor | None = None,
+                                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the logits [B, M, V] for the gradient of what
+    process_block_logits made of them: 0 where masked, the repetition
+    penalty's slope where the token was seen (1 / penalty for a logit above
+    zero, else the penalty), else the gradient itself.  ``logits`` and the
+    rules as in the forward call (frequency and presence penalties and biases
+    only shift, so they are not asked for); ``out`` may be
+    ``grad_processed`` itself."""
+    B, M, V = _block(logits, token_ids, "logits")
+    if grad_processed.shape != logits.shape or grad_processed.dtype != logits.dtype:
+        raise ValueError("grad_processed must be shaped and typed like logits")
+    dev = logits.device
+    _check_device(dev, None, grad_processed=grad_processed, token_ids=token_ids, out=out)
+    tag = _dtype_tag(logits)
+    rules, keep = _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, None, None, None,
+                               token_mask)
+    g, x = grad_processed.contiguous(), logits.contiguous()
+    if out is None:
+        out = torch.empty_like(g)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor shaped and typed like logits")
+    ids = None if token_ids is None else token_ids.to(torch.int64).contiguous()
+    with torch.cuda.device(dev):
+        st = _lib.load().dspark_markov_process_block_backward(_ptr(g), _ptr(x), tag, _ptr(ids), rules, B, M, V, _ptr(out),
+                                                              _stream_handle(dev))
+    _lib.check(st, "process_block_logits_backward")
+    return out
+
+
+def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_ids: torch.Tensor, w1: torch.Tensor,
+                                  w2: torch.Tensor, temperature: float | None = 0.0, *,
+                                  history: torch.Tensor | None = None, lengths: torch.Tensor | None = None,
+                                  prompt_lengths: torch.Tensor | None = None,
+                                  repetition_penalty: torch.Tensor | None = None,
+                                  frequency_penalty: torch.Tensor | None = None,
+                                  presence_penalty: torch.Tensor | None = None,
+                                  logit_bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                                  seed: int = 0, position_offset: int = 0, batch_offset: int = 0,
+                                  tokens_out: torch.Tensor | None = None, logits_out: torch.Tensor | None = None,
+                                  workspace: Workspace | None = None):
+    """sample_block_tokens under the rules of process_block_logits: position k
+    draws from the processed corrected logits, and the tokens drawn before it
+    count as outputs beside ``history`` (which ends with
+    first_prev_token_ids).  Returns ``(tokens [B, M], processed [B, M, V])``.
+    A row left with nothing above -inf gets token -1 (the position after it
+    then has no bias).  M = 1 with ``position_offset`` is the single-token
+    form, for masks that depend on the tokens drawn."""
+    _check_weights(w1, w2)
+    B, M, V = _block(base_logits, None, "base_logits")
+    if tuple(first_prev_token_ids.shape) != (B,):
+        raise ValueError("first_prev_token_ids must be [B]")
+    if w1.shape[0] != V:
+        raise ValueError(f"weights have vocabulary {w1.shape[0]}, logits {V}")
+    T = 0.0 if temperature is None else float(temperature)
+    dev = base_logits.device
+    _check_device(dev, workspace, first_prev_token_ids=first_prev_token_ids, w1=w1, w2=w2, tokens_out=tokens_out,
+                  logits_out=logits_out)
+    tag, wtag = _dtype_tag(base_logits), _dtype_tag(w1)
+    rules, keep = _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, frequency_penalty,
+                               presence_penalty, logit_bias, token_mask)
+    if tokens_out is None:
+        tokens_out = torch.empty((B, M), dtype=torch.int64, device=dev)
+    elif tuple(tokens_out.shape) != (B, M) or tokens_out.dtype != torch.int64 or not tokens_out.is_contiguous():
+        raise ValueError(f"tokens_out must be a contiguous int64 tensor of shape {(B, M)}")
+    if logits_out is None:
+        logits_out = torch.empty(base_logits.shape, dtype=base_logits.dtype, device=dev)
+    elif logits_out.shape != base_logits.shape or logits_out.dtype != base_logits.dtype or not logits_out.is_contiguous():
+        raise ValueError("logits_out must be a contiguous tensor shaped and typed like base_logits")
+    if B == 0 or M == 0:
+        return tokens_out, logits_out
+    base = base_logits.contiguous()
+    first = first_prev_token_ids.to(torch.int64).contiguous()
+    w1c, w2c = w1.contiguous(), w2.contiguous()
+    r = w1.shape[1]
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = Workspace(B, M, V, r, sample=True, device=dev, processed=True)
+        st = _lib.load().dspark_markov_sample_block_processed(
+            _ptr(base), tag, _ptr(first), _ptr(w1c), _ptr(w2c), wtag, rules, B, M, V, r, T, int(seed) & (2**64 - 1),
+            int(position_offset), int(batch_offset), _ptr(tokens_out), _ptr(logits_out), workspace.ptr, workspace.nbytes,
+            _stream_handle(dev))
+    _lib.check(st, "sample_block_tokens_processed")
+    return tokens_out, logits_out

@@ -41,12 +41,40 @@ EXPORTS = (
     "dspark_markov_backward_workspace_bytes",
     "dspark_markov_apply_block_backward",
     "dspark_markov_apply_block_lm_head",
+    "dspark_markov_quantize_rows",
+    "dspark_markov_lm_head_int8_workspace_bytes",
+    "dspark_markov_lm_head_int8",
+    "dspark_markov_process_block",
+    "dspark_markov_process_block_backward",
+    "dspark_markov_processed_workspace_bytes",
+    "dspark_markov_sample_block_processed",
     "dspark_markov_read_device_error",
     "dspark_status_string",
     "dspark_markov_last_error",
 )
 
 _lib = None
+
+
+class LogitRules(ctypes.Structure):
+    """dspark_logit_rules_t: device pointers (None: that rule is off), lengths and strides."""
+
+    _fields_ = [
+        ("history", ctypes.c_void_p),
+        ("history_len", ctypes.c_int64),
+        ("history_stride", ctypes.c_int64),
+        ("lengths", ctypes.c_void_p),
+        ("prompt_lengths", ctypes.c_void_p),
+        ("repetition_penalty", ctypes.c_void_p),
+        ("frequency_penalty", ctypes.c_void_p),
+        ("presence_penalty", ctypes.c_void_p),
+        ("logit_bias", ctypes.c_void_p),
+        ("bias_stride", ctypes.c_int64),
+        ("bias_dtype", ctypes.c_int),
+        ("token_mask", ctypes.c_void_p),
+        ("mask_stride_b", ctypes.c_int64),
+        ("mask_stride_m", ctypes.c_int64),
+    ]
 
 
 class DsparkError(RuntimeError):
@@ -102,6 +130,22 @@ def load():
     L.dspark_markov_apply_block_lm_head.argtypes = [p, i32, i64, p, i32, p, p, p, i32, i64, i64, i64, i64, p, p,
                                                     sz, p]
     L.dspark_markov_apply_block_lm_head.restype = i32
+    rules = ctypes.POINTER(LogitRules)
+    L.dspark_markov_quantize_rows.argtypes = [p, i32, i64, i64, p, p, p]
+    L.dspark_markov_quantize_rows.restype = i32
+    L.dspark_markov_lm_head_int8_workspace_bytes.argtypes = [i64, i64, i64]
+    L.dspark_markov_lm_head_int8_workspace_bytes.restype = sz
+    L.dspark_markov_lm_head_int8.argtypes = [p, i32, i64, p, p, i64, i64, i64, p, i32, p, sz, p]
+    L.dspark_markov_lm_head_int8.restype = i32
+    L.dspark_markov_process_block.argtypes = [p, i32, p, rules, i64, i64, i64, p, p]
+    L.dspark_markov_process_block.restype = i32
+    L.dspark_markov_process_block_backward.argtypes = [p, p, i32, p, rules, i64, i64, i64, p, p]
+    L.dspark_markov_process_block_backward.restype = i32
+    L.dspark_markov_processed_workspace_bytes.argtypes = [i64, i64, i64, i64]
+    L.dspark_markov_processed_workspace_bytes.restype = sz
+    L.dspark_markov_sample_block_processed.argtypes = [p, i32, p, p, p, i32, rules, i64, i64, i64, i64,
+                                                       ctypes.c_double, u64, i64, i64, p, p, p, sz, p]
+    L.dspark_markov_sample_block_processed.restype = i32
     L.dspark_markov_read_device_error.argtypes = [p, p, ctypes.POINTER(i64)]
     L.dspark_markov_read_device_error.restype = i32
     L.dspark_status_string.argtypes = [i32]

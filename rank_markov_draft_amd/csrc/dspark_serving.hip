@@ -1,0 +1,369 @@
+// dspark_serving.hip -- host side of the 8-bit vocabulary head and of the
+// logit rules (include/dspark_markov.h): argument validation, workspace
+// layout and launches.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "dspark_markov.h"
+#include "host_common.h"
+#include "int8_head.h"
+#include "logit_rules.h"
+#include "markov_kernels.h"
+
+namespace {
+
+using namespace dspark::host;
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// ---- 8-bit head: the quantised rows, then their scales and the floats past
+// them that the product reads in whole vectors
+size_t int8_rows_bytes(int64_t rows, int64_t d) {
+  return align256(mul_sz((size_t)rows, (size_t)round_up(d, dspark::kInt8K)));
+}
+size_t int8_scales_bytes(int64_t rows) {
+  return align256(mul_sz(add_sz((size_t)rows, (size_t)dspark::kInt8RowPad), sizeof(float)));
+}
+
+// ---- logit rules
+// Byte ranges that a call's rules read, for the overlap checks.
+struct Ranges {
+  const void* at[16];
+  size_t bytes[16];
+  int n = 0;
+  void add(const void* p, size_t b) {
+    at[n] = p;
+    bytes[n++] = b;
+  }
+  bool meet(const void* p, size_t b) const {
+    for (int i = 0; i < n; ++i)
+      if (overlaps(p, b, at[i], bytes[i])) return true;
+    return false;
+  }
+};
+
+// Bytes from the first to the last element of `count` rows of `len` elements
+// `stride` apart; -1 when they cannot be represented.
+int64_t extent(int64_t count, int64_t stride, int64_t len, int64_t size) {
+  int64_t t = 0;
+  if (count <= 0 || len <= 0) return 0;
+  if (!mul_ok(count - 1, stride, &t) || __builtin_add_overflow(t, len, &t) || !mul_ok(t, size, &t)) return -1;
+  return t;
+}
+
+dspark_status_t check_rules(const dspark_logit_rules_t* c, int64_t B, int64_t M, int64_t V, dspark::RuleSet* r,
+                            Ranges* in) {
+  if (!c) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (c->history && (c->history_len < 0 || (B > 1 && c->history_stride < c->history_len)))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  if (c->logit_bias && (!known_dtype(c->bias_dtype) || (c->bias_stride != 0 && c->bias_stride < V)))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  if (c->token_mask && (c->mask_stride_b < 0 || c->mask_stride_m < 0)) return DSPARK_ERR_INVALID_ARGUMENT;
+  const int64_t W = dspark::rule_words(V);
+  const size_t vec = (size_t)B * sizeof(float), ids = (size_t)B * sizeof(int64_t);
+  int64_t hist = 0, bias = 0, mask = 0, mm = 0;
+  if (c->history && c->history_len > 0) hist = extent(B, B > 1 ? c->history_stride : 0, c->history_len, 8);
+  if (c->logit_bias) bias = extent(B, c->bias_stride, V, (int64_t)dtype_bytes(c->bias_dtype));
+  if (c->token_mask) {
+    if (!mul_ok(M - 1, c->mask_stride_m, &mm) || __builtin_add_overflow(mm, W, &mm)) return DSPARK_ERR_INVALID_ARGUMENT;
+    mask = extent(B, c->mask_stride_b, mm, 4);
+  }
+  if (hist < 0 || bias < 0 || mask < 0) return DSPARK_ERR_INVALID_ARGUMENT;
+  in->add(c->history, (size_t)hist);
+  in->add(c->history ? c->lengths : nullptr, ids);
+  in->add(c->history ? c->prompt_lengths : nullptr, ids);
+  in->add(c->repetition_penalty, vec);
+  in->add(c->frequency_penalty, vec);
+  in->add(c->presence_penalty, vec);
+  in->add(c->logit_bias, (size_t)bias);
+  in->add(c->token_mask, (size_t)mask);
+  *r = dspark::RuleSet{};
+  if (c->history && c->history_len > 0) {
+    r->history = c->history;
+    r->lengths = c->lengths;
+    r->prompt_lengths = c->prompt_lengths;
+    r->history_len = c->history_len;
+    r->history_stride = B > 1 ? c->history_stride : 0;
+  }
+  r->repetition = c->repetition_penalty;
+  r->frequency = c->frequency_penalty;
+  r->presence = c->presence_penalty;
+  r->bias = c->logit_bias;
+  r->bias_stride = c->bias_stride;
+  r->bias_bf16 = c->logit_bias && c->bias_dtype == DSPARK_BF16;
+  r->mask = c->token_mask;
+  r->mask_stride_b = c->mask_stride_b;
+  r->mask_stride_m = c->mask_stride_m;
+  return DSPARK_OK;
+}
+
+// The rules on logits, or their gradient (grad not null).
+dspark_status_t run_rules(const void* grad, const void* logits, dspark_dtype_t dtype, const int64_t* token_ids,
+                          const dspark_logit_rules_t* rules, int64_t B, int64_t M, int64_t V, void* out, bool backward,
+                          void* stream) {
+  if (!known_dtype(dtype) || B < 0 || M < 0 || V < 0) return DSPARK_ERR_INVALID_ARGUMENT;
+  int64_t rows = 0, elems = 0, bytes = 0;
+  if (!mul_ok(B, M, &rows) || !mul_ok(rows, V, &elems) || !mul_ok(elems, 4, &bytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (V > ((int64_t)1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  if (!rules) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (elems == 0) return DSPARK_OK;
+  dspark::RulesParams p{};
+  Ranges in;
+  const dspark_status_t st = check_rules(rules, B, M, V, &p.r, &in);
+  if (st != DSPARK_OK) return st;
+  if (!logits || !out || (backward && !grad)) return DSPARK_ERR_INVALID_ARGUMENT;
+  const size_t lbytes = (size_t)elems * dtype_bytes(dtype);
+  in.add(token_ids, (size_t)rows * sizeof(int64_t));
+  const void* const streamed = backward ? grad : logits;
+  if (out != streamed && overlaps(out, lbytes, streamed, lbytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (backward && overlaps(out, lbytes, logits, lbytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (in.meet(out, lbytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (backward) p.r.bias = nullptr;
+  p.logits = logits;
+  p.grad = grad;
+  p.out = out;
+  p.token_ids = token_ids;
+  p.B = B;
+  p.M = M;
+  p.V = V;
+  const int cus = device_cus();
+  const hipError_t e = dspark::launch_logit_rules(p, dtype == DSPARK_BF16, cus > 0 ? cus : 1, (hipStream_t)stream);
+  if (e == hipErrorNotSupported) {
+    (void)hipGetLastError();
+    return DSPARK_ERR_UNSUPPORTED;
+  }
+  if (e != hipSuccess) return device_failure(e, "logit rules launch");
+  return DSPARK_OK;
+}
+
+// Workspace of a processed draft past the vanilla sampling layout: the table's
+// bits, then its counts.
+size_t table_bits_bytes(int64_t B, int64_t V) {
+  return align256(mul_sz(mul_sz((size_t)B, (size_t)dspark::rule_words(V)), 4));
+}
+size_t table_counts_bytes(int64_t B, int64_t V) { return align256(mul_sz(mul_sz((size_t)B, (size_t)V), 4)); }
+
+// Corrected logits of step k into p.out by the sampling step's kernels.
+hipError_t corrected_step(dspark::KernelParams& p, bool tile, bool f32_tile, bool logits_bf16, bool weights_bf16,
+                          int cus, hipStream_t s) {
+  hipError_t e = hipErrorNotSupported;
+  if (tile || f32_tile) {
+    p.nparts = dspark::sample_step_parts(p.V);
+    e = dspark::launch_sample_step(p, f32_tile, cus, s);
+    if (e == hipErrorNotSupported && tile) {
+      (void)hipGetLastError();
+      p.nparts = vocab_slices(p.V);
+      e = dspark::launch_tile(p, s);
+    }
+  }
+  if (e == hipErrorNotSupported) {
+    (void)hipGetLastError();
+    p.nparts = dspark::generic_parts(p.V);
+    e = dspark::launch_generic(p, logits_bf16, weights_bf16, s);
+  }
+  return e;
+}
+
+}  // namespace
+
+extern "C" {
+
+dspark_status_t dspark_markov_quantize_rows(const void* x, dspark_dtype_t dtype, int64_t rows, int64_t d, int8_t* q,
+                                            float* scale, void* stream) {
+  if (!known_dtype(dtype) || rows < 0 || d < 0) return DSPARK_ERR_INVALID_ARGUMENT;
+  int64_t n = 0, bytes = 0;
+  if (!mul_ok(rows, d, &n) || !mul_ok(n, 4, &bytes) || !mul_ok(rows, 4, &bytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (rows > (int64_t)0x7FFFFFFF) return DSPARK_ERR_UNSUPPORTED;
+  if (rows == 0) return DSPARK_OK;
+  if (!scale || (d > 0 && (!x || !q))) return DSPARK_ERR_INVALID_ARGUMENT;
+  const size_t xb = (size_t)n * dtype_bytes(dtype), sb = (size_t)rows * sizeof(float);
+  if (overlaps(q, (size_t)n, x, xb) || overlaps(scale, sb, x, xb) || overlaps(q, (size_t)n, scale, sb))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  const hipStream_t s = (hipStream_t)stream;
+  const dspark::QuantizeParams p{x, q, scale, rows, d, d};
+  const hipError_t e = d == 0 ? dspark::launch_fill_zero(scale, sb, s) : dspark::launch_quantize_rows(p, dtype == DSPARK_BF16, s);
+  if (e != hipSuccess) return device_failure(e, "quantize launch");
+  return DSPARK_OK;
+}
+
+size_t dspark_markov_lm_head_int8_workspace_bytes(int64_t B, int64_t M, int64_t d) {
+  if (B < 0 || M < 0 || d < 0 || d > dspark::kInt8MaxInner) return kDataOffset;
+  int64_t rows = 0;
+  if (!mul_ok(B, M, &rows)) return SIZE_MAX;
+  return add_sz(kDataOffset, add_sz(int8_rows_bytes(rows, d), int8_scales_bytes(rows)));
+}
+
+dspark_status_t dspark_markov_lm_head_int8(const void* hidden_states, dspark_dtype_t hidden_dtype, int64_t d,
+                                           const int8_t* head_q, const float* head_scale, int64_t B, int64_t M,
+                                           int64_t V, void* logits, dspark_dtype_t logits_dtype, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (!known_dtype(hidden_dtype) || !known_dtype(logits_dtype)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (B < 0 || M < 0 || V < 0 || d <= 0) return DSPARK_ERR_INVALID_ARGUMENT;
+  int64_t rows = 0, elems = 0, t = 0;
+  if (!mul_ok(B, M, &rows) || !mul_ok(rows, V, &elems) || !mul_ok(elems, 4, &t) || !mul_ok(V, d, &t) ||
+      !mul_ok(rows, d, &t) || !mul_ok(t, 4, &t))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  if (d > dspark::kInt8MaxInner) {
+    dspark::set_last_error("lm_head_int8: the hidden size must be at most 131072");
+    return DSPARK_ERR_UNSUPPORTED;
+  }
+  if (rows > (int64_t)0x7FFFFFFF || V > (int64_t)0x7FFFFFFF) return DSPARK_ERR_UNSUPPORTED;
+  if (elems == 0) return DSPARK_OK;
+  if (!hidden_states || !head_q || !head_scale || !logits) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dspark_markov_lm_head_int8_workspace_bytes(B, M, d))
+    return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t obytes = (size_t)elems * dtype_bytes(logits_dtype);
+  Ranges in;
+  in.add(hidden_states, (size_t)(rows * d) * dtype_bytes(hidden_dtype));
+  in.add(head_q, (size_t)(V * d));
+  in.add(head_scale, (size_t)V * sizeof(float));
+  if (in.meet(logits, obytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  const hipStream_t s = (hipStream_t)stream;
+  dspark::Int8HeadParams p{};
+  int8_t* const xq = (int8_t*)workspace + kDataOffset;
+  float* const xs = (float*)(xq + int8_rows_bytes(rows, d));
+  p.xq = xq;
+  p.xs = xs;
+  p.wq = head_q;
+  p.ws = head_scale;
+  p.out = logits;
+  p.rows = rows;
+  p.V = V;
+  p.d = d;
+  p.ldx = round_up(d, dspark::kInt8K);
+  const dspark::QuantizeParams q{hidden_states, xq, xs, rows, d, p.ldx};
+  hipError_t e = dspark::launch_quantize_rows(q, hidden_dtype == DSPARK_BF16, s);
+  if (e != hipSuccess) return device_failure(e, "hidden state quantize launch");
+  e = dspark::launch_int8_head(p, logits_dtype == DSPARK_BF16, device_cus(), s);
+  if (e == hipErrorNotSupported) {
+    (void)hipGetLastError();
+    return DSPARK_ERR_UNSUPPORTED;
+  }
+  if (e != hipSuccess) return device_failure(e, "int8 head launch");
+  return DSPARK_OK;
+}
+
+dspark_status_t dspark_markov_process_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* token_ids,
+                                            const dspark_logit_rules_t* rules, int64_t B, int64_t M, int64_t V,
+                                            void* processed, void* stream) {
+  return run_rules(nullptr, logits, logits_dtype, token_ids, rules, B, M, V, processed, false, stream);
+}
+
+dspark_status_t dspark_markov_process_block_backward(const void* grad_processed, const void* logits,
+                                                     dspark_dtype_t logits_dtype, const int64_t* token_ids,
+                                                     const dspark_logit_rules_t* rules, int64_t B, int64_t M, int64_t V,
+                                                     void* grad_logits, void* stream) {
+  // only the repetition penalty has a slope: the others shift
+  dspark_logit_rules_t slope{};
+  if (rules) {
+    slope = *rules;
+    slope.frequency_penalty = slope.presence_penalty = nullptr;
+  }
+  return run_rules(grad_processed, logits, logits_dtype, token_ids, rules ? &slope : nullptr, B, M, V, grad_logits, true,
+                   stream);
+}
+
+size_t dspark_markov_processed_workspace_bytes(int64_t B, int64_t M, int64_t V, int64_t r) {
+  const size_t base = align256(dspark_markov_workspace_bytes(B, M, V, r, 1));
+  if (B < 0 || M < 0 || V < 0) return base;
+  return add_sz(base, add_sz(table_bits_bytes(B, V), table_counts_bytes(B, V)));
+}
+
+dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, dspark_dtype_t logits_dtype,
+                                                     const int64_t* first_prev_token_ids, const void* w1,
+                                                     const void* w2, dspark_dtype_t weight_dtype,
+                                                     const dspark_logit_rules_t* rules, int64_t B, int64_t M,
+                                                     int64_t V, int64_t r, double temperature, uint64_t seed,
+                                                     int64_t position_offset, int64_t batch_offset,
+                                                     int64_t* sampled_tokens, void* processed_logits, void* workspace,
+                                                     size_t workspace_bytes, void* stream) {
+  int64_t elems = 0;
+  dspark_status_t st = check_common(logits_dtype, weight_dtype, B, M, V, r, &elems);
+  if (st != DSPARK_OK) return st;
+  if (std::isnan(temperature) || !rules) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (V > ((int64_t)1 << 30) || r > kGenericMaxRank) return DSPARK_ERR_UNSUPPORTED;
+  if (B == 0 || M == 0) return DSPARK_OK;
+  if (V == 0) return DSPARK_ERR_INVALID_ARGUMENT;  // nothing to draw from
+  dspark::SelectParams c{};
+  Ranges in;
+  st = check_rules(rules, B, M, V, &c.r, &in);
+  if (st != DSPARK_OK) return st;
+  if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !processed_logits)
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dspark_markov_processed_workspace_bytes(B, M, V, r))
+    return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t lbytes = (size_t)elems * dtype_bytes(logits_dtype);
+  const size_t wbytes = (size_t)(V * r) * dtype_bytes(weight_dtype);
+  const size_t tbytes = (size_t)(B * M) * sizeof(int64_t);
+  in.add(base_logits, lbytes);
+  in.add(w1, wbytes);
+  in.add(w2, wbytes);
+  in.add(first_prev_token_ids, (size_t)B * sizeof(int64_t));
+  if (in.meet(sampled_tokens, tbytes) || in.meet(processed_logits, lbytes) ||
+      overlaps(processed_logits, lbytes, sampled_tokens, tbytes))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+
+  const hipStream_t s = (hipStream_t)stream;
+  const bool lbf = logits_dtype == DSPARK_BF16, wbf = weight_dtype == DSPARK_BF16;
+  const int cus = device_cus();
+  char* const region = (char*)workspace + align256(dspark_markov_workspace_bytes(B, M, V, r, 1));
+  uint32_t* const seen = (uint32_t*)region;
+  uint32_t* const counts = (uint32_t*)(region + table_bits_bytes(B, V));
+  // without penalties, or with nothing before a single position, no token is
+  // ever looked up
+  const bool table = dspark::rules_penalise(c.r) && (c.r.history != nullptr || M > 1);
+  hipError_t e = hipSuccess;
+  if (table) {
+    const dspark::TableParams t{c.r, seen, counts, B, V};
+    e = dspark::launch_rule_table(t, cus, s);
+    if (e != hipSuccess) return device_failure(e, "rule table launch");
+  }
+  const bool greedy = temperature < 1e-5;
+  dspark::KernelParams p{};
+  p.base = base_logits;
+  p.out = processed_logits;
+  p.ids = first_prev_token_ids;
+  p.tokens = sampled_tokens;
+  p.w1 = w1;
+  p.w2 = w2;
+  p.bad_rows = (uint32_t*)workspace;
+  p.partials = (uint64_t*)((char*)workspace + kDataOffset);
+  p.rows = B;
+  p.V = V;
+  p.r = r;
+  p.M = M;
+  p.mode = dspark::MODE_GREEDY;  // its keys are not used: the rules come first
+  const bool tile = tile_path(logits_dtype, weight_dtype, V, r, base_logits, processed_logits, w1, w2);
+  const bool f32_tile =
+      !lbf && tile_path(DSPARK_BF16, weight_dtype, V, r, base_logits, processed_logits, w1, w2);
+  c.logits = processed_logits;
+  c.seen = table ? seen : nullptr;
+  c.counts = counts;
+  c.partials = p.partials;
+  c.B = B;
+  c.M = M;
+  c.V = V;
+  c.batch_offset = batch_offset;
+  c.kappa = greedy ? 0.0f : (float)(1.4426950408889634 / temperature);
+  c.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
+  c.seed_hi = (uint32_t)(seed >> 32);
+  c.greedy = greedy;
+  for (int64_t k = 0; k < M; ++k) {
+    p.k = k;
+    p.k_abs = (uint32_t)(position_offset + k);
+    c.k = k;
+    c.k_abs = p.k_abs;
+    e = corrected_step(p, tile, f32_tile, lbf, wbf, cus, s);
+    if (e != hipSuccess) return device_failure(e, "corrected step launch");
+    e = dspark::launch_rule_select(c, lbf, s);
+    if (e != hipSuccess) return device_failure(e, "rule select launch");
+    e = dspark::launch_rule_choose(c.partials, dspark::select_parts(V), B, M, k, V, sampled_tokens,
+                                   table ? seen : nullptr, counts, s);
+    if (e != hipSuccess) return device_failure(e, "token choice launch");
+  }
+  return DSPARK_OK;
+}
+
+}  // extern "C"
