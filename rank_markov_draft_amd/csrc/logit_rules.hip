@@ -17,8 +17,8 @@
 // column, whether its token stands in the history.  A workgroup owns one
 // request and one tile of the vocabulary: it walks the request's ids once,
 // keeps those of its tile as a bitmap and counts in LDS, then streams the
-// tile of all M positions past that table.  The ids are re-read once per tile
-// of the vocabulary, from L2; nothing is sorted or written to memory.
+// tile of the request's positions past that table.  The ids are re-read once
+// per tile of the vocabulary, from L2; nothing is sorted or written to memory.
 #include "device_common.h"
 #include "logit_rules.h"
 
@@ -27,18 +27,6 @@ namespace dspark {
 namespace {
 
 constexpr int kRuleThreads = 256;
-
-// Bits c .. c + 7 of a bitmap of n words (c may lie outside: zeros there).
-__device__ __forceinline__ uint32_t bits8(const uint32_t* w, int n, int c) {
-  const int i = c >> 5;
-  const uint32_t lo = (uint32_t)i < (uint32_t)n ? w[i] : 0u;
-  const uint32_t hi = (uint32_t)(i + 1) < (uint32_t)n ? w[i + 1] : 0u;
-  return (uint32_t)((((uint64_t)hi << 32) | lo) >> (c & 31)) & 0xFFu;
-}
-
-__device__ __forceinline__ float bias_at(const RuleSet& r, int64_t i) {
-  return r.bias_bf16 ? bf16_lo(((const uint16_t*)r.bias)[i]) : ((const float*)r.bias)[i];
-}
 
 // A request's penalties; a rule that is off leaves x as it is.
 struct Penalty {
@@ -86,171 +74,242 @@ __device__ __forceinline__ void count_history(const RuleSet& r, int64_t b, int64
   }
 }
 
-// The 8 values at columns c .. c + 7 of a row; `full`: all of them exist and
-// the vector may be loaded whole, else those with c + i in [0, n).
+// Vectors of rows that start at any element (an odd vocabulary): the hardware
+// loads and stores 16 bytes at any address.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+
+// 8 consecutive values of a row as they are stored.
 template <bool BF>
-__device__ __forceinline__ void load8(const void* row, int c, int n, bool full, float (&x)[8]) {
-  if (full) {
+struct Raw8 {
+  u32x4_t w[BF ? 1 : 2];
+  __device__ __forceinline__ float operator[](int i) const {
     if constexpr (BF) {
-      const u32x4_t w = __builtin_nontemporal_load((const u32x4_t*)((const uint16_t*)row + c));
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(q[i]);
-        x[2 * i + 1] = bf16_hi(q[i]);
-      }
+      const uint32_t q = w[0][i >> 1];
+      return (i & 1) ? bf16_hi(q) : bf16_lo(q);
     } else {
-      const f32x4_t a = __builtin_nontemporal_load((const f32x4_t*)((const float*)row + c));
-      const f32x4_t b = __builtin_nontemporal_load((const f32x4_t*)((const float*)row + c + 4));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = a[i];
-        x[4 + i] = b[i];
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = 0.0f;
-      if ((uint32_t)(c + i) < (uint32_t)n)
-        x[i] = BF ? bf16_lo(((const uint16_t*)row)[c + i]) : ((const float*)row)[c + i];
+      return __uint_as_float(w[i >> 2][i & 3]);
     }
   }
-}
-template <bool BF>
-__device__ __forceinline__ void store8(void* row, int c, int n, bool full, const float (&x)[8]) {
-  if (full) {
-    if constexpr (BF) {
-      const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                         pack_bf16x2(x[6], x[7])};
-      __builtin_nontemporal_store(w, (u32x4_t*)((uint16_t*)row + c));
-    } else {
-      __builtin_nontemporal_store(f32x4_t{x[0], x[1], x[2], x[3]}, (f32x4_t*)((float*)row + c));
-      __builtin_nontemporal_store(f32x4_t{x[4], x[5], x[6], x[7]}, (f32x4_t*)((float*)row + c + 4));
+};
+
+// The first n of them (n < 8 at the row's end; the others are zero).
+template <bool BF, bool STREAM>
+__device__ __forceinline__ Raw8<BF> load8(const void* at, int n) {
+  Raw8<BF> r;
+#pragma unroll
+  for (int h = 0; h < (BF ? 1 : 2); ++h) r.w[h] = u32x4_t{0u, 0u, 0u, 0u};
+  if (n >= 8) {
+#pragma unroll
+    for (int h = 0; h < (BF ? 1 : 2); ++h) {
+      const u32x4_any_t* const p = (const u32x4_any_t*)at + h;
+      r.w[h] = STREAM ? __builtin_nontemporal_load(p) : *p;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if ((uint32_t)(c + i) < (uint32_t)n) {
-        if constexpr (BF) ((uint16_t*)row)[c + i] = (uint16_t)(pack_bf16x2(x[i], 0.0f) & 0xFFFFu);
-        else ((float*)row)[c + i] = x[i];
+      if (i < n) {
+        if constexpr (BF) r.w[0][i >> 1] |= (uint32_t)((const uint16_t*)at)[i] << (16 * (i & 1));
+        else r.w[i >> 2][i & 3] = ((const uint32_t*)at)[i];
       }
+  }
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ void store8(void* at, int n, const float (&x)[8]) {
+  u32x4_t w[2];
+  if constexpr (BF) {
+    w[0] = u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = u32x4_t{__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), __float_as_uint(x[4 * h + 2]),
+                     __float_as_uint(x[4 * h + 3])};
+  }
+  if (n >= 8) {
+#pragma unroll
+    for (int h = 0; h < (BF ? 1 : 2); ++h) __builtin_nontemporal_store(w[h], (u32x4_any_t*)at + h);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (BF) ((uint16_t*)at)[i] = (uint16_t)(w[0][i >> 1] >> (16 * (i & 1)));
+        else ((uint32_t*)at)[i] = w[i >> 2][i & 3];
+      }
+  }
+}
+
+// Biases of columns i .. i + 7 of the bias tensor (the first n exist).
+__device__ __forceinline__ void bias8(const RuleSet& r, int64_t i, int n, float (&x)[8]) {
+  if (r.bias_bf16) {
+    const Raw8<true> w = load8<true, false>((const uint16_t*)r.bias + i, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = w[e];
+  } else {
+    const Raw8<false> w = load8<false, false>((const float*)r.bias + i, n);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = w[e];
   }
 }
 
 }  // namespace
 
-// T columns of one request a workgroup, all its positions.  Rows of an odd
-// vocabulary start anywhere, so each row's vectors of 8 are laid from the
-// 16-byte boundary at or before the tile's first column; a vector that
-// reaches past the tile is moved by elements.  `whole` is false where the
-// streamed tensors differ in alignment: then every vector is.
-template <bool BF, bool BWD>
+// A workgroup: T columns of one request, its positions in groups of R, a
+// thread 8 columns of a group's rows (and U such columns) at a time, so that
+// R * U vectors are in flight while the bias and the table's bits of a column
+// are read once for its R rows.
+//
+// The block's own tokens differ from row to row.  Before a group, those up to
+// its first row join the table for good; the few within it only set their
+// bit in `any`, and a column whose bit is set looks them up one by one.
+template <bool BF, bool BWD, int R, int U>
 __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p, int T, int tiles, bool track,
-                                                                   bool keep_counts, bool whole) {
+                                                                   bool keep_counts) {
   extern __shared__ uint32_t rule_lds[];
-  uint32_t* const seen = rule_lds;                                    // T / 32 words
-  uint32_t* const counts = keep_counts ? rule_lds + T / 32 : nullptr;  // T words
+  uint32_t* const any = rule_lds;                                        // T / 32 words
+  uint32_t* const seen = rule_lds + T / 32;                              // T / 32 words
+  uint32_t* const counts = keep_counts ? rule_lds + T / 16 : nullptr;    // T words
+  __shared__ uint32_t blk[R];  // columns of the group's tokens k0 + 1 .. k0 + R - 1 relative to the tile, at 1 .. R - 1
   const int64_t b = blockIdx.x / (unsigned)tiles;
   const int64_t t0 = (int64_t)(blockIdx.x % (unsigned)tiles) * T;
   const int tn = (int)(p.V - t0 < T ? p.V - t0 : T);
   const int tid = threadIdx.x;
   constexpr int ES = BF ? 2 : 4;
   const Penalty pen = penalty_of(p.r, b);
+  const int64_t* const ids = track && p.token_ids ? p.token_ids + b * p.M : nullptr;
   if (track) {
-    const int words = keep_counts ? T / 32 + T : T / 32;
+    const int words = keep_counts ? T / 16 + T : T / 16;
     for (int i = tid; i < words; i += kRuleThreads) rule_lds[i] = 0u;
     __syncthreads();
     count_history(p.r, b, t0, tn, seen, counts);
     __syncthreads();
+    for (int i = tid; i < T / 32; i += kRuleThreads) any[i] = seen[i];
+    __syncthreads();
   }
-  const int W = (int)((p.V + 31) / 32);
-  for (int64_t k = 0; k < p.M; ++k) {
-    if (track && k > 0 && p.token_ids) {
-      // the block's token before this position, if it is the tile's
-      const int64_t id = p.token_ids[b * p.M + k];
-      const uint64_t c = (uint64_t)id - (uint64_t)t0;
-      if (id >= 0 && c < (uint64_t)tn) {  // the same in every thread
-        __syncthreads();
-        if (tid == 0) {
-          seen[c >> 5] |= 1u << (c & 31);
-          if (counts) counts[c] += 1u;
+  for (int64_t k0 = 0; k0 < p.M; k0 += R) {
+    if (ids) {
+      if (k0 > 0) __syncthreads();
+      for (int j = tid; j < 2 * R - 1; j += kRuleThreads) {  // tokens k0 - R + 1 .. k0 + R - 1
+        const int64_t at = k0 - R + 1 + j;
+        const int64_t id = at >= 1 && at < p.M ? ids[at] : -1;
+        const uint64_t c = (uint64_t)id - (uint64_t)t0;
+        const bool mine = id >= 0 && c < (uint64_t)tn;
+        if (at > k0) blk[at - k0] = mine ? (uint32_t)c : 0xFFFFFFFFu;
+        if (!mine) continue;
+        atomicOr(&any[c >> 5], 1u << (c & 31));
+        if (at <= k0) {
+          atomicOr(&seen[c >> 5], 1u << (c & 31));
+          if (counts) atomicAdd(&counts[c], 1u);
         }
-        __syncthreads();
       }
+      __syncthreads();
     }
-    const int64_t row = (b * p.M + k) * p.V + t0;
-    const char* const in = (const char*)(BWD ? p.grad : p.logits) + row * ES;
-    char* const out = (char*)p.out + row * ES;
-    const char* const lg = (const char*)p.logits + row * ES;
-    const int a = whole ? (int)(((uintptr_t)out % 16) / ES) : 0;
-    const uint32_t* const mask = p.r.mask ? p.r.mask + b * p.r.mask_stride_b + k * p.r.mask_stride_m : nullptr;
-    const int64_t bias0 = b * p.r.bias_stride + t0;
-    constexpr int U = 2;
-    for (int c0 = 8 * tid - a; c0 < tn; c0 += U * 8 * kRuleThreads) {
-      float x[U][8];
+    const int rows = (int)(p.M - k0 < R ? p.M - k0 : R);
+    const int64_t first = (b * p.M + k0) * p.V + t0;
+    const char* const in = (const char*)(BWD ? p.grad : p.logits) + first * ES;
+    const char* const lg = (const char*)p.logits + first * ES;
+    char* const out = (char*)p.out + first * ES;
+    const uint8_t* const mask =
+        p.r.mask ? (const uint8_t*)(p.r.mask + b * p.r.mask_stride_b + k0 * p.r.mask_stride_m) + t0 / 8 : nullptr;
+    for (int c0 = 8 * tid; c0 < tn; c0 += U * 8 * kRuleThreads) {
+      Raw8<BF> raw[U][R];
+      uint32_t m8[U][R];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * 8 * kRuleThreads;
-        if (c < tn) load8<BF>(in, c, tn, whole && c >= 0 && c + 8 <= tn, x[u]);
+#pragma unroll
+        for (int q = 0; q < R; ++q) {
+          m8[u][q] = 0xFFu;
+          if (c < tn && q < rows) {
+            raw[u][q] = load8<BF, true>(in + (q * p.V + c) * ES, tn - c);
+            if (mask) m8[u][q] = mask[4 * q * p.r.mask_stride_m + c / 8];
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * 8 * kRuleThreads;
         if (c >= tn) break;
-        const uint32_t s8 = track ? bits8(seen, T / 32, c) : 0u;
-        if (s8) {
+        float bias[8];
+        if constexpr (!BWD)
+          if (p.r.bias) bias8(p.r, b * p.r.bias_stride + t0 + c, tn - c, bias);
+        // what the penalties need where a bit is set, fetched before the rows
+        const uint32_t a8 = track ? ((const uint8_t*)any)[c / 8] : 0u;
+        uint32_t s8 = 0;
+        uint32_t n8[8];
+        Raw8<BF> slope[R];
+        if (a8) {
+          s8 = ((const uint8_t*)seen)[c / 8];
+          if constexpr (BWD) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (s8 >> i & 1u) {
-              if constexpr (BWD) {
-                const float l = BF ? bf16_lo(((const uint16_t*)lg)[c + i]) : ((const float*)lg)[c + i];
-                x[u][i] = l > 0.0f ? x[u][i] / pen.repetition : x[u][i] * pen.repetition;
-              } else {
-                x[u][i] = pen.apply(x[u][i], counts ? counts[c + i] : 0u);
-              }
-            }
-        }
-        if constexpr (!BWD) {
-          if (p.r.bias) {
+            for (int q = 0; q < R; ++q)
+              if (q < rows) slope[q] = load8<BF, false>(lg + (q * p.V + c) * ES, tn - c);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if ((uint32_t)(c + i) < (uint32_t)tn) x[u][i] += bias_at(p.r, bias0 + c + i);
+            for (int i = 0; i < 8; ++i) n8[i] = counts ? counts[c + i] : 0u;
           }
         }
-        if (mask) {
-          const uint32_t m8 = bits8(mask, W, (int)t0 + c);
+        uint32_t packed = 0;  // 4 bits a column: times it stands among the group's tokens so far
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[u][i] = (m8 >> i & 1u) ? x[u][i] : BWD ? 0.0f : -__builtin_inff();
+        for (int q = 0; q < R; ++q) {
+          if (q >= rows) break;
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = raw[u][q][i];
+          if (a8) {
+            if (q > 0 && ids) {
+              const uint32_t d = blk[q] - (uint32_t)c;
+              if (d < 8u) {
+                packed += 1u << (4 * d);
+                s8 |= 1u << d;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (s8 >> i & 1u) {
+                if constexpr (BWD) x[i] = slope[q][i] > 0.0f ? x[i] / pen.repetition : x[i] * pen.repetition;
+                else x[i] = pen.apply(x[i], n8[i] + (packed >> (4 * i) & 15u));
+              }
+          }
+          if constexpr (!BWD) {
+            if (p.r.bias) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[i] += bias[i];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = (m8[u][q] >> i & 1u) ? x[i] : BWD ? 0.0f : -__builtin_inff();
+          store8<BF>(out + (q * p.V + c) * ES, tn - c, x);
         }
-        store8<BF>(out, c, tn, whole && c >= 0 && c + 8 <= tn, x[u]);
       }
     }
   }
 }
 
-hipError_t launch_logit_rules(const RulesParams& p, bool logits_bf16, int num_cus, hipStream_t s) {
+namespace {
+template <bool BF, bool BWD>
+hipError_t rules_go(const RulesParams& p, int num_cus, hipStream_t s) {
   const bool track = rules_penalise(p.r) && (p.r.history != nullptr || (p.token_ids != nullptr && p.M > 1));
-  const bool bwd = p.grad != nullptr;
-  const bool keep_counts = track && !bwd && (p.r.frequency != nullptr || p.r.presence != nullptr);
+  const bool keep_counts = track && !BWD && (p.r.frequency != nullptr || p.r.presence != nullptr);
   int T = 8192;
   while (T > 2048 && p.B * ((p.V + T - 1) / T) < 4 * (int64_t)num_cus) T /= 2;
   const int64_t tiles = (p.V + T - 1) / T;
   if (p.B * tiles > 0x7FFFFFFF) return hipErrorNotSupported;
-  const size_t lds = track ? (size_t)(T / 32 + (keep_counts ? T : 0)) * 4 : 0;
-  const bool whole = ((uintptr_t)(bwd ? p.grad : p.logits) - (uintptr_t)p.out) % 16 == 0;
+  const size_t lds = track ? (size_t)(T / 16 + (keep_counts ? T : 0)) * 4 : 0;
   const dim3 grid((unsigned)(p.B * tiles)), block(kRuleThreads);
-#define DSPARK_RULES(BF, BWD) \
-  hipLaunchKernelGGL((logit_rules_kernel<BF, BWD>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts, whole)
-  if (logits_bf16) {
-    if (bwd) DSPARK_RULES(true, true);
-    else DSPARK_RULES(true, false);
-  } else {
-    if (bwd) DSPARK_RULES(false, true);
-    else DSPARK_RULES(false, false);
-  }
-#undef DSPARK_RULES
+  if (p.M == 1)
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 1, 4>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
+  else if (p.M <= 4)
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 4, 2>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
+  else
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 8, 1>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_logit_rules(const RulesParams& p, bool logits_bf16, int num_cus, hipStream_t s) {
+  const bool bwd = p.grad != nullptr;
+  if (logits_bf16) return bwd ? rules_go<true, true>(p, num_cus, s) : rules_go<true, false>(p, num_cus, s);
+  return bwd ? rules_go<false, true>(p, num_cus, s) : rules_go<false, false>(p, num_cus, s);
 }
 
 // ---------------------------------------------------------------- left to right
@@ -296,53 +355,57 @@ int64_t select_parts(int64_t V) { return (V + kSelectCols - 1) / kSelectCols; }
 // One row's slice: the rules in place, then the slice's best key (the scores
 // of sample_block_tokens on the processed values).
 template <bool BF>
-__global__ __launch_bounds__(kRuleThreads) void rule_select_kernel(SelectParams p, int parts, bool whole) {
+__global__ __launch_bounds__(kRuleThreads) void rule_select_kernel(SelectParams p, int parts) {
   __shared__ uint64_t lds_key[kRuleThreads / 64];
   const int64_t b = blockIdx.x / (unsigned)parts;
   const int part = (int)(blockIdx.x % (unsigned)parts);
   const int tid = threadIdx.x;
   const int V = (int)p.V;
   const int end = V - part * kSelectCols < kSelectCols ? V : (part + 1) * kSelectCols;
-  const int W = (V + 31) / 32;
   const Penalty pen = penalty_of(p.r, b);
-  char* const row = (char*)p.logits + (b * p.M + p.k) * p.V * (BF ? 2 : 4);
-  const uint32_t* const seen = p.seen ? p.seen + b * W : nullptr;
+  constexpr int ES = BF ? 2 : 4;
+  char* const row = (char*)p.logits + (b * p.M + p.k) * p.V * ES;
+  const uint8_t* const seen = p.seen ? (const uint8_t*)(p.seen + b * ((V + 31) / 32)) : nullptr;
   const uint32_t* const counts = p.seen ? p.counts + b * p.V : nullptr;
-  const uint32_t* const mask = p.r.mask ? p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m : nullptr;
-  const int64_t bias0 = b * p.r.bias_stride;
+  const uint8_t* const mask =
+      p.r.mask ? (const uint8_t*)(p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m) : nullptr;
   uint64_t best = 0;
   constexpr int U = kSelectCols / (8 * kRuleThreads);
-  float x[U][8];
+  Raw8<BF> raw[U];
+  uint32_t s8[U], m8[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = part * kSelectCols + 8 * (tid + u * kRuleThreads);
-    if (c < end) load8<BF>(row, c, V, whole && c + 8 <= V, x[u]);
+    if (c < end) {
+      raw[u] = load8<BF, true>(row + (int64_t)c * ES, V - c);
+      s8[u] = seen ? seen[c / 8] : 0u;
+      m8[u] = mask ? mask[c / 8] : 0xFFu;
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int c = part * kSelectCols + 8 * (tid + u * kRuleThreads);
     if (c >= end) break;
-    const uint32_t s8 = seen ? bits8(seen, W, c) : 0u;
-    if (s8) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = raw[u][i];
+    if (s8[u]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if ((s8 >> i & 1u) && c + i < V) x[u][i] = pen.apply(x[u][i], counts[c + i]);
+        if (s8[u] >> i & 1u) x[i] = pen.apply(x[i], counts[c + i]);
     }
     if (p.r.bias) {
+      float bias[8];
+      bias8(p.r, b * p.r.bias_stride + c, V - c, bias);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < V) x[u][i] += bias_at(p.r, bias0 + c + i);
+      for (int i = 0; i < 8; ++i) x[i] += bias[i];
     }
-    if (mask) {
-      const uint32_t m8 = bits8(mask, W, c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = (m8 >> i & 1u) ? x[u][i] : -__builtin_inff();
+    for (int i = 0; i < 8; ++i) {
+      x[i] = (m8[u] >> i & 1u) ? x[i] : -__builtin_inff();
+      if constexpr (BF) x[i] = bf16_rne(x[i]);
     }
-    if constexpr (BF) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = bf16_rne(x[u][i]);
-    }
-    store8<BF>(row, c, V, whole && c + 8 <= V, x[u]);
+    store8<BF>(row + (int64_t)c * ES, V - c, x);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -357,7 +420,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_select_kernel(SelectParams 
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int v = c + 4 * j + i;
-        const float sc = p.greedy ? x[u][4 * j + i] : __builtin_fmaf(x[u][4 * j + i], p.kappa, g[i]);
+        const float sc = p.greedy ? x[4 * j + i] : __builtin_fmaf(x[4 * j + i], p.kappa, g[i]);
         if (v < V) best = max_u64(best, argmax_key(sc, (uint32_t)v));
       }
     }
@@ -375,12 +438,11 @@ __global__ __launch_bounds__(kRuleThreads) void rule_select_kernel(SelectParams 
 hipError_t launch_rule_select(const SelectParams& p, bool logits_bf16, hipStream_t s) {
   const int64_t parts = select_parts(p.V);
   if (p.B * parts > 0x7FFFFFFF) return hipErrorNotSupported;
-  const bool whole = (uintptr_t)p.logits % 16 == 0 && p.V % 8 == 0;
   const dim3 grid((unsigned)(p.B * parts)), block(kRuleThreads);
   if (logits_bf16)
-    hipLaunchKernelGGL(rule_select_kernel<true>, grid, block, 0, s, p, (int)parts, whole);
+    hipLaunchKernelGGL(rule_select_kernel<true>, grid, block, 0, s, p, (int)parts);
   else
-    hipLaunchKernelGGL(rule_select_kernel<false>, grid, block, 0, s, p, (int)parts, whole);
+    hipLaunchKernelGGL(rule_select_kernel<false>, grid, block, 0, s, p, (int)parts);
   return hipGetLastError();
 }
 
