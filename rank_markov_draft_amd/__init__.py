@@ -55,8 +55,18 @@ def _dtype_tag(t: torch.Tensor) -> int:
     raise TypeError(f"unsupported dtype {t.dtype}; the head takes float32 or bfloat16")
 
 
-def _stream_handle(device: torch.device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream_handle(device: torch.device) -> int:
+    # the hipStream_t of torch's current stream, without the Stream object
+    # that torch.cuda.current_stream would build (2 us of a small call's 14)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
+
+
+def _call(device: torch.device, fn, *args) -> int:
+    """fn(*args, stream) with ``device`` the current one."""
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, _stream_handle(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream_handle(device))
 
 
 def _ptr(t):
@@ -445,9 +455,8 @@ def quantize_rows(x: torch.Tensor, *, out: torch.Tensor | None = None, scale_out
     elif scale_out.shape != x.shape[:-1] or scale_out.dtype != torch.float32 or not scale_out.is_contiguous():
         raise ValueError(f"scale_out must be a contiguous float32 tensor of shape {tuple(x.shape[:-1])}")
     xc = x.contiguous()
-    with torch.cuda.device(x.device):
-        st = _lib.load().dspark_markov_quantize_rows(_ptr(xc), tag, scale_out.numel(), x.shape[-1], _ptr(out),
-                                                     _ptr(scale_out), _stream_handle(x.device))
+    st = _call(x.device, _lib.load().dspark_markov_quantize_rows, _ptr(xc), tag, scale_out.numel(), x.shape[-1],
+               _ptr(out), _ptr(scale_out))
     _lib.check(st, "quantize_rows")
     return out, scale_out
 
@@ -483,46 +492,52 @@ def lm_head_logits_int8(hidden_states: torch.Tensor, head_q: torch.Tensor, head_
         return out
     rows = out.numel() // V
     h, hq, hs = hidden_states.contiguous(), head_q.contiguous(), head_scale.contiguous()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            nbytes = int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(rows, 1, d))
-            buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
-        else:
-            nbytes, buffer = workspace.nbytes, workspace.buffer
-        st = _lib.load().dspark_markov_lm_head_int8(_ptr(h), tag, d, _ptr(hq), _ptr(hs), rows, 1, V, _ptr(out), out_tag,
-                                                    _ptr(buffer), nbytes, _stream_handle(dev))
+    if workspace is None:
+        nbytes = int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(rows, 1, d))
+        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+    else:
+        nbytes, buffer = workspace.nbytes, workspace.buffer
+    st = _call(dev, _lib.load().dspark_markov_lm_head_int8, _ptr(h), tag, d, _ptr(hq), _ptr(hs), rows, 1, V, _ptr(out),
+               out_tag, _ptr(buffer), nbytes)
     _lib.check(st, "lm_head_logits_int8")
     return out
 
 
 def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, frequency_penalty, presence_penalty,
                  logit_bias, token_mask):
-    """The rules as dspark_logit_rules_t, and the tensors it points into."""
-    keep = []
+    """The rules as dspark_logit_rules_t, and the tensors made for it that must live until the call."""
+    r, keep = _lib.LogitRules(), []
+
+    def here(t, name):
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the logits on {dev}")
 
     def per_request(t, name, dtype):
         if t is None:
             return None
-        if tuple(t.shape) != (B,):
+        if t.shape != (B,):
             raise ValueError(f"{name} must be [{B}], got {tuple(t.shape)}")
         if t.is_floating_point() != dtype.is_floating_point:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        keep.append(t.to(dtype).contiguous())
-        return _ptr(keep[-1])
+        here(t, name)
+        if t.dtype != dtype or not t.is_contiguous():
+            t = t.to(dtype).contiguous()
+            keep.append(t)
+        return t.data_ptr()
 
-    r = _lib.LogitRules()
-    if history is None and (lengths is not None or prompt_lengths is not None):
-        raise ValueError("lengths and prompt_lengths need a history")
     if history is not None:
         if history.dim() != 2 or history.shape[0] != B or history.is_floating_point():
             raise ValueError(f"history must be integer ids [{B}, L], got {history.dtype} {tuple(history.shape)}")
-        h = history.to(torch.int64)
-        if h.shape[1] > 1 and h.stride(1) != 1 or B > 1 and h.stride(0) < h.shape[1]:
-            h = h.contiguous()
-        keep.append(h)
-        r.history, r.history_len, r.history_stride = _ptr(h), h.shape[1], h.stride(0) if B > 1 else h.shape[1]
+        here(history, "history")
+        L = history.shape[1]
+        if history.dtype != torch.int64 or L > 1 and history.stride(1) != 1 or B > 1 and history.stride(0) < L:
+            history = history.to(torch.int64).contiguous()
+            keep.append(history)
+        r.history, r.history_len, r.history_stride = history.data_ptr(), L, history.stride(0) if B > 1 else L
         r.lengths = per_request(lengths, "lengths", torch.int64)
         r.prompt_lengths = per_request(prompt_lengths, "prompt_lengths", torch.int64)
+    elif lengths is not None or prompt_lengths is not None:
+        raise ValueError("lengths and prompt_lengths need a history")
     r.repetition_penalty = per_request(repetition_penalty, "repetition_penalty", torch.float32)
     r.frequency_penalty = per_request(frequency_penalty, "frequency_penalty", torch.float32)
     r.presence_penalty = per_request(presence_penalty, "presence_penalty", torch.float32)
@@ -530,9 +545,12 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
         if tuple(logit_bias.shape) not in ((V,), (1, V), (B, V)):
             raise ValueError(f"logit_bias must be [{V}] or [{B}, {V}], got {tuple(logit_bias.shape)}")
         r.bias_dtype = _dtype_tag(logit_bias)
-        bias = logit_bias.contiguous()
-        keep.append(bias)
-        r.logit_bias, r.bias_stride = _ptr(bias), V if bias.dim() == 2 and bias.shape[0] > 1 else 0
+        here(logit_bias, "logit_bias")
+        if not logit_bias.is_contiguous():
+            logit_bias = logit_bias.contiguous()
+            keep.append(logit_bias)
+        r.logit_bias = logit_bias.data_ptr()
+        r.bias_stride = V if logit_bias.dim() == 2 and logit_bias.shape[0] > 1 else 0
     if token_mask is not None:
         W = (V + 31) // 32
         if token_mask.dtype != torch.int32:
@@ -541,16 +559,13 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
         if mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] not in (1, M) or mask.shape[2] != W:
             raise ValueError(f"token_mask must be [{B}, {W}] or [{B}, {M}, {W}] (or 1 in place of either size), "
                              f"got {tuple(token_mask.shape)}")
-        if W > 1 and mask.stride(2) != 1 or any(s < 0 for s in mask.stride()):
+        here(token_mask, "token_mask")
+        if W > 1 and mask.stride(2) != 1:
             mask = mask.contiguous()
-        keep.append(mask)
-        r.token_mask = _ptr(mask)
+            keep.append(mask)
+        r.token_mask = mask.data_ptr()
         r.mask_stride_b = mask.stride(0) if mask.shape[0] > 1 else 0
         r.mask_stride_m = mask.stride(1) if mask.shape[1] > 1 else 0
-    for name, t in (("history", history), ("lengths", lengths), ("prompt_lengths", prompt_lengths),
-                    ("repetition_penalty", repetition_penalty), ("frequency_penalty", frequency_penalty),
-                    ("presence_penalty", presence_penalty), ("logit_bias", logit_bias), ("token_mask", token_mask)):
-        _check_device(dev, None, **{name: t})
     return r, keep
 
 
@@ -597,9 +612,7 @@ def process_block_logits(logits: torch.Tensor, *, token_ids: torch.Tensor | None
     elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped and typed like logits")
     ids = None if token_ids is None else token_ids.to(torch.int64).contiguous()
-    with torch.cuda.device(dev):
-        st = _lib.load().dspark_markov_process_block(_ptr(x), tag, _ptr(ids), rules, B, M, V, _ptr(out),
-                                                     _stream_handle(dev))
+    st = _call(dev, _lib.load().dspark_markov_process_block, _ptr(x), tag, _ptr(ids), rules, B, M, V, _ptr(out))
     _lib.check(st, "process_block_logits")
     return out
 
@@ -631,9 +644,8 @@ def process_block_logits_backward(grad_processed: torch.Tensor, logits: torch.Te
     elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped and typed like logits")
     ids = None if token_ids is None else token_ids.to(torch.int64).contiguous()
-    with torch.cuda.device(dev):
-        st = _lib.load().dspark_markov_process_block_backward(_ptr(g), _ptr(x), tag, _ptr(ids), rules, B, M, V, _ptr(out),
-                                                              _stream_handle(dev))
+    st = _call(dev, _lib.load().dspark_markov_process_block_backward, _ptr(g), _ptr(x), tag, _ptr(ids), rules, B, M, V,
+               _ptr(out))
     _lib.check(st, "process_block_logits_backward")
     return out
 
@@ -683,12 +695,11 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
     first = first_prev_token_ids.to(torch.int64).contiguous()
     w1c, w2c = w1.contiguous(), w2.contiguous()
     r = w1.shape[1]
-    with torch.cuda.device(dev):
-        if workspace is None:
+    if workspace is None:
+        with torch.cuda.device(dev):
             workspace = Workspace(B, M, V, r, sample=True, device=dev, processed=True)
-        st = _lib.load().dspark_markov_sample_block_processed(
-            _ptr(base), tag, _ptr(first), _ptr(w1c), _ptr(w2c), wtag, rules, B, M, V, r, T, int(seed) & (2**64 - 1),
-            int(position_offset), int(batch_offset), _ptr(tokens_out), _ptr(logits_out), workspace.ptr, workspace.nbytes,
-            _stream_handle(dev))
+    st = _call(dev, _lib.load().dspark_markov_sample_block_processed, _ptr(base), tag, _ptr(first), _ptr(w1c), _ptr(w2c),
+               wtag, rules, B, M, V, r, T, int(seed) & (2**64 - 1), int(position_offset), int(batch_offset),
+               _ptr(tokens_out), _ptr(logits_out), workspace.ptr, workspace.nbytes)
     _lib.check(st, "sample_block_tokens_processed")
     return tokens_out, logits_out

@@ -176,6 +176,27 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
   constexpr int ES = BF ? 2 : 4;
   const Penalty pen = penalty_of(p.r, b);
   const int64_t* const ids = track && p.token_ids ? p.token_ids + b * p.M : nullptr;
+  // the values and mask bits of a group's columns c0 (+ U - 1 strides)
+  Raw8<BF> raw[U][R];
+  uint32_t m8[U][R];
+  auto fetch = [&](int64_t k0, int c0) __attribute__((always_inline)) {
+    const char* const in = (const char*)(BWD ? p.grad : p.logits) + ((b * p.M + k0) * p.V + t0) * ES;
+    const uint8_t* const mask =
+        p.r.mask ? (const uint8_t*)(p.r.mask + b * p.r.mask_stride_b + k0 * p.r.mask_stride_m) + t0 / 8 : nullptr;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * 8 * kRuleThreads;
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        m8[u][q] = 0xFFu;
+        if (c < tn && k0 + q < p.M) {
+          raw[u][q] = load8<BF, true>(in + (q * p.V + c) * ES, tn - c);
+          if (mask) m8[u][q] = mask[4 * q * p.r.mask_stride_m + c / 8];
+        }
+      }
+    }
+  };
+  fetch(0, 8 * tid);  // in flight while the history is walked
   if (track) {
     const int words = keep_counts ? T / 16 + T : T / 16;
     for (int i = tid; i < words; i += kRuleThreads) rule_lds[i] = 0u;
@@ -205,26 +226,10 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
     }
     const int rows = (int)(p.M - k0 < R ? p.M - k0 : R);
     const int64_t first = (b * p.M + k0) * p.V + t0;
-    const char* const in = (const char*)(BWD ? p.grad : p.logits) + first * ES;
     const char* const lg = (const char*)p.logits + first * ES;
     char* const out = (char*)p.out + first * ES;
-    const uint8_t* const mask =
-        p.r.mask ? (const uint8_t*)(p.r.mask + b * p.r.mask_stride_b + k0 * p.r.mask_stride_m) + t0 / 8 : nullptr;
     for (int c0 = 8 * tid; c0 < tn; c0 += U * 8 * kRuleThreads) {
-      Raw8<BF> raw[U][R];
-      uint32_t m8[U][R];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * 8 * kRuleThreads;
-#pragma unroll
-        for (int q = 0; q < R; ++q) {
-          m8[u][q] = 0xFFu;
-          if (c < tn && q < rows) {
-            raw[u][q] = load8<BF, true>(in + (q * p.V + c) * ES, tn - c);
-            if (mask) m8[u][q] = mask[4 * q * p.r.mask_stride_m + c / 8];
-          }
-        }
-      }
+      if (k0 > 0 || c0 > 8 * tid) fetch(k0, c0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * 8 * kRuleThreads;
@@ -290,7 +295,8 @@ template <bool BF, bool BWD>
 hipError_t rules_go(const RulesParams& p, int num_cus, hipStream_t s) {
   const bool track = rules_penalise(p.r) && (p.r.history != nullptr || (p.token_ids != nullptr && p.M > 1));
   const bool keep_counts = track && !BWD && (p.r.frequency != nullptr || p.r.presence != nullptr);
-  int T = 8192;
+  int T = 2048;
+  while (T < 8192 && (double)T * p.M * (BF ? 2 : 4) < 0.4 * (8.0 * (track ? p.r.history_len : 0) + 36864)) T *= 2;
   while (T > 2048 && p.B * ((p.V + T - 1) / T) < 4 * (int64_t)num_cus) T /= 2;
   const int64_t tiles = (p.V + T - 1) / T;
   if (p.B * tiles > 0x7FFFFFFF) return hipErrorNotSupported;
