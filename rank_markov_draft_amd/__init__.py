@@ -506,11 +506,7 @@ def lm_head_logits_int8(hidden_states: torch.Tensor, head_q: torch.Tensor, head_
 def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_penalty, frequency_penalty, presence_penalty,
                  logit_bias, token_mask):
     """The rules as dspark_logit_rules_t, and the tensors made for it that must live until the call."""
-    r, keep = _lib.LogitRules(), []
-
-    def here(t, name):
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the logits on {dev}")
+    r, keep, given = _lib.LogitRules(), [], {}
 
     def per_request(t, name, dtype):
         if t is None:
@@ -519,7 +515,7 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
             raise ValueError(f"{name} must be [{B}], got {tuple(t.shape)}")
         if t.is_floating_point() != dtype.is_floating_point:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        here(t, name)
+        given[name] = t
         if t.dtype != dtype or not t.is_contiguous():
             t = t.to(dtype).contiguous()
             keep.append(t)
@@ -528,7 +524,7 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
     if history is not None:
         if history.dim() != 2 or history.shape[0] != B or history.is_floating_point():
             raise ValueError(f"history must be integer ids [{B}, L], got {history.dtype} {tuple(history.shape)}")
-        here(history, "history")
+        given["history"] = history
         L = history.shape[1]
         if history.dtype != torch.int64 or L > 1 and history.stride(1) != 1 or B > 1 and history.stride(0) < L:
             history = history.to(torch.int64).contiguous()
@@ -545,7 +541,7 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
         if tuple(logit_bias.shape) not in ((V,), (1, V), (B, V)):
             raise ValueError(f"logit_bias must be [{V}] or [{B}, {V}], got {tuple(logit_bias.shape)}")
         r.bias_dtype = _dtype_tag(logit_bias)
-        here(logit_bias, "logit_bias")
+        given["logit_bias"] = logit_bias
         if not logit_bias.is_contiguous():
             logit_bias = logit_bias.contiguous()
             keep.append(logit_bias)
@@ -559,13 +555,16 @@ def _logit_rules(B, M, V, dev, history, lengths, prompt_lengths, repetition_pena
         if mask.dim() != 3 or mask.shape[0] not in (1, B) or mask.shape[1] not in (1, M) or mask.shape[2] != W:
             raise ValueError(f"token_mask must be [{B}, {W}] or [{B}, {M}, {W}] (or 1 in place of either size), "
                              f"got {tuple(token_mask.shape)}")
-        here(token_mask, "token_mask")
+        given["token_mask"] = token_mask
         if W > 1 and mask.stride(2) != 1:
             mask = mask.contiguous()
             keep.append(mask)
         r.token_mask = mask.data_ptr()
         r.mask_stride_b = mask.stride(0) if mask.shape[0] > 1 else 0
         r.mask_stride_m = mask.stride(1) if mask.shape[1] > 1 else 0
+    for name, t in given.items():
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the logits on {dev}")
     return r, keep
 
 
