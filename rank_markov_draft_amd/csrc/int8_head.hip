@@ -140,34 +140,41 @@ hipError_t launch_quantize_rows(const QuantizeParams& p, bool bf16, hipStream_t 
 // ---------------------------------------------------------------- product
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // rows of the output start at any element
 
 // A workgroup of WM x WN waves owns tiles of 32 MI WM rows x 32 NJ WN
 // vocabulary columns and walks them in a persistent loop; a wave holds MI x
 // NJ blocks of 32 x 32 sums.  The inner dimension is cut into chunks of 128
 // bytes; a chunk's rows of q and of the head are loaded straight into LDS
-// (16 bytes a lane, no registers), STAGES - 1 chunks ahead of their use.  A
-// row's eight 16-byte pieces sit at positions piece ^ (row % 8), so that the
-// fragment reads of eight consecutive rows fall on different banks.  The chunk
-// stream runs on across tiles.
+// (16 bytes a lane, no registers), up to STAGES chunks at a time.  A row's
+// eight 16-byte pieces sit at positions piece ^ (row % 8), so that the
+// fragment reads of eight consecutive rows fall on different banks.  The
+// chunk stream runs on across tiles.
 //
-// v_mfma_i32_32x32x32_i8: rows of q on M, vocabulary columns on N, so that a
-// store instruction writes 32 consecutive columns of two rows, whatever V's
-// parity.
+// v_mfma_i32_32x32x32_i8: rows of q on M, vocabulary columns on N.
+//
+// AHEAD (tiles bound by the matrix cores): the fragments of a product are
+// read while the product before it runs, and the hand-over from chunk to
+// chunk (wait, barrier, first reads) runs behind the chunk's last products.
+// Otherwise (tiles bound by the head's stream) all of a chunk's fragments are
+// read at once, so that their latency is paid once a chunk.
 //
 // DIRECT needs rows of the head in whole 16-byte pieces; otherwise its pieces
 // go through registers by unaligned loads.
-template <int MI, int NJ, int WM, int WN, int STAGES, bool DIRECT, bool OBF>
+template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, bool DIRECT, bool OBF>
 __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams p, int row_tiles, int tiles) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
   constexpr int BM = 32 * MI * WM, BN = 32 * NJ * WN, BK = (int)kInt8K;
   constexpr int STAGE = (BM + BN) * BK;
-  constexpr int IA = BM / 8, IB = DIRECT ? BN / 8 : 0;   // load instructions of a chunk, 8 rows each
-  constexpr int PER = (IA + IB + NW - 1) / NW;           // per wave
+  // load instructions of a chunk, 8 rows each, per wave
+  constexpr int PA = BM / 8 / NW, PB = DIRECT ? BN / 8 / NW : 0, PER = PA + PB;
   constexpr int REGS = DIRECT ? 1 : BN * 8 / THREADS;    // pieces of the head a thread moves itself
-  static_assert(DIRECT || STAGES == 2, "register pieces are one chunk ahead");
-  static_assert((STAGES - 2) * PER < 64, "wait count");
-  constexpr int JUNK = (IA + IB) % NW ? 1024 : 0;        // where loads without a place go
-  __shared__ __attribute__((aligned(16))) unsigned char lds[STAGES * STAGE + JUNK];
+  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "whole load instructions per wave");
+  static_assert(DIRECT || (STAGES == 2 && !AHEAD), "register pieces are one chunk ahead");
+  static_assert((STAGES - 1) * PER < 64, "wait count");
+  // a wave's part of the output on its way to memory: ER rows x 32 NJ columns
+  constexpr int OS = OBF ? 2 : 4, ER = OBF ? 16 : 8, EROW = 32 * NJ * OS, EBYTES = ER * EROW;
+  __shared__ __attribute__((aligned(16))) unsigned char lds[STAGES * STAGE + NW * EBYTES];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -183,7 +190,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
   const int my = first < tiles ? (tiles - 1 - first) / G + 1 : 0;
   const int total = my * C;
 
-  // the load stream
+  // ---- the load stream
   int lt = 0, lc = 0;  // tile (of mine) and chunk
   BufferWords ba, bb;
   int64_t lv0 = 0;
@@ -195,25 +202,23 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
     if constexpr (DIRECT) bb = buffer_words(p.wq + v0 * p.d, (uint32_t)(nv * p.d));
     lv0 = v0;
   };
-  const uint32_t q16 = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));  // the piece this lane's position holds
+  // load instruction j of this wave fills rows 8 (wave + j NW) .. + 7, lane l
+  // the position l % 8 of row l / 8 (which holds piece l % 8 ^ row % 8)
+  const uint32_t row8 = 8u * (uint32_t)wave + (uint32_t)(lane >> 3);
+  const uint32_t q16 = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+  const uint32_t offa = row8 * (uint32_t)p.ldx + q16, offb = row8 * (uint32_t)p.d + q16;
   u32x4_t held[REGS];
   auto issue = [&](int g) __attribute__((always_inline)) {  // chunk g of the stream, in order
     const bool live = g < total;
-    const uint32_t k0 = (uint32_t)lc * BK + q16;
-    const uint32_t stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]);
+    const uint32_t k0 = (uint32_t)lc * BK;
+    const uint32_t stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]) + 1024u * (uint32_t)wave;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int i = wave + j * NW;  // uniform over the wave
-      if (i < IA) {
-        const uint32_t off = live ? (uint32_t)(8 * i + (lane >> 3)) * (uint32_t)p.ldx + k0 : kBufferOob;
-        load_lds16(ba, off, stage + (uint32_t)i * 1024u);
-      } else if (i < IA + IB) {
-        const uint32_t off = live ? (uint32_t)(8 * (i - IA) + (lane >> 3)) * (uint32_t)p.d + k0 : kBufferOob;
-        load_lds16(bb, off, stage + (uint32_t)i * 1024u);
-      } else {
-        load_lds16(ba, kBufferOob, lds_address(&lds[STAGES * STAGE]));
-      }
-    }
+    for (int j = 0; j < PA; ++j)
+      load_lds16(ba, live ? offa + (uint32_t)(8 * NW * j) * (uint32_t)p.ldx + k0 : kBufferOob, stage + 1024u * NW * j);
+#pragma unroll
+    for (int j = 0; j < PB; ++j)
+      load_lds16(bb, live ? offb + (uint32_t)(8 * NW * j) * (uint32_t)p.d + k0 : kBufferOob,
+                 stage + BM * BK + 1024u * NW * j);
     if constexpr (!DIRECT) {
 #pragma unroll
       for (int j = 0; j < REGS; ++j) {
@@ -248,15 +253,55 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
     }
   };
 
+  // ---- the products: fragments of the wave's MI x NJ blocks for one matrix
+  // instruction each
+  constexpr int S = BK / 32;
+  struct Frags {
+    i32x4_t a[MI], b[NJ];
+  };
+  auto read = [&](int g, int s, Frags& f) __attribute__((always_inline)) {  // step s of chunk g
+    const unsigned char* const st = &lds[(g % STAGES) * STAGE + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7))];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) f.a[i] = *(const i32x4_t*)(st + (32 * (MI * wm + i) + (lane & 31)) * BK);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) f.b[j] = *(const i32x4_t*)(st + (BM + 32 * (NJ * wn + j) + (lane & 31)) * BK);
+  };
+  i32x16_t acc[MI][NJ];
+  auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+
   if (my == 0) return;
   bind(0);
+  issue(0);
+  put(0);
 #pragma unroll
-  for (int g = 0; g < STAGES - 1; ++g) issue(g);
-  if constexpr (!DIRECT) put(0);
-
-  i32x16_t acc[MI][NJ];
-  int g = 0, landed = 0;  // steps whose chunk is known to have landed
+  for (int g = 1; g < STAGES - (AHEAD ? 0 : 1); ++g) issue(g);
+  Frags f[AHEAD ? 2 : S];
+  if constexpr (AHEAD) {
+    wait_vmcnt<(STAGES - 1) * PER>();
+    lds_barrier();
+    read(0, 0, f[0]);
+  }
+  int g = 0, landed = 0;  // landed: steps whose chunk is known to have arrived
   for (int t = 0; t < my; ++t) {
+    const int tile = first + t * G;
+    const int64_t r0 = (int64_t)(tile % row_tiles) * BM + 32 * MI * wm;
+    const int64_t v0 = (int64_t)(tile / row_tiles) * BN + 32 * NJ * wn;
+    // The scales of the lane's columns are loaded here, and those of its rows
+    // (the same for half a wave) by scalar loads at the end: a vector load
+    // that some path leaves unused would make the compiler wait for all
+    // memory inside the chunk loop.
+    float wsc[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      const int64_t v = v0 + 32 * j + (lane & 31);
+      wsc[j] = p.ws[v < p.V ? v : p.V - 1];
+    }
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -264,61 +309,84 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
     for (int c = 0; c < C; ++c, ++g) {
-      // chunk g has landed for every wave, and every wave has read chunk g - 1
-      if (landed > 0) --landed;
-      else wait_vmcnt<(STAGES - 2) * PER>();
-      lds_barrier();
-      issue(g + STAGES - 1);
-      const unsigned char* const sa = &lds[(g % STAGES) * STAGE + (32 * MI * wm + (lane & 31)) * BK];
-      const unsigned char* const sb = &lds[(g % STAGES) * STAGE + (BM + 32 * NJ * wn + (lane & 31)) * BK];
+      if constexpr (AHEAD) {
 #pragma unroll
-      for (int s = 0; s < BK / 32; ++s) {
-        const int at = 16 * ((2 * s + (lane >> 5)) ^ (lane & 7));
-        i32x4_t fa[MI], fb[NJ];
+        for (int s = 0; s < S - 1; ++s) {
+          read(g, s + 1, f[(s + 1) & 1]);
+          multiply(f[s & 1]);
+        }
+        // The chunk's last products run behind the hand-over to the next: its
+        // loads have landed for every wave, every wave has read all of this
+        // chunk, whose stage takes the loads of chunk g + STAGES.
+        wait_vmcnt<(STAGES - 2) * PER>();
+        lds_barrier();
+        read(g + 1, 0, f[0]);  // before the loads, which would hold up LDS
+        issue(g + STAGES);
+        multiply(f[(S - 1) & 1]);
+      } else {
+        // chunk g has landed for every wave, and every wave has read chunk g - 1
+        if (landed > 0) --landed;
+        else wait_vmcnt<(STAGES - 2) * PER>();
+        lds_barrier();
+        issue(g + STAGES - 1);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) fa[i] = *(const i32x4_t*)(sa + i * 32 * BK + at);
+        for (int s = 0; s < S; ++s) read(g, s, f[s]);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) fb[j] = *(const i32x4_t*)(sb + j * 32 * BK + at);
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        for (int s = 0; s < S; ++s) multiply(f[s]);
+        put(g + 1);
       }
-      if constexpr (!DIRECT) put(g + 1);
     }
-    // The counted waits above hold for loads alone, so every chunk on its way
-    // is waited for before the stores go out (the last was issued a step ago).
-    wait_vmcnt<0>();
-    landed = STAGES - 1;
-    // the tile's sums times its scales: lane l holds column l % 32 of rows
-    // 8 (e / 4) + 4 (l / 32) + e % 4 of each block
-    const int tile = first + t * G;
-    const int64_t r0 = (int64_t)(tile % row_tiles) * BM + 32 * MI * wm + 4 * (lane >> 5);
-    const int64_t v0 = (int64_t)(tile / row_tiles) * BN + 32 * NJ * wn + (lane & 31);
-    float wsc[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) wsc[j] = v0 + 32 * j < p.V ? p.ws[v0 + 32 * j] : 0.0f;
+    if constexpr (!AHEAD) {
+      // the chunks on their way (the last was issued a step ago), so that the
+      // next steps need not wait for the stores
+      wait_vmcnt<0>();
+      landed = STAGES - 1;
+    }
+    // The tile's sums times its scales.  Lane l holds column l % 32 of rows
+    // 8 (e / 4) + 4 (l / 32) + e % 4 of each block, which as they are would
+    // leave in stores of one element a lane (a ninth of the whole time at
+    // 2560 rows).  So ER rows at a time go through the wave's own LDS, in
+    // 16-byte pieces, those of every other four rows moved by half a row so
+    // that both halves of the wave write to different banks, and leave in
+    // whole pieces of consecutive columns.
+    unsigned char* const mine = &lds[STAGES * STAGE + wave * EBYTES];
+    constexpr int PIECES = EROW / 16, HALF = PIECES / 2;  // of a row
+    constexpr int SETS = ER / 8;                          // groups of 8 rows in an exchange
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const int64_t rb = r0 + 32 * i + 8 * e4;
+      for (int x = 0; x < 4 / SETS; ++x) {
+        const int64_t rb = r0 + 32 * i + ER * x;  // first row of the exchange
         if (rb >= p.rows) continue;
-        const f32x4_t xsc = *(const f32x4_t*)(p.xs + rb);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t n = rb + e;
-          if (n >= p.rows) continue;
+        for (int u = 0; u < SETS; ++u) {
+          const int lr = 8 * u + 4 * (lane >> 5);  // first of the lane's four rows
+          const auto* const xs = (const __attribute__((address_space(4))) float*)(p.xs + rb + 8 * u);
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const int64_t v = v0 + 32 * j;
-            const float y = (xsc[e] * wsc[j]) * (float)acc[i][j][4 * e4 + e];
-            if (v < p.V) {
-              if constexpr (OBF)
-                __builtin_nontemporal_store((uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu), (uint16_t*)p.out + n * p.V + v);
-              else
-                __builtin_nontemporal_store(y, (float*)p.out + n * p.V + v);
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+              const float y = ((lane >> 5 ? xs[4 + e] : xs[e]) * wsc[j]) * (float)acc[i][j][4 * (SETS * x + u) + e];
+              const int byte = (32 * j + (lane & 31)) * OS;
+              unsigned char* const at = mine + (lr + e) * EROW + 16 * ((byte >> 4) ^ (HALF * (lane >> 5))) + (byte & 15);
+              if constexpr (OBF) *(uint16_t*)at = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
+              else *(float*)at = y;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < ER * PIECES / 64; ++h) {
+          const int pc = lane + 64 * h, lr = pc / PIECES, q = pc % PIECES;
+          const u32x4_t w = *(const u32x4_t*)(mine + lr * EROW + 16 * (q ^ (HALF * (lr >> 2 & 1))));
+          const int64_t n = rb + lr, v = v0 + q * (16 / OS);
+          if (n < p.rows && v < p.V) {
+            unsigned char* const dst = (unsigned char*)p.out + (n * p.V + v) * OS;
+            if (v + 16 / OS <= p.V) {
+              __builtin_nontemporal_store(w, (u32x4_any_t*)dst);
+            } else {
+              for (int e = 0; e < (int)(p.V - v); ++e) {
+                if constexpr (OBF) ((uint16_t*)dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                else ((uint32_t*)dst)[e] = w[e];
+              }
             }
           }
         }
@@ -328,7 +396,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
 }
 
 namespace {
-template <int MI, int NJ, int WM, int WN, int STAGES, bool DIRECT>
+template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, bool DIRECT>
 hipError_t head_go(const Int8HeadParams& p, bool obf, int groups, hipStream_t s) {
   constexpr int BM = 32 * MI * WM, BN = 32 * NJ * WN;
   const int64_t rt = (p.rows + BM - 1) / BM, tiles = rt * ((p.V + BN - 1) / BN);
@@ -337,21 +405,70 @@ hipError_t head_go(const Int8HeadParams& p, bool obf, int groups, hipStream_t s)
   if ((tiles / groups + 1) * (p.ldx / kInt8K) > 0x3FFFFFFF) return hipErrorNotSupported;
   const dim3 grid((unsigned)(tiles < groups ? tiles : groups)), block(64 * WM * WN);
   if (obf)
-    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, DIRECT, true>), grid, block, 0, s, p, (int)rt, (int)tiles);
+    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, DIRECT, true>), grid, block, 0, s, p, (int)rt,
+                       (int)tiles);
   else
-    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, DIRECT, false>), grid, block, 0, s, p, (int)rt, (int)tiles);
+    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, DIRECT, false>), grid, block, 0, s, p, (int)rt,
+                       (int)tiles);
   return hipGetLastError();
+}
+}  // namespace
+
+// The forms of the kernel, and what a round of their tiles over the CUs takes
+// beside one another (us at d = 5120, tiles sharing the head's rows; a round
+// of one tile a CU, or of two where two workgroups fit).  Small tiles win
+// where a larger one would compute rows that do not exist or leave CUs
+// without a tile, large ones by their rate: the form with the shortest sum
+// of rounds is taken.  At V = 129280, in us (128x256, 192x256, 256x256,
+// 320x256 tiles): 128 rows 132, 155, 167, 188; 192 rows 192, 163, 180, 195;
+// 256 rows 204, 259, 186, 204; 320 rows 268, 269, 311, 211.  64 rows:
+// 121 with 64x256 tiles, 171 with 32x128; one row at V = 32003 as well as
+// 37 rows are fastest with the smallest tiles that cover them.
+namespace {
+struct Form {
+  int bm, bn, per_cu;
+  float round;
+};
+constexpr Form kDirect[] = {{32, 128, 1, 14.0f},  {64, 128, 1, 19.0f},  {64, 256, 1, 32.0f}, {128, 256, 1, 45.0f},
+                            {192, 256, 1, 59.0f}, {256, 256, 1, 78.0f}, {320, 256, 1, 90.0f}};
+constexpr Form kStaged[] = {{64, 128, 2, 48.0f}, {128, 256, 1, 68.0f}, {192, 256, 1, 78.0f}, {256, 256, 1, 92.0f}};
+
+template <int N>
+int pick_form(const Form (&forms)[N], int64_t rows, int64_t V, int num_cus) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < N; ++i) {
+    const Form& f = forms[i];
+    const int64_t tiles = ((rows + f.bm - 1) / f.bm) * ((V + f.bn - 1) / f.bn), slots = (int64_t)num_cus * f.per_cu;
+    const double cost = (double)((tiles + slots - 1) / slots) * f.round;
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
 }
 }  // namespace
 
 hipError_t launch_int8_head(const Int8HeadParams& p, bool out_bf16, int num_cus, hipStream_t s) {
   if (num_cus < 1 || p.d > kInt8MaxInner || p.ldx % kInt8K != 0 || p.ldx < p.d) return hipErrorNotSupported;
-  const bool direct = p.d % 16 == 0 && (uintptr_t)p.wq % 16 == 0;
-  if (!direct) return head_go<2, 1, 1, 4, 2, false>(p, out_bf16, 3 * num_cus, s);
-  if (p.rows <= 32) return head_go<1, 1, 1, 4, 4, true>(p, out_bf16, num_cus, s);
-  if (p.rows <= 64) return head_go<2, 1, 1, 4, 4, true>(p, out_bf16, num_cus, s);
-  if (p.rows <= 128) return head_go<2, 2, 2, 4, 3, true>(p, out_bf16, num_cus, s);
-  return head_go<4, 2, 2, 4, 2, true>(p, out_bf16, num_cus, s);
+  if (p.d % 16 == 0 && (uintptr_t)p.wq % 16 == 0) {
+    switch (pick_form(kDirect, p.rows, p.V, num_cus)) {
+      case 0: return head_go<1, 1, 1, 4, 4, false, true>(p, out_bf16, num_cus, s);
+      case 1: return head_go<1, 1, 2, 4, 4, false, true>(p, out_bf16, num_cus, s);
+      case 2: return head_go<1, 2, 2, 4, 3, false, true>(p, out_bf16, num_cus, s);
+      case 3: return head_go<2, 2, 2, 4, 3, true, true>(p, out_bf16, num_cus, s);
+      case 4: return head_go<3, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
+      case 5: return head_go<4, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
+      default: return head_go<5, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
+    }
+  }
+  switch (pick_form(kStaged, p.rows, p.V, num_cus)) {
+    case 0: return head_go<1, 1, 2, 4, 2, false, false>(p, out_bf16, 2 * num_cus, s);
+    case 1: return head_go<2, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
+    case 2: return head_go<3, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
+    default: return head_go<4, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
+  }
 }
 
 }  // namespace dspark

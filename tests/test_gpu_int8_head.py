@@ -236,3 +236,21 @@ def test_int8_head_feeds_the_draft(native):
                                                   token_mask=mask)
     assert (tok % 7 == 0).all()
     assert torch.equal(proc.cpu().argmax(-1), tok.cpu())
+
+
+@pytest.mark.parametrize("d", [144, 151])
+@pytest.mark.parametrize("rows,V", [(5, 200), (40, 300), (64, 70000), (65, 70000), (192, 70001), (250, 70000), (320, 70100),
+                                    (512, 33000), (321, 70000)])
+def test_every_tile_form(native, rows, V, d):
+    """Sizes on both sides of the rule that picks the tile, heads read straight
+    into LDS (d a multiple of 16) and through registers; several tiles a
+    workgroup, and the last of them partial."""
+    x = _rows(rows, d, BF16, rows + d).cuda()
+    hq, hs = (t.cuda() for t in _head(V, d, V))
+    for out in (F32, BF16):
+        got = rmd.lm_head_logits_int8(x, hq, hs, out_dtype=out)
+        q, s = rmd.quantize_rows(x)
+        # sums of 151 products of 127 * 127 are whole numbers below 2^24: exact in fp32
+        acc = q.float() @ hq.float().t()
+        want = ((s[:, None] * hs[None, :]) * acc).to(out)
+        assert torch.equal(got, want)
