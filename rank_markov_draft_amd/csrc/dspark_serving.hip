@@ -143,27 +143,8 @@ dspark_status_t run_rules(const void* grad, const void* logits, dspark_dtype_t d
 size_t table_bits_bytes(int64_t B, int64_t V) {
   return align256(mul_sz(mul_sz((size_t)B, (size_t)dspark::rule_words(V)), 4));
 }
-size_t table_counts_bytes(int64_t B, int64_t V) { return align256(mul_sz(mul_sz((size_t)B, (size_t)V), 4)); }
-
-// Corrected logits of step k into p.out by the sampling step's kernels.
-hipError_t corrected_step(dspark::KernelParams& p, bool tile, bool f32_tile, bool logits_bf16, bool weights_bf16,
-                          int cus, hipStream_t s) {
-  hipError_t e = hipErrorNotSupported;
-  if (tile || f32_tile) {
-    p.nparts = dspark::sample_step_parts(p.V);
-    e = dspark::launch_sample_step(p, f32_tile, cus, s);
-    if (e == hipErrorNotSupported && tile) {
-      (void)hipGetLastError();
-      p.nparts = vocab_slices(p.V);
-      e = dspark::launch_tile(p, s);
-    }
-  }
-  if (e == hipErrorNotSupported) {
-    (void)hipGetLastError();
-    p.nparts = dspark::generic_parts(p.V);
-    e = dspark::launch_generic(p, logits_bf16, weights_bf16, s);
-  }
-  return e;
+size_t table_counts_bytes(int64_t B, int64_t V) {
+  return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 64));  // read in whole vectors of 16 columns
 }
 
 }  // namespace
@@ -286,9 +267,9 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   if (V > ((int64_t)1 << 30) || r > kGenericMaxRank) return DSPARK_ERR_UNSUPPORTED;
   if (B == 0 || M == 0) return DSPARK_OK;
   if (V == 0) return DSPARK_ERR_INVALID_ARGUMENT;  // nothing to draw from
-  dspark::SelectParams c{};
+  dspark::RuleStepParams p{};
   Ranges in;
-  st = check_rules(rules, B, M, V, &c.r, &in);
+  st = check_rules(rules, B, M, V, &p.r, &in);
   if (st != DSPARK_OK) return st;
   if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !processed_logits)
     return DSPARK_ERR_INVALID_ARGUMENT;
@@ -306,60 +287,43 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
     return DSPARK_ERR_INVALID_ARGUMENT;
 
   const hipStream_t s = (hipStream_t)stream;
-  const bool lbf = logits_dtype == DSPARK_BF16, wbf = weight_dtype == DSPARK_BF16;
-  const int cus = device_cus();
   char* const region = (char*)workspace + align256(dspark_markov_workspace_bytes(B, M, V, r, 1));
   uint32_t* const seen = (uint32_t*)region;
   uint32_t* const counts = (uint32_t*)(region + table_bits_bytes(B, V));
   // without penalties, or with nothing before a single position, no token is
   // ever looked up
-  const bool table = dspark::rules_penalise(c.r) && (c.r.history != nullptr || M > 1);
+  const bool table = dspark::rules_penalise(p.r) && (p.r.history != nullptr || M > 1);
   hipError_t e = hipSuccess;
   if (table) {
-    const dspark::TableParams t{c.r, seen, counts, B, V};
-    e = dspark::launch_rule_table(t, cus, s);
+    const dspark::TableParams t{p.r, seen, counts, B, V};
+    e = dspark::launch_rule_table(t, s);
     if (e != hipSuccess) return device_failure(e, "rule table launch");
   }
-  const bool greedy = temperature < 1e-5;
-  dspark::KernelParams p{};
   p.base = base_logits;
   p.out = processed_logits;
-  p.ids = first_prev_token_ids;
+  p.first = first_prev_token_ids;
   p.tokens = sampled_tokens;
   p.w1 = w1;
   p.w2 = w2;
-  p.bad_rows = (uint32_t*)workspace;
+  p.seen = table ? seen : nullptr;
+  p.counts = counts;
   p.partials = (uint64_t*)((char*)workspace + kDataOffset);
-  p.rows = B;
-  p.V = V;
-  p.r = r;
+  p.bad_rows = (uint32_t*)workspace;
+  p.B = B;
   p.M = M;
-  p.mode = dspark::MODE_GREEDY;  // its keys are not used: the rules come first
-  const bool tile = tile_path(logits_dtype, weight_dtype, V, r, base_logits, processed_logits, w1, w2);
-  const bool f32_tile =
-      !lbf && tile_path(DSPARK_BF16, weight_dtype, V, r, base_logits, processed_logits, w1, w2);
-  c.logits = processed_logits;
-  c.seen = table ? seen : nullptr;
-  c.counts = counts;
-  c.partials = p.partials;
-  c.B = B;
-  c.M = M;
-  c.V = V;
-  c.batch_offset = batch_offset;
-  c.kappa = greedy ? 0.0f : (float)(1.4426950408889634 / temperature);
-  c.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
-  c.seed_hi = (uint32_t)(seed >> 32);
-  c.greedy = greedy;
+  p.V = V;
+  p.rank = r;
+  p.batch_offset = batch_offset;
+  p.greedy = temperature < 1e-5;
+  p.kappa = p.greedy ? 0.0f : (float)(1.4426950408889634 / temperature);
+  p.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
+  p.seed_hi = (uint32_t)(seed >> 32);
   for (int64_t k = 0; k < M; ++k) {
     p.k = k;
     p.k_abs = (uint32_t)(position_offset + k);
-    c.k = k;
-    c.k_abs = p.k_abs;
-    e = corrected_step(p, tile, f32_tile, lbf, wbf, cus, s);
-    if (e != hipSuccess) return device_failure(e, "corrected step launch");
-    e = dspark::launch_rule_select(c, lbf, s);
-    if (e != hipSuccess) return device_failure(e, "rule select launch");
-    e = dspark::launch_rule_choose(c.partials, dspark::select_parts(V), B, M, k, V, sampled_tokens,
+    e = dspark::launch_rule_step(p, logits_dtype == DSPARK_BF16, weight_dtype == DSPARK_BF16, s);
+    if (e != hipSuccess) return device_failure(e, "rule step launch");
+    e = dspark::launch_rule_choose(p.partials, dspark::rule_step_parts(V), B, M, k, V, sampled_tokens,
                                    table ? seen : nullptr, counts, s);
     if (e != hipSuccess) return device_failure(e, "token choice launch");
   }

@@ -56,19 +56,27 @@ struct TableParams {
   int64_t B;
   int64_t V;
 };
-hipError_t launch_rule_table(const TableParams& p, int num_cus, hipStream_t s);
+hipError_t launch_rule_table(const TableParams& p, hipStream_t s);
 
-// Step k of a left-to-right draft: the rules on row (b, k) of `logits` in
-// place, and the row's best keys over select_parts(V) slices.
-struct SelectParams {
+// Step k of a left-to-right draft in one pass: the corrected logits of row
+// (b, k) (base plus the bias of its predecessor), the rules, the processed row
+// to `out`, and the row's best keys over rule_step_parts(V) blocks of columns.
+struct RuleStepParams {
   RuleSet r;
-  void* logits;            // [B, M, V]
+  const void* base;        // [B, M, V]
+  void* out;               // [B, M, V]
+  const int64_t* first;    // [B] predecessors of position 0
+  const int64_t* tokens;   // [B, M] predecessors of the others, at k - 1
+  const void* w1;          // [V, rank]
+  const void* w2;          // [V, rank]
   const uint32_t* seen;    // table, or null (no penalty)
-  const uint32_t* counts;
-  uint64_t* partials;      // [B, select_parts(V)]
+  const uint32_t* counts;  // readable 64 bytes past its end
+  uint64_t* partials;      // [B, rule_step_parts(V)]
+  uint32_t* bad_rows;
   int64_t B;
   int64_t M;
   int64_t V;
+  int64_t rank;
   int64_t k;
   int64_t batch_offset;
   float kappa;             // (float)(log2(e) / T); unused when greedy
@@ -77,8 +85,8 @@ struct SelectParams {
   uint32_t seed_hi;
   bool greedy;
 };
-int64_t select_parts(int64_t V);
-hipError_t launch_rule_select(const SelectParams& p, bool logits_bf16, hipStream_t s);
+int64_t rule_step_parts(int64_t V);
+hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, hipStream_t s);
 
 // tokens[b, k] = the column of the row's best key, -1 when its score is -inf;
 // a drawn token joins the table (seen null: no table).

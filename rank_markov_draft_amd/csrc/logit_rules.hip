@@ -345,8 +345,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_table_kernel(TableParams p,
     if (seen[i >> 5] >> (i & 31) & 1u) gc[i] = counts[i];
 }
 
-hipError_t launch_rule_table(const TableParams& p, int num_cus, hipStream_t s) {
-  (void)num_cus;
+hipError_t launch_rule_table(const TableParams& p, hipStream_t s) {
   const int64_t tiles = (p.V + kTableCols - 1) / kTableCols;
   if (p.B * tiles > 0x7FFFFFFF) return hipErrorNotSupported;
   hipLaunchKernelGGL(rule_table_kernel, dim3((unsigned)(p.B * tiles)), dim3(kRuleThreads), 0, s, p, (int)tiles);
@@ -354,102 +353,256 @@ hipError_t launch_rule_table(const TableParams& p, int num_cus, hipStream_t s) {
 }
 
 namespace {
-constexpr int kSelectCols = 4096;  // columns of a workgroup's slice of a row
-}
-int64_t select_parts(int64_t V) { return (V + kSelectCols - 1) / kSelectCols; }
+constexpr int kStepWaveCols = 64;                    // columns of a wave
+constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
+constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
+constexpr int kStepPitch = kStepRowBytes + 16;       // its pitch in LDS
 
-// One row's slice: the rules in place, then the slice's best key (the scores
-// of sample_block_tokens on the processed values).
-template <bool BF>
-__global__ __launch_bounds__(kRuleThreads) void rule_select_kernel(SelectParams p, int parts) {
-  __shared__ uint64_t lds_key[kRuleThreads / 64];
-  const int64_t b = blockIdx.x / (unsigned)parts;
-  const int part = (int)(blockIdx.x % (unsigned)parts);
+// 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
+template <int EB>
+__device__ __forceinline__ u32x4_t weights16(const char* row, int64_t k, int64_t rank) {
+  constexpr int E = 16 / EB;
+  u32x4_t w = {0u, 0u, 0u, 0u};
+  if (k + E <= rank) {
+    w = *(const u32x4_any_t*)(row + k * EB);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (k + e < rank) {
+        if constexpr (EB == 2) w[e >> 1] |= (uint32_t)((const uint16_t*)row)[k + e] << (16 * (e & 1));
+        else w[e] = ((const uint32_t*)row)[k + e];
+      }
+  }
+  return w;
+}
+}  // namespace
+
+int64_t rule_step_parts(int64_t V) { return (V + kStepCols - 1) / kStepCols; }
+
+// A workgroup: 256 columns, all rows of the step in passes of 16 RT.  The
+// bias of a row tile is a product on the matrix cores with the vocabulary on
+// M and the rows on N (16 x 16 blocks, bf16 or fp32 as the weights are); the
+// columns of a wave's four blocks are interleaved, block t's column m at
+// 16 (m / 4) + 4 t + m % 4, so that a lane ends up with 16 consecutive columns of
+// one row, to which it adds the base logits (loaded before the product),
+// applies the rules and finds the best score, all in registers.  W2 goes from
+// memory to the operands directly (each element is used by one wave of the
+// workgroup), the gathered W1 rows through LDS.
+template <bool WBF, bool BF, int RT>
+__global__ __launch_bounds__(256, RT == 4 ? 2 : 3) void rule_step_kernel(RuleStepParams p) {
+  constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;          // bytes of a weight, weights of a 16-byte piece
+  constexpr int KI = 4 * KE;                             // rank elements of a step (32 or 16)
+  constexpr int KC = kStepRowBytes / WB;                 // and of a chunk
+  constexpr int LB = BF ? 2 : 4, LV = BF ? 2 : 4;        // bytes of a logit, 16-byte vectors of 16 logits
+  __shared__ __attribute__((aligned(16))) unsigned char lds_e[16 * RT * kStepPitch];
+  __shared__ int64_t lds_src[16 * RT];
+  __shared__ uint64_t lds_key[4][16 * RT];
   const int tid = threadIdx.x;
-  const int V = (int)p.V;
-  const int end = V - part * kSelectCols < kSelectCols ? V : (part + 1) * kSelectCols;
-  const Penalty pen = penalty_of(p.r, b);
-  constexpr int ES = BF ? 2 : 4;
-  char* const row = (char*)p.logits + (b * p.M + p.k) * p.V * ES;
-  const uint8_t* const seen = p.seen ? (const uint8_t*)(p.seen + b * ((V + 31) / 32)) : nullptr;
-  const uint32_t* const counts = p.seen ? p.counts + b * p.V : nullptr;
-  const uint8_t* const mask =
-      p.r.mask ? (const uint8_t*)(p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m) : nullptr;
-  uint64_t best = 0;
-  constexpr int U = kSelectCols / (8 * kRuleThreads);
-  Raw8<BF> raw[U];
-  uint32_t s8[U], m8[U];
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int n16 = lane & 15, g4 = lane >> 4;
+  const int64_t V = p.V, rank = p.rank;
+  const int64_t wc0 = (int64_t)blockIdx.x * kStepCols + kStepWaveCols * wave;  // the wave's first column
+  const int64_t c = wc0 + 16 * g4;                                            // the lane's first
+  const int cn = c < V ? (int)(V - c < 16 ? V - c : 16) : 0;                   // columns of it that exist
+
+  // the lane's W2 rows as operands (rows past V read the last one: their sums are not used)
+  const char* wrow[4];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = part * kSelectCols + 8 * (tid + u * kRuleThreads);
-    if (c < end) {
-      raw[u] = load8<BF, true>(row + (int64_t)c * ES, V - c);
-      s8[u] = seen ? seen[c / 8] : 0u;
-      m8[u] = mask ? mask[c / 8] : 0xFFu;
-    }
+  for (int t = 0; t < 4; ++t) {
+    const int64_t v = wc0 + 16 * (n16 >> 2) + 4 * t + (n16 & 3);
+    wrow[t] = (const char*)p.w2 + (v < V ? v : V - 1) * rank * WB;
   }
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int c = part * kSelectCols + 8 * (tid + u * kRuleThreads);
-    if (c >= end) break;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = raw[u][i];
-    if (s8[u]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (s8[u] >> i & 1u) x[i] = pen.apply(x[i], counts[c + i]);
-    }
-    if (p.r.bias) {
-      float bias[8];
-      bias8(p.r, b * p.r.bias_stride + c, V - c, bias);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] += bias[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = (m8[u] >> i & 1u) ? x[i] : -__builtin_inff();
-      if constexpr (BF) x[i] = bf16_rne(x[i]);
-    }
-    store8<BF>(row + (int64_t)c * ES, V - c, x);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (!p.greedy) {
-        const Philox4 q = philox4x32_10((uint32_t)(c >> 2) + (uint32_t)j, p.k_abs,
-                                        (uint32_t)p.batch_offset + (uint32_t)b, 0u, p.seed_lo, p.seed_hi);
-        g[0] = gumbel2_from_word(q.x0);
-        g[1] = gumbel2_from_word(q.x1);
-        g[2] = gumbel2_from_word(q.x2);
-        g[3] = gumbel2_from_word(q.x3);
+  for (int64_t b0 = 0; b0 < p.B; b0 += 16 * RT) {
+    if (b0 > 0) __syncthreads();
+    if (tid < 16 * RT) {
+      int64_t x = -1;
+      if (b0 + tid < p.B) {
+        x = p.k == 0 ? p.first[b0 + tid] : p.tokens[(b0 + tid) * p.M + p.k - 1];
+        if (x < 0 || x >= V) {
+          if (blockIdx.x == 0 && p.k == 0) atomicAdd(p.bad_rows, 1u);
+          x = -1;
+        }
       }
+      lds_src[tid] = x;
+    }
+    // base logits and the bits of the rules, on their way during the product
+    u32x4_t base[RT][LV];
+    uint32_t mask[RT], seen[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = c + 4 * j + i;
-        const float sc = p.greedy ? x[4 * j + i] : __builtin_fmaf(x[4 * j + i], p.kappa, g[i]);
-        if (v < V) best = max_u64(best, argmax_key(sc, (uint32_t)v));
+    for (int i = 0; i < RT; ++i) {
+      const int64_t b = b0 + 16 * i + n16;
+      mask[i] = 0xFFFFu;
+      seen[i] = 0u;
+#pragma unroll
+      for (int h = 0; h < LV; ++h) base[i][h] = u32x4_t{0u, 0u, 0u, 0u};
+      if (b < p.B && cn > 0) {
+        const char* const at = (const char*)p.base + ((b * p.M + p.k) * V + c) * LB;
+        if (cn == 16) {
+#pragma unroll
+          for (int h = 0; h < LV; ++h) base[i][h] = __builtin_nontemporal_load((const u32x4_any_t*)at + h);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e < cn) {
+              if constexpr (BF) base[i][e >> 3][e >> 1 & 3] |= (uint32_t)((const uint16_t*)at)[e] << (16 * (e & 1));
+              else base[i][e >> 2][e & 3] = ((const uint32_t*)at)[e];
+            }
+        }
+        if (p.r.mask) mask[i] = ((const uint16_t*)(p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m))[c >> 4];
+        if (p.seen) seen[i] = ((const uint16_t*)(p.seen + b * ((V + 31) / 32)))[c >> 4];
       }
     }
-  }
-  best = wave_max_u64_lane63(best);
-  if ((tid & 63) == 63) lds_key[tid >> 6] = best;
-  __syncthreads();
-  if (tid == 0) {
+    f32x4_t acc[RT][4];
 #pragma unroll
-    for (int w = 1; w < kRuleThreads / 64; ++w) best = max_u64(w == 1 ? lds_key[0] : best, lds_key[w]);
-    p.partials[b * parts + part] = best;
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int64_t k0 = 0; k0 < rank; k0 += KC) {
+      __syncthreads();  // the sources are set, and the last chunk is read
+      for (int i = tid; i < 16 * RT * (kStepRowBytes / 16); i += 256) {
+        const int row = i / (kStepRowBytes / 16), q = i % (kStepRowBytes / 16);
+        const int64_t x = lds_src[row];
+        *(u32x4_t*)&lds_e[row * kStepPitch + 16 * q] =
+            x >= 0 ? weights16<WB>((const char*)p.w1 + x * rank * WB, k0 + q * KE, rank) : u32x4_t{0u, 0u, 0u, 0u};
+      }
+      __syncthreads();
+      auto step = [&](int kk, const u32x4_t (&w)[4]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const u32x4_t e = *(const u32x4_t*)&lds_e[(16 * i + n16) * kStepPitch + (4 * kk + g4) * 16];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if constexpr (WBF) {
+              acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[t]),
+                                                                  __builtin_bit_cast(bf16x8_t, e), acc[i][t], 0, 0, 0);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[t][j]), __uint_as_float(e[j]),
+                                                                 acc[i][t], 0, 0, 0);
+            }
+          }
+        }
+      };
+      const int64_t left = rank - k0 < KC ? rank - k0 : KC;
+      const int whole = (int)(left / KI);
+#pragma unroll 4
+      for (int kk = 0; kk < whole; ++kk) {
+        u32x4_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = *(const u32x4_any_t*)(wrow[t] + (k0 + kk * KI + g4 * KE) * WB);
+        step(kk, w);
+      }
+      if (whole * KI < left) {
+        u32x4_t w[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) w[t] = weights16<WB>(wrow[t], k0 + whole * KI + g4 * KE, rank);
+        step(whole, w);
+      }
+    }
+    // counts of the columns that stand in the table, all fetched before use
+    u32x4_t count[RT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      if (seen[i]) {
+        const u32x4_any_t* const at = (const u32x4_any_t*)(p.counts + (b0 + 16 * i + n16) * V + c);
+#pragma unroll
+        for (int h = 0; h < 4; ++h) count[i][h] = at[h];
+      }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int64_t b = b0 + 16 * i + n16;
+      const bool live = b < p.B && cn > 0;
+      float x[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        float bias = acc[i][e >> 2][e & 3];
+        if constexpr (WBF || BF) bias = bf16_rne(bias);
+        if constexpr (BF) {
+          const uint32_t w = base[i][e >> 3][e >> 1 & 3];
+          x[e] = bf16_rne(((e & 1) ? bf16_hi(w) : bf16_lo(w)) + bias);
+        } else {
+          x[e] = __uint_as_float(base[i][e >> 2][e & 3]) + bias;
+        }
+      }
+      if (live) {
+        if (seen[i]) {
+          const Penalty pen = penalty_of(p.r, b);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (seen[i] >> e & 1u) x[e] = pen.apply(x[e], count[i][e >> 2][e & 3]);
+        }
+        if (p.r.bias) {
+          float bias[8];
+          bias8(p.r, b * p.r.bias_stride + c, cn, bias);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] += bias[e];
+          if (cn > 8) {
+            bias8(p.r, b * p.r.bias_stride + c + 8, cn - 8, bias);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[8 + e] += bias[e];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        x[e] = (mask[i] >> e & 1u) ? x[e] : -__builtin_inff();
+        if constexpr (BF) x[e] = bf16_rne(x[e]);
+      }
+      uint64_t best = 0;
+      if (live) {
+        char* const at = (char*)p.out + ((b * p.M + p.k) * V + c) * LB;
+        float half[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) half[e] = x[e];
+        store8<BF>(at, cn, half);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) half[e] = x[8 + e];
+        store8<BF>(at + 8 * LB, cn - 8, half);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (!p.greedy) {
+            const Philox4 q = philox4x32_10((uint32_t)(c >> 2) + (uint32_t)j, p.k_abs,
+                                            (uint32_t)p.batch_offset + (uint32_t)b, 0u, p.seed_lo, p.seed_hi);
+            g[0] = gumbel2_from_word(q.x0);
+            g[1] = gumbel2_from_word(q.x1);
+            g[2] = gumbel2_from_word(q.x2);
+            g[3] = gumbel2_from_word(q.x3);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float sc = p.greedy ? x[4 * j + e] : __builtin_fmaf(x[4 * j + e], p.kappa, g[e]);
+            if (4 * j + e < cn) best = max_u64(best, argmax_key(sc, (uint32_t)(c + 4 * j + e)));
+          }
+        }
+      }
+      best = max_row_lanes(best);
+      if (lane < 16) lds_key[wave][16 * i + lane] = best;
+    }
+    __syncthreads();
+    if (tid < 16 * RT && b0 + tid < p.B) {
+      const uint64_t a = max_u64(lds_key[0][tid], lds_key[1][tid]), b = max_u64(lds_key[2][tid], lds_key[3][tid]);
+      p.partials[(b0 + tid) * gridDim.x + blockIdx.x] = max_u64(a, b);
+    }
   }
 }
 
-hipError_t launch_rule_select(const SelectParams& p, bool logits_bf16, hipStream_t s) {
-  const int64_t parts = select_parts(p.V);
-  if (p.B * parts > 0x7FFFFFFF) return hipErrorNotSupported;
-  const dim3 grid((unsigned)(p.B * parts)), block(kRuleThreads);
-  if (logits_bf16)
-    hipLaunchKernelGGL(rule_select_kernel<true>, grid, block, 0, s, p, (int)parts);
-  else
-    hipLaunchKernelGGL(rule_select_kernel<false>, grid, block, 0, s, p, (int)parts);
+namespace {
+template <bool WBF, bool BF>
+hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)rule_step_parts(p.V)), block(256);
+  if (p.B <= 16) hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 1>), grid, block, 0, s, p);
+  else if (p.B <= 32) hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 2>), grid, block, 0, s, p);
+  else hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 4>), grid, block, 0, s, p);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, hipStream_t s) {
+  if (weights_bf16) return logits_bf16 ? rule_step_go<true, true>(p, s) : rule_step_go<true, false>(p, s);
+  return logits_bf16 ? rule_step_go<false, true>(p, s) : rule_step_go<false, false>(p, s);
 }
 
 // One workgroup per row.  The row's table belongs to this workgroup alone, so
