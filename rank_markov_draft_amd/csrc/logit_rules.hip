@@ -138,16 +138,27 @@ __device__ __forceinline__ void store8(void* at, int n, const float (&x)[8]) {
   }
 }
 
-// Biases of columns i .. i + 7 of the bias tensor (the first n exist).
+// Biases of columns i .. i + N - 1 of the bias tensor (N 8 or 4; the first n exist).
+template <int N>
 __device__ __forceinline__ void bias8(const RuleSet& r, int64_t i, int n, float (&x)[8]) {
-  if (r.bias_bf16) {
-    const Raw8<true> w = load8<true, false>((const uint16_t*)r.bias + i, n);
+  if (n >= N) {
+    if (r.bias_bf16) {
+      typedef uint32_t words_t __attribute__((ext_vector_type(N / 2), aligned(2)));
+      const words_t w = *(const words_t*)((const uint16_t*)r.bias + i);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = w[e];
+      for (int e = 0; e < N; ++e) x[e] = (e & 1) ? bf16_hi(w[e >> 1]) : bf16_lo(w[e >> 1]);
+    } else {
+#pragma unroll
+      for (int h = 0; h < N / 4; ++h) {
+        const u32x4_t w = *(const u32x4_any_t*)((const float*)r.bias + i + 4 * h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[4 * h + e] = __uint_as_float(w[e]);
+      }
+    }
   } else {
-    const Raw8<false> w = load8<false, false>((const float*)r.bias + i, n);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = w[e];
+    for (int e = 0; e < N; ++e)
+      x[e] = e >= n ? 0.0f : r.bias_bf16 ? bf16_lo(((const uint16_t*)r.bias)[i + e]) : ((const float*)r.bias)[i + e];
   }
 }
 
@@ -236,7 +247,7 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
         if (c >= tn) break;
         float bias[8];
         if constexpr (!BWD)
-          if (p.r.bias) bias8(p.r, b * p.r.bias_stride + t0 + c, tn - c, bias);
+          if (p.r.bias) bias8<8>(p.r, b * p.r.bias_stride + t0 + c, tn - c, bias);
         // what the penalties need where a bit is set, fetched before the rows
         const uint32_t a8 = track ? ((const uint8_t*)any)[c / 8] : 0u;
         uint32_t s8 = 0;
@@ -382,18 +393,21 @@ int64_t rule_step_parts(int64_t V) { return (V + kStepCols - 1) / kStepCols; }
 // A workgroup: 256 columns, all rows of the step in passes of 16 RT.  The
 // bias of a row tile is a product on the matrix cores with the vocabulary on
 // M and the rows on N (16 x 16 blocks, bf16 or fp32 as the weights are); the
-// columns of a wave's four blocks are interleaved, block t's column m at
-// 16 (m / 4) + 4 t + m % 4, so that a lane ends up with 16 consecutive columns of
-// one row, to which it adds the base logits (loaded before the product),
-// applies the rules and finds the best score, all in registers.  W2 goes from
+// columns of a wave's four blocks are dealt so that a lane ends up with whole
+// 16-byte vectors of logits of one row, NV of them, VC columns each: 16
+// consecutive columns in bf16, four quarters of the row's 64 in fp32, where a
+// lane's own 64 bytes at once would spread each load over all its lines (64
+// rows at V = 129280: 323 us so, 211 us as here).  To them it adds the base
+// logits (loaded before the product), applies the rules and finds the best
+// score, all in registers.  W2 goes from
 // memory to the operands directly (each element is used by one wave of the
 // workgroup), the gathered W1 rows through LDS.
 template <bool WBF, bool BF, int RT>
-__global__ __launch_bounds__(256, RT == 4 ? 2 : 3) void rule_step_kernel(RuleStepParams p) {
+__global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_kernel(RuleStepParams p, int tiles, unsigned chunks) {
   constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;          // bytes of a weight, weights of a 16-byte piece
   constexpr int KI = 4 * KE;                             // rank elements of a step (32 or 16)
   constexpr int KC = kStepRowBytes / WB;                 // and of a chunk
-  constexpr int LB = BF ? 2 : 4, LV = BF ? 2 : 4;        // bytes of a logit, 16-byte vectors of 16 logits
+  constexpr int LB = BF ? 2 : 4, VC = 16 / LB, NV = 16 / VC;
   __shared__ __attribute__((aligned(16))) unsigned char lds_e[16 * RT * kStepPitch];
   __shared__ int64_t lds_src[16 * RT];
   __shared__ uint64_t lds_key[4][16 * RT];
@@ -401,202 +415,275 @@ __global__ __launch_bounds__(256, RT == 4 ? 2 : 3) void rule_step_kernel(RuleSte
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63;
   const int n16 = lane & 15, g4 = lane >> 4;
+  // the row chunks of a column tile lie eight workgroups apart: on one XCD,
+  // whose L2 then holds the tile's W2 for all of them
+  const int tile = (int)(blockIdx.x / (8u * chunks)) * 8 + (int)(blockIdx.x % 8u);
+  const int64_t b0 = (int64_t)(blockIdx.x / 8u % chunks) * 16 * RT;
+  if (tile >= tiles) return;
   const int64_t V = p.V, rank = p.rank;
-  const int64_t wc0 = (int64_t)blockIdx.x * kStepCols + kStepWaveCols * wave;  // the wave's first column
-  const int64_t c = wc0 + 16 * g4;                                            // the lane's first
-  const int cn = c < V ? (int)(V - c < 16 ? V - c : 16) : 0;                   // columns of it that exist
-
+  const int wc0 = tile * kStepCols + kStepWaveCols * wave;  // the wave's first column (V is at most 2^30)
+  // first column of the lane's vector q, and how many of its columns exist
+  auto column = [&](int q) __attribute__((always_inline)) -> int {
+    return BF ? wc0 + 16 * g4 + VC * q : wc0 + 4 * VC * q + VC * g4;
+  };
+  int have[NV];
+#pragma unroll
+  for (int q = 0; q < NV; ++q) {
+    const int n = (int)V - column(q);
+    have[q] = n <= 0 ? 0 : n < VC ? n : VC;
+  }
   // the lane's W2 rows as operands (rows past V read the last one: their sums are not used)
   const char* wrow[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const int64_t v = wc0 + 16 * (n16 >> 2) + 4 * t + (n16 & 3);
-    wrow[t] = (const char*)p.w2 + (v < V ? v : V - 1) * rank * WB;
+    const int v = wc0 + (BF ? 16 * (n16 >> 2) + 4 * t + (n16 & 3) : 16 * t + n16);
+    wrow[t] = (const char*)p.w2 + (v < V ? (int64_t)v : V - 1) * rank * WB;
   }
-  for (int64_t b0 = 0; b0 < p.B; b0 += 16 * RT) {
-    if (b0 > 0) __syncthreads();
-    if (tid < 16 * RT) {
-      int64_t x = -1;
-      if (b0 + tid < p.B) {
-        x = p.k == 0 ? p.first[b0 + tid] : p.tokens[(b0 + tid) * p.M + p.k - 1];
-        if (x < 0 || x >= V) {
-          if (blockIdx.x == 0 && p.k == 0) atomicAdd(p.bad_rows, 1u);
-          x = -1;
-        }
+  if (tid < 16 * RT) {
+    int64_t x = -1;
+    if (b0 + tid < p.B) {
+      x = p.k == 0 ? p.first[b0 + tid] : p.tokens[(b0 + tid) * p.M + p.k - 1];
+      if (x < 0 || x >= V) {
+        if (tile == 0 && p.k == 0) atomicAdd(p.bad_rows, 1u);
+        x = -1;
       }
-      lds_src[tid] = x;
     }
-    // base logits and the bits of the rules, on their way during the product
-    u32x4_t base[RT][LV];
-    uint32_t mask[RT], seen[RT];
+    lds_src[tid] = x;
+  }
+  // base logits and the bits of the rules (the wave's 64 columns), on their
+  // way during the product
+  u32x4_t base[RT][NV];
+  uint64_t mask[RT], seen[RT];
+  const int W = (int)((V + 31) / 32);
+  // bits of the lane's columns from a row of words: its own 16 (bf16), or the
+  // wave's 64 (fp32, where they do not stand together)
+  auto row_bits = [&](const uint32_t* row) __attribute__((always_inline)) -> uint64_t {
+    if constexpr (BF) {
+      return have[0] > 0 ? ((const uint16_t*)row)[column(0) >> 4] : 0u;
+    } else {
+      const int w0 = wc0 >> 5;
+      return (uint64_t)(w0 < W ? row[w0] : 0u) | (uint64_t)(w0 + 1 < W ? row[w0 + 1] : 0u) << 32;
+    }
+  };
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int64_t b = b0 + 16 * i + n16;
-      mask[i] = 0xFFFFu;
-      seen[i] = 0u;
+  for (int i = 0; i < RT; ++i) {
+    const int64_t b = b0 + 16 * i + n16;
+    mask[i] = ~(uint64_t)0;
+    seen[i] = 0;
 #pragma unroll
-      for (int h = 0; h < LV; ++h) base[i][h] = u32x4_t{0u, 0u, 0u, 0u};
-      if (b < p.B && cn > 0) {
-        const char* const at = (const char*)p.base + ((b * p.M + p.k) * V + c) * LB;
-        if (cn == 16) {
+    for (int q = 0; q < NV; ++q) base[i][q] = u32x4_t{0u, 0u, 0u, 0u};
+    if (b < p.B) {
+      const char* const row = (const char*)p.base + (b * p.M + p.k) * V * LB;
 #pragma unroll
-          for (int h = 0; h < LV; ++h) base[i][h] = __builtin_nontemporal_load((const u32x4_any_t*)at + h);
+      for (int q = 0; q < NV; ++q) {
+        const char* const at = row + (int64_t)column(q) * LB;
+        const int n = have[q];
+        if (n == VC) {
+          base[i][q] = __builtin_nontemporal_load((const u32x4_any_t*)at);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e < cn) {
-              if constexpr (BF) base[i][e >> 3][e >> 1 & 3] |= (uint32_t)((const uint16_t*)at)[e] << (16 * (e & 1));
-              else base[i][e >> 2][e & 3] = ((const uint32_t*)at)[e];
+          for (int e = 0; e < VC; ++e)
+            if (e < n) {
+              if constexpr (BF) base[i][q][e >> 1] |= (uint32_t)((const uint16_t*)at)[e] << (16 * (e & 1));
+              else base[i][q][e] = ((const uint32_t*)at)[e];
             }
         }
-        if (p.r.mask) mask[i] = ((const uint16_t*)(p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m))[c >> 4];
-        if (p.seen) seen[i] = ((const uint16_t*)(p.seen + b * ((V + 31) / 32)))[c >> 4];
       }
+      if (p.r.mask) mask[i] = row_bits(p.r.mask + b * p.r.mask_stride_b + p.k * p.r.mask_stride_m);
+      if (p.seen) seen[i] = row_bits(p.seen + b * W);
     }
-    f32x4_t acc[RT][4];
+  }
+  // bits of the lane's 16 columns, as they stand in its vectors
+  auto own_bits = [&](uint64_t m) __attribute__((always_inline)) -> uint32_t {
+    if constexpr (BF) return (uint32_t)m & 0xFFFFu;
+    uint32_t o = 0;
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int q = 0; q < NV; ++q) o |= (uint32_t)(m >> (4 * VC * q + VC * g4) & ((1u << VC) - 1)) << (VC * q);
+    return o;
+  };
+  f32x4_t acc[RT][4];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int64_t k0 = 0; k0 < rank; k0 += KC) {
-      __syncthreads();  // the sources are set, and the last chunk is read
-      for (int i = tid; i < 16 * RT * (kStepRowBytes / 16); i += 256) {
-        const int row = i / (kStepRowBytes / 16), q = i % (kStepRowBytes / 16);
-        const int64_t x = lds_src[row];
-        *(u32x4_t*)&lds_e[row * kStepPitch + 16 * q] =
-            x >= 0 ? weights16<WB>((const char*)p.w1 + x * rank * WB, k0 + q * KE, rank) : u32x4_t{0u, 0u, 0u, 0u};
-      }
-      __syncthreads();
-      auto step = [&](int kk, const u32x4_t (&w)[4]) __attribute__((always_inline)) {
+  for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          const u32x4_t e = *(const u32x4_t*)&lds_e[(16 * i + n16) * kStepPitch + (4 * kk + g4) * 16];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if constexpr (WBF) {
-              acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[t]),
-                                                                  __builtin_bit_cast(bf16x8_t, e), acc[i][t], 0, 0, 0);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[t][j]), __uint_as_float(e[j]),
-                                                                 acc[i][t], 0, 0, 0);
-            }
-          }
-        }
-      };
-      const int64_t left = rank - k0 < KC ? rank - k0 : KC;
-      const int whole = (int)(left / KI);
-#pragma unroll 4
-      for (int kk = 0; kk < whole; ++kk) {
-        u32x4_t w[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = *(const u32x4_any_t*)(wrow[t] + (k0 + kk * KI + g4 * KE) * WB);
-        step(kk, w);
-      }
-      if (whole * KI < left) {
-        u32x4_t w[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = weights16<WB>(wrow[t], k0 + whole * KI + g4 * KE, rank);
-        step(whole, w);
-      }
-    }
-    // counts of the columns that stand in the table, all fetched before use
-    u32x4_t count[RT][4];
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-      if (seen[i]) {
-        const u32x4_any_t* const at = (const u32x4_any_t*)(p.counts + (b0 + 16 * i + n16) * V + c);
-#pragma unroll
-        for (int h = 0; h < 4; ++h) count[i][h] = at[h];
-      }
+    for (int t = 0; t < 4; ++t) acc[i][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](int kk, const u32x4_t (&w)[4]) __attribute__((always_inline)) {  // step kk of the chunk in LDS
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      const int64_t b = b0 + 16 * i + n16;
-      const bool live = b < p.B && cn > 0;
-      float x[16];
+      const u32x4_t e = *(const u32x4_t*)&lds_e[(16 * i + n16) * kStepPitch + (4 * kk + g4) * 16];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        float bias = acc[i][e >> 2][e & 3];
-        if constexpr (WBF || BF) bias = bf16_rne(bias);
-        if constexpr (BF) {
-          const uint32_t w = base[i][e >> 3][e >> 1 & 3];
-          x[e] = bf16_rne(((e & 1) ? bf16_hi(w) : bf16_lo(w)) + bias);
+      for (int t = 0; t < 4; ++t) {
+        if constexpr (WBF) {
+          acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, w[t]),
+                                                              __builtin_bit_cast(bf16x8_t, e), acc[i][t], 0, 0, 0);
         } else {
-          x[e] = __uint_as_float(base[i][e >> 2][e & 3]) + bias;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[t][j]), __uint_as_float(e[j]), acc[i][t],
+                                                             0, 0, 0);
         }
       }
-      if (live) {
-        if (seen[i]) {
-          const Penalty pen = penalty_of(p.r, b);
+    }
+  };
+  // W2 runs two steps of the rank ahead of the products, the first of them
+  // ahead of the gather
+  const int whole = (int)(rank / KI);
+  constexpr int SC = KC / KI;  // steps of a chunk
+  u32x4_t ahead[2][4];
+  auto fetch = [&](int s, u32x4_t (&w)[4]) __attribute__((always_inline)) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (seen[i] >> e & 1u) x[e] = pen.apply(x[e], count[i][e >> 2][e & 3]);
-        }
-        if (p.r.bias) {
-          float bias[8];
-          bias8(p.r, b * p.r.bias_stride + c, cn, bias);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] += bias[e];
-          if (cn > 8) {
-            bias8(p.r, b * p.r.bias_stride + c + 8, cn - 8, bias);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[8 + e] += bias[e];
-          }
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = (mask[i] >> e & 1u) ? x[e] : -__builtin_inff();
-        if constexpr (BF) x[e] = bf16_rne(x[e]);
-      }
-      uint64_t best = 0;
-      if (live) {
-        char* const at = (char*)p.out + ((b * p.M + p.k) * V + c) * LB;
-        float half[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) half[e] = x[e];
-        store8<BF>(at, cn, half);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) half[e] = x[8 + e];
-        store8<BF>(at + 8 * LB, cn - 8, half);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (!p.greedy) {
-            const Philox4 q = philox4x32_10((uint32_t)(c >> 2) + (uint32_t)j, p.k_abs,
-                                            (uint32_t)p.batch_offset + (uint32_t)b, 0u, p.seed_lo, p.seed_hi);
-            g[0] = gumbel2_from_word(q.x0);
-            g[1] = gumbel2_from_word(q.x1);
-            g[2] = gumbel2_from_word(q.x2);
-            g[3] = gumbel2_from_word(q.x3);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float sc = p.greedy ? x[4 * j + e] : __builtin_fmaf(x[4 * j + e], p.kappa, g[e]);
-            if (4 * j + e < cn) best = max_u64(best, argmax_key(sc, (uint32_t)(c + 4 * j + e)));
-          }
-        }
-      }
-      best = max_row_lanes(best);
-      if (lane < 16) lds_key[wave][16 * i + lane] = best;
+    for (int t = 0; t < 4; ++t)
+      if (s < whole) w[t] = *(const u32x4_any_t*)(wrow[t] + ((int64_t)s * KI + g4 * KE) * WB);
+  };
+  auto gather = [&](int64_t k0) __attribute__((always_inline)) {
+    __syncthreads();  // the sources are set, and the last chunk is read
+    for (int i = tid; i < 16 * RT * (kStepRowBytes / 16); i += 256) {
+      const int row = i / (kStepRowBytes / 16), q = i % (kStepRowBytes / 16);
+      const int64_t x = lds_src[row];
+      *(u32x4_t*)&lds_e[row * kStepPitch + 16 * q] =
+          x >= 0 ? weights16<WB>((const char*)p.w1 + x * rank * WB, k0 + q * KE, rank) : u32x4_t{0u, 0u, 0u, 0u};
     }
     __syncthreads();
-    if (tid < 16 * RT && b0 + tid < p.B) {
-      const uint64_t a = max_u64(lds_key[0][tid], lds_key[1][tid]), b = max_u64(lds_key[2][tid], lds_key[3][tid]);
-      p.partials[(b0 + tid) * gridDim.x + blockIdx.x] = max_u64(a, b);
+  };
+  fetch(0, ahead[0]);
+  fetch(1, ahead[1]);
+  for (int s = 0; s < whole; s += 2) {
+    if (s % SC == 0) gather((int64_t)s * KI);
+    u32x4_t w[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int t = 0; t < 4; ++t) w[h][t] = ahead[h][t];
+    fetch(s + 2, ahead[0]);
+    fetch(s + 3, ahead[1]);
+    multiply(s % SC, w[0]);
+    if (s + 1 < whole) multiply(s % SC + 1, w[1]);
+  }
+  if ((int64_t)whole * KI < rank) {  // the rest of a rank that is no whole number of steps
+    if (whole % SC == 0) gather((int64_t)whole * KI);
+    u32x4_t w[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) w[t] = weights16<WB>(wrow[t], (int64_t)whole * KI + g4 * KE, rank);
+    multiply(whole % SC, w);
+  }
+  // counts of the columns that stand in the table, a row tile ahead of their use
+  uint32_t count[2][16];
+  auto fetch_counts = [&](int i) __attribute__((always_inline)) {
+    if (i < RT && own_bits(seen[i < RT ? i : 0])) {
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const u32x4_t w = *(const u32x4_any_t*)(p.counts + (b0 + 16 * i + n16) * V + column(4 * e4 / VC) + 4 * e4 % VC);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) count[i & 1][4 * e4 + e] = w[e];
+      }
     }
+  };
+  fetch_counts(0);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t b = b0 + 16 * i + n16;
+    fetch_counts(i + 1);
+    const uint32_t s16 = own_bits(seen[i]), m16 = own_bits(mask[i]);
+    float x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float bias = acc[i][e >> 2][e & 3];
+      if constexpr (WBF || BF) bias = bf16_rne(bias);
+      if constexpr (BF) {
+        const uint32_t w = base[i][e >> 3][e >> 1 & 3];
+        x[e] = bf16_rne(((e & 1) ? bf16_hi(w) : bf16_lo(w)) + bias);
+      } else {
+        x[e] = __uint_as_float(base[i][e >> 2][e & 3]) + bias;
+      }
+    }
+    if (s16) {
+      const Penalty pen = penalty_of(p.r, b);
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (s16 >> e & 1u) x[e] = pen.apply(x[e], count[i & 1][e]);
+    }
+    uint64_t best = 0;
+    if (b < p.B) {
+      if (p.r.bias) {
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+          float bias[8];
+          bias8<VC>(p.r, b * p.r.bias_stride + column(q), have[q], bias);
+#pragma unroll
+          for (int e = 0; e < VC; ++e) x[VC * q + e] += bias[e];
+        }
+      }
+      char* const row = (char*)p.out + (b * p.M + p.k) * V * LB;
+#pragma unroll
+      for (int q = 0; q < NV; ++q) {
+        const int n = have[q];
+        u32x4_t w;
+#pragma unroll
+        for (int e = 0; e < VC; ++e) {
+          float& y = x[VC * q + e];
+          y = (m16 >> (VC * q + e) & 1u) ? y : -__builtin_inff();
+          if constexpr (BF) y = bf16_rne(y);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (BF) w[e] = join_bf16(x[VC * q + 2 * e], x[VC * q + 2 * e + 1]);
+          else w[e] = __float_as_uint(x[VC * q + e]);
+        }
+        char* const at = row + (int64_t)column(q) * LB;
+        if (n == VC) {
+          __builtin_nontemporal_store(w, (u32x4_any_t*)at);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VC; ++e)
+            if (e < n) {
+              if constexpr (BF) ((uint16_t*)at)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+              else ((uint32_t*)at)[e] = w[e];
+            }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // groups of four columns: the words of one noise block
+        const int v = column(4 * j / VC) + 4 * j % VC;
+        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (!p.greedy) {
+          const Philox4 q = philox4x32_10((uint32_t)(v >> 2), p.k_abs, (uint32_t)p.batch_offset + (uint32_t)b, 0u,
+                                          p.seed_lo, p.seed_hi);
+          g[0] = gumbel2_from_word(q.x0);
+          g[1] = gumbel2_from_word(q.x1);
+          g[2] = gumbel2_from_word(q.x2);
+          g[3] = gumbel2_from_word(q.x3);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float sc = p.greedy ? x[4 * j + e] : __builtin_fmaf(x[4 * j + e], p.kappa, g[e]);
+          if (4 * j % VC + e < have[4 * j / VC]) best = max_u64(best, argmax_key(sc, (uint32_t)(v + e)));
+        }
+      }
+    }
+    best = max_row_lanes(best);
+    if (lane < 16) lds_key[wave][16 * i + lane] = best;
+  }
+  __syncthreads();
+  if (tid < 16 * RT && b0 + tid < p.B) {
+    const uint64_t a = max_u64(lds_key[0][tid], lds_key[1][tid]), b = max_u64(lds_key[2][tid], lds_key[3][tid]);
+    p.partials[(b0 + tid) * tiles + tile] = max_u64(a, b);
   }
 }
 
 namespace {
+template <bool WBF, bool BF, int RT>
+hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
+  const int64_t tiles = rule_step_parts(p.V), chunks = (p.B + 16 * RT - 1) / (16 * RT);
+  const int64_t groups = (tiles + 7) / 8 * 8 * chunks;
+  if (groups > 0x7FFFFFFF) return hipErrorNotSupported;
+  hipLaunchKernelGGL((rule_step_kernel<WBF, BF, RT>), dim3((unsigned)groups), dim3(256), 0, s, p, (int)tiles,
+                     (unsigned)chunks);
+  return hipGetLastError();
+}
 template <bool WBF, bool BF>
 hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)rule_step_parts(p.V)), block(256);
-  if (p.B <= 16) hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 1>), grid, block, 0, s, p);
-  else if (p.B <= 32) hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 2>), grid, block, 0, s, p);
-  else hipLaunchKernelGGL((rule_step_kernel<WBF, BF, 4>), grid, block, 0, s, p);
-  return hipGetLastError();
+  if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
+  if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
+  return rule_step_form<WBF, BF, 4>(p, s);
 }
 }  // namespace
 
