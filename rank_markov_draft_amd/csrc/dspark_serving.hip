@@ -54,7 +54,7 @@ int64_t extent(int64_t count, int64_t stride, int64_t len, int64_t size) {
 }
 
 dspark_status_t check_rules(const dspark_logit_rules_t* c, int64_t B, int64_t M, int64_t V, dspark::RuleSet* r,
-                            Ranges* in) {
+                            Ranges* in, int64_t* mask_bytes) {
   if (!c) return DSPARK_ERR_INVALID_ARGUMENT;
   if (c->history && (c->history_len < 0 || (B > 1 && c->history_stride < c->history_len)))
     return DSPARK_ERR_INVALID_ARGUMENT;
@@ -79,6 +79,7 @@ dspark_status_t check_rules(const dspark_logit_rules_t* c, int64_t B, int64_t M,
   in->add(c->presence_penalty, vec);
   in->add(c->logit_bias, (size_t)bias);
   in->add(c->token_mask, (size_t)mask);
+  *mask_bytes = mask;
   *r = dspark::RuleSet{};
   if (c->history && c->history_len > 0) {
     r->history = c->history;
@@ -111,7 +112,8 @@ dspark_status_t run_rules(const void* grad, const void* logits, dspark_dtype_t d
   if (elems == 0) return DSPARK_OK;
   dspark::RulesParams p{};
   Ranges in;
-  const dspark_status_t st = check_rules(rules, B, M, V, &p.r, &in);
+  int64_t mask_bytes = 0;
+  const dspark_status_t st = check_rules(rules, B, M, V, &p.r, &in, &mask_bytes);
   if (st != DSPARK_OK) return st;
   if (!logits || !out || (backward && !grad)) return DSPARK_ERR_INVALID_ARGUMENT;
   const size_t lbytes = (size_t)elems * dtype_bytes(dtype);
@@ -144,7 +146,7 @@ size_t table_bits_bytes(int64_t B, int64_t V) {
   return align256(mul_sz(mul_sz((size_t)B, (size_t)dspark::rule_words(V)), 4));
 }
 size_t table_counts_bytes(int64_t B, int64_t V) {
-  return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 64));  // read in whole vectors of 16 columns
+  return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 128));  // read in whole words of 32 columns
 }
 
 }  // namespace
@@ -269,7 +271,8 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   if (V == 0) return DSPARK_ERR_INVALID_ARGUMENT;  // nothing to draw from
   dspark::RuleStepParams p{};
   Ranges in;
-  st = check_rules(rules, B, M, V, &p.r, &in);
+  int64_t mask_bytes = 0;
+  st = check_rules(rules, B, M, V, &p.r, &in, &mask_bytes);
   if (st != DSPARK_OK) return st;
   if (!base_logits || !first_prev_token_ids || !w1 || !w2 || !sampled_tokens || !processed_logits)
     return DSPARK_ERR_INVALID_ARGUMENT;
@@ -308,7 +311,7 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   p.seen = table ? seen : nullptr;
   p.counts = counts;
   p.partials = (uint64_t*)((char*)workspace + kDataOffset);
-  p.bad_rows = (uint32_t*)workspace;
+  p.bad_rows = &((Control*)workspace)->bad_rows;
   p.B = B;
   p.M = M;
   p.V = V;
@@ -318,6 +321,39 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   p.kappa = p.greedy ? 0.0f : (float)(1.4426950408889634 / temperature);
   p.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
   p.seed_hi = (uint32_t)(seed >> 32);
+  // Greedy drafts with bf16 logits and weights that the persistent chain can
+  // hold run as one launch (per-request biases do not fit in its LDS).
+  const int cus = device_cus();
+  if (p.greedy && cus > 0 && tile_path(logits_dtype, weight_dtype, V, r, base_logits, processed_logits, w1, w2) &&
+      B <= dspark::chain_max_rows() && M <= kChainMaxSteps && (V + 31) / 32 <= (int64_t)cus * dspark::chain_waves_per_group() &&
+      (p.r.bias == nullptr || p.r.bias_stride == 0)) {
+    Control* const ctl = (Control*)workspace;
+    dspark::ChainParams c{};
+    c.base = base_logits;
+    c.out = processed_logits;
+    c.first_prev = first_prev_token_ids;
+    c.tokens = sampled_tokens;
+    c.w1 = (const uint16_t*)w1;
+    c.w2 = (const uint16_t*)w2;
+    c.sync = (uint32_t*)((char*)workspace + kControlBytes);
+    c.keys = (uint64_t*)((char*)c.sync + dspark::kChainSyncBytes);
+    c.bad_rows = &ctl->bad_rows;
+    c.sync_failures = &ctl->sync_failures;
+    c.test_hook = &ctl->chain_test_hook;
+    c.B = B;
+    c.M = M;
+    c.V = V;
+    c.r = r;
+    c.S = (V + 31) / 32;
+    c.rules = true;
+    c.rule_set = p.r;
+    c.seen = p.seen;
+    c.counts = counts;
+    c.mask_bytes = mask_bytes;
+    e = dspark::launch_chain_greedy(c, cus, s);
+    if (e == hipSuccess) return DSPARK_OK;
+    (void)hipGetLastError();  // not launchable here: a launch per position
+  }
   for (int64_t k = 0; k < M; ++k) {
     p.k = k;
     p.k_abs = (uint32_t)(position_offset + k);

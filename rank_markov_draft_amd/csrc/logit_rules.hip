@@ -21,28 +21,13 @@
 // per tile of the vocabulary, from L2; nothing is sorted or written to memory.
 #include "device_common.h"
 #include "logit_rules.h"
+#include "logit_rules_device.h"
 
 namespace dspark {
 
 namespace {
 
 constexpr int kRuleThreads = 256;
-
-// A request's penalties; a rule that is off leaves x as it is.
-struct Penalty {
-  float repetition, frequency, presence;
-  bool repeat, count;
-  __device__ __forceinline__ float apply(float x, uint32_t c) const {
-    if (repeat) x = x > 0.0f ? x / repetition : x * repetition;
-    if (count && c > 0u) x = x - (frequency * (float)c + presence);
-    return x;
-  }
-};
-__device__ __forceinline__ Penalty penalty_of(const RuleSet& r, int64_t b) {
-  return Penalty{r.repetition ? r.repetition[b] : 1.0f, r.frequency ? r.frequency[b] : 0.0f,
-                 r.presence ? r.presence[b] : 0.0f, r.repetition != nullptr,
-                 r.frequency != nullptr || r.presence != nullptr};
-}
 
 // Adds the ids of request b that lie in [t0, t0 + tn) to a tile's table:
 // every counted id to the bitmap, those past the prompt to the counts (null:
@@ -709,8 +694,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_
   __syncthreads();
   if (tid == 0) {
     for (int w = 0; w < kRuleThreads / 64; ++w) best = max_u64(best, lds_key[w]);
-    const uint32_t lowest = 0x007FFFFFu;  // the code of -inf: nothing was left to draw
-    const int64_t t = (uint32_t)(best >> 32) > lowest ? key_index(best) : -1;
+    const int64_t t = (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
     tokens[b * M + k] = t;
     if (seen && t >= 0) {
       uint32_t* const w = seen + b * ((V + 31) / 32) + (t >> 5);

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "logit_rules.h"
+
 namespace dspark {
 
 // Rank blocks (of 16) the tile kernel is instantiated for, covering r; 0 if none.
@@ -37,6 +39,14 @@ struct ChainParams {
   int64_t r;
   int64_t S;                  // 32-column vocabulary slices
   bool lf32;                  // fp32 logits (bf16 weights either way)
+  // Under logit rules (bf16 logits; one bias row for all requests or none):
+  // each position is selected from the processed corrected logits, which
+  // `out` receives.
+  bool rules;
+  RuleSet rule_set;
+  const uint32_t* seen;       // the history's table (logit_rules.h), or null: no penalty
+  uint32_t* counts;           // its counts; those that outgrow a byte are kept up to date
+  int64_t mask_bytes;         // extent of rule_set.mask
 };
 
 // Arguments of the persistent temperature chain (bf16): keys holds one

@@ -45,10 +45,20 @@
 // tokens.  A
 // launch that finds the failure count already nonzero (a failure nobody has
 // read back and cleared) does no work and also returns -1 tokens.
+//
+// With RULES the values are selected after the logit rules (penalties, a
+// shared bias, masks; bf16 logits): the lane that adds a column's bias also
+// penalises and masks it, so the rules cost no pass over the logits.  The
+// counts of the workgroup's 512 columns stay in LDS for the whole call, a byte
+// each (0: the token was not seen, n: n - 1 times among the outputs, 255: look
+// it up in memory); a row's drawn token joins them in the workgroup that owns
+// its column when the tokens are merged, a window before they are needed.  The
+// mask words of a group's next step are staged with its base rows.
 #include <type_traits>
 
 #include "chain_common.h"
 #include "device_common.h"
+#include "logit_rules_device.h"
 #include "markov_chain.h"
 
 namespace dspark {
@@ -93,8 +103,9 @@ __device__ __forceinline__ uint32_t argmax_code_bf16(uint32_t h) {
 
 }  // namespace
 
-template <int K32, bool LF32>
+template <int K32, bool LF32, bool RULES>
 __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams p) {
+  static_assert(!(LF32 && RULES), "the counts and fp32 rows do not fit in LDS together");
   // bf16 or (LF32) fp32 logits: bytes per logit, 1 KB segments of a staged
   // row of 512 columns, LDS bytes of a staged row
   constexpr int kEl = LF32 ? 4 : 2;
@@ -117,6 +128,13 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   __shared__ __attribute__((aligned(16))) unsigned char lds_kv[2][2 * 1024];
   __shared__ __attribute__((aligned(16))) unsigned char lds_poll[64 * 16];  // polled counter lines
   __shared__ int lds_flag;
+  // Rules: counts and biases of the workgroup's columns, mask words of each
+  // group's staged rows, and each row's penalties.
+  constexpr int kCols = 32 * kWaves;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_n[RULES ? kMaxRows * kCols : 16];
+  __shared__ __attribute__((aligned(16))) float lds_bias[RULES ? kCols : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds_mask[RULES ? kMaxGroups * kGroupRows * kWaves : 4];
+  __shared__ float lds_pen[RULES ? kMaxRows * 3 : 1];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar branches
@@ -212,6 +230,22 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
     load_row_lds(gg, kd + 1, row);
   };
 
+  // Rules: mask words of group gg's step kd, four rows of 16 words each by
+  // waves 4 .. 7.
+  const bool penalise = RULES && p.seen != nullptr;
+  const bool mask_wave = RULES && p.rule_set.mask != nullptr && wave >= 4 && wave < 8;
+  BufferWords bw_mask{};
+  if constexpr (RULES) bw_mask = buffer_words(p.rule_set.mask, p.rule_set.mask != nullptr ? (uint32_t)p.mask_bytes : 0u);
+  auto load_mask = [&](int gg, int kd) __attribute__((always_inline)) {
+    if constexpr (RULES) {
+      const int row = 4 * (wave - 4) + (lane >> 4), word = (int)(vbeg / 32u) + (lane & 15), b = gg * rpg + row;
+      const bool ok = row < rpg && b < B && kd < M && word < (V + 31) / 32;
+      const uint32_t off = 4u * ((uint32_t)b * (uint32_t)p.rule_set.mask_stride_b + (uint32_t)kd * (uint32_t)p.rule_set.mask_stride_m +
+                                 (uint32_t)word);
+      load_lds4(bw_mask, ok ? off : kBufferOob, lds_address(&lds_mask[gg * kGroupRows * kWaves + 64 * (wave - 4)]));
+    }
+  };
+
   // ---- gather: W1 rows of tokens x (lane l: the token of row l % 16 of the
   // unit's group, or -1 for a zero row) into lds_e[buf].
   auto gather = [&](int buf, int x) __attribute__((always_inline)) {
@@ -237,8 +271,17 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
     for (int i = 0; i < 8; ++i) merged = max_u64(merged, kv[i]);
     const int b = gg * rpg + n16;
     const bool row_ok = n16 < rpg && b < B;
-    const int64_t t = key_index(merged);
+    const int64_t t = !RULES || (uint32_t)(merged >> 32) > kNothingLeft16 ? key_index(merged) : -1;
     if (g == 0 && g4 == 0 && row_ok) p.tokens[(uint32_t)(b * M + kt)] = t;
+    if constexpr (RULES) {
+      if (penalise && g4 == 0 && row_ok && t >= (int64_t)vbeg && t < (int64_t)vend) {
+        uint8_t& n = lds_n[b * kCols + (int)(t - vbeg)];
+        uint32_t* const big = p.counts + (int64_t)b * V + t;
+        if (n == 255) __hip_atomic_fetch_add(big, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        else if (n == 254) __hip_atomic_store(big, 254u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        n = n == 0 ? 2 : n < 255 ? n + 1 : 255;
+      }
+    }
     return (row_ok && t >= 0 && t < V) ? (int)t : -1;
   };
   // Key slots of group gg's step kt into lds_kv[buf].
@@ -272,6 +315,39 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   for (int gg = 0; gg < NR; ++gg) {
     if (nbulk >= 1) load_row_lds(gg, 0, brow0);
     if (nbulk >= 2) load_row_lds(gg, 0, brow1);
+    if (mask_wave) load_mask(gg, 0);
+  }
+  if constexpr (RULES) {
+    // a thread a word of the table: 32 columns of a row
+    static_assert(kMaxRows * kWaves == kThreads, "one table word per thread");
+    for (int i = tid; i < kMaxRows * kCols / 16; i += kThreads) *(u32x4_t*)&lds_n[16 * i] = u32x4_t{0u, 0u, 0u, 0u};
+    if (tid < B) {
+      lds_pen[3 * tid] = p.rule_set.repetition ? p.rule_set.repetition[tid] : 1.0f;
+      lds_pen[3 * tid + 1] = p.rule_set.frequency ? p.rule_set.frequency[tid] : 0.0f;
+      lds_pen[3 * tid + 2] = p.rule_set.presence ? p.rule_set.presence[tid] : 0.0f;
+    }
+    if (tid < kCols) {
+      const uint32_t v = vbeg + (uint32_t)tid;
+      lds_bias[tid] = p.rule_set.bias == nullptr || v >= vend ? 0.0f
+                      : p.rule_set.bias_bf16                  ? bf16_lo(((const uint16_t*)p.rule_set.bias)[v])
+                                                       : ((const float*)p.rule_set.bias)[v];
+    }
+    lds_barrier();
+    const int b = tid / kWaves, word = (int)(vbeg / 32u) + tid % kWaves;
+    if (penalise && b < B && word < (V + 31) / 32 && 32u * (uint32_t)word < vend) {
+      const uint32_t bits = p.seen[b * ((V + 31) / 32) + word];
+      if (bits) {
+        u32x4_t c[8];  // a row's last word reads up to 31 counts past it (the table's end is padded)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) c[q] = *(const u32x4_t*)(p.counts + (int64_t)b * V + 32 * word + 4 * q);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (bits >> i & 1u) {
+            const uint32_t n = c[i >> 2][i & 3];
+            lds_n[b * kCols + 32 * (tid % kWaves) + i] = (uint8_t)(n < 254u ? n + 1u : 255u);
+          }
+      }
+    }
   }
   if (wave == 1 && !poisoned) {
     for (int gg = 0; gg < (LF32 ? (NR < 2 ? NR : 2) : NR); ++gg) gather(ebuf(gg), first_token(gg));
@@ -352,6 +428,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
       const int gp = (w - 1) % kSlots, kp = (w - 1) / kSlots;
       if (nbulk >= 1) flush_row(gp, kp, brow0);
       if (nbulk >= 2) flush_row(gp, kp, brow1);
+      if (mask_wave) load_mask(gp, kp + 1);
     }
 
     if (role_a) {
@@ -435,12 +512,55 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
           const float hi = bf16_hi(xw[q]) + bf16_hi(bw[q]);
           ow[q] = pack_bf16x2(lo, hi);
           __asm__("" : "+v"(ow[q]));  // keep the packed word (else the codes below repack it)
+          if constexpr (RULES) continue;
           sum += lo + hi;
           // order codes of both values at once; key = code << 16 | (0xFFFF - column)
           const uint32_t c2 = pair_order_codes(ow[q]);
           const uint32_t klo = (c2 << 16) | (0xFFFFu - (uint32_t)(colw + 2 * q));
           const uint32_t khi = (c2 & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(colw + 2 * q + 1));
           key = max(key, max(klo, khi));
+        }
+        if constexpr (RULES) {
+          // the rules on the lane's 8 corrected values, then their keys
+          const int b = gc * rpg + n16;
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = (i & 1) ? bf16_hi(ow[i >> 1]) : bf16_lo(ow[i >> 1]);
+          const uint64_t n8 = *(const uint64_t*)&lds_n[b * kCols + colw];
+          if (n8 != 0) {
+            const Penalty pen{lds_pen[3 * b], lds_pen[3 * b + 1], lds_pen[3 * b + 2], p.rule_set.repetition != nullptr,
+                              p.rule_set.frequency != nullptr || p.rule_set.presence != nullptr};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t n = (uint32_t)(n8 >> (8 * i)) & 255u;
+              if (n != 0) {
+                uint32_t c = n - 1u;
+                if (n == 255u)
+                  c = __hip_atomic_load(p.counts + (int64_t)b * V + vbeg + colw + i, __ATOMIC_RELAXED,
+                                        __HIP_MEMORY_SCOPE_AGENT);
+                x[i] = pen.apply(x[i], c);
+              }
+            }
+          }
+          if (p.rule_set.bias != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] += lds_bias[colw + i];
+          }
+          if (p.rule_set.mask != nullptr) {
+            const uint32_t m8 = ((const uint8_t*)&lds_mask[gc * kGroupRows * kWaves + n16 * kWaves])[colw >> 3];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = (m8 >> i & 1u) ? x[i] : -__builtin_inff();
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            ow[q] = pack_bf16x2(x[2 * q], x[2 * q + 1]);
+            __asm__("" : "+v"(ow[q]));
+            sum += x[2 * q] + x[2 * q + 1];
+            const uint32_t c2 = pair_order_codes(ow[q]);
+            const uint32_t klo = (c2 << 16) | (0xFFFFu - (uint32_t)(colw + 2 * q));
+            const uint32_t khi = (c2 & 0xFFFF0000u) | (0xFFFFu - (uint32_t)(colw + 2 * q + 1));
+            key = max(key, max(klo, khi));
+          }
         }
         *(u32x4_t*)xp = u32x4_t{ow[0], ow[1], ow[2], ow[3]};
         // The plain order codes rank -0 below +0 and order NaNs by payload.
@@ -487,7 +607,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
     // since then issued a store and a load per row.
     if (nbulk > 0 && w + 1 < U && w + 1 >= kSlots && real(w + 1)) {
       int later = 0;
-      for (int x = w - kSlots + 3; x <= w; ++x) later += (x >= 1 && real(x - 1)) ? 2 * kSegs * nbulk : 0;
+      for (int x = w - kSlots + 3; x <= w; ++x) later += (x >= 1 && real(x - 1)) ? 2 * kSegs * nbulk + (mask_wave ? 1 : 0) : 0;
       wait_vmcnt_upto16(later);
     }
     lds_barrier();
@@ -534,7 +654,9 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
                                  : 0;
       const uint64_t best = max_u64(k0, k1);
       const uint64_t merged = max_row_lanes(best);
-      if (g4 == 0 && row_ok) p.tokens[(uint32_t)(b * M + M - 1)] = key_index(merged);
+      if (g4 == 0 && row_ok)
+        p.tokens[(uint32_t)(b * M + M - 1)] =
+            !RULES || (uint32_t)(merged >> 32) > kNothingLeft16 ? key_index(merged) : -1;
     }
     lds_barrier();  // the last keys are read before they are cleared
     for (int i = tid; i < M * kGroups * kMaxRows; i += kThreads)
@@ -557,9 +679,9 @@ namespace {
 // workgroup still cannot start while the others wait (CUs held by other
 // streams' kernels), their bounded waits end the launch with a recorded
 // synchronisation failure and -1 tokens instead of a hang.
-// Workgroups of markov_chain_greedy_bf16<K32, LF32> one CU of the current
+// Workgroups of markov_chain_greedy_bf16<K32, LF32, RULES> one CU of the current
 // device can hold, cached per device; the chain needs at least one.
-template <int K32, bool LF32>
+template <int K32, bool LF32, bool RULES>
 int chain_occupancy() {
   static int cache[64];
   static bool known[64];
@@ -567,7 +689,7 @@ int chain_occupancy() {
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
   if (!known[dev]) {
     int blocks = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, markov_chain_greedy_bf16<K32, LF32>, kThreads, 0) !=
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, markov_chain_greedy_bf16<K32, LF32, RULES>, kThreads, 0) !=
         hipSuccess)
       blocks = 0;
     cache[dev] = blocks;
@@ -576,16 +698,18 @@ int chain_occupancy() {
   return cache[dev];
 }
 
+template <int K32, bool LF32, bool RULES>
+hipError_t launch_chain_form(const ChainParams& p, int grid, hipStream_t s) {
+  if (chain_occupancy<K32, LF32, RULES>() < 1) return hipErrorNotSupported;
+  hipLaunchKernelGGL((markov_chain_greedy_bf16<K32, LF32, RULES>), dim3(grid), dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
 template <int K32>
 hipError_t launch_chain_k(const ChainParams& p, int grid, hipStream_t s) {
-  if (p.lf32) {
-    if (chain_occupancy<K32, true>() < 1) return hipErrorNotSupported;
-    hipLaunchKernelGGL((markov_chain_greedy_bf16<K32, true>), dim3(grid), dim3(kThreads), 0, s, p);
-  } else {
-    if (chain_occupancy<K32, false>() < 1) return hipErrorNotSupported;
-    hipLaunchKernelGGL((markov_chain_greedy_bf16<K32, false>), dim3(grid), dim3(kThreads), 0, s, p);
-  }
-  return hipGetLastError();
+  if (p.rules) return launch_chain_form<K32, false, true>(p, grid, s);
+  if (p.lf32) return launch_chain_form<K32, true, false>(p, grid, s);
+  return launch_chain_form<K32, false, false>(p, grid, s);
 }
 
 }  // namespace
@@ -601,6 +725,9 @@ hipError_t launch_chain_greedy(const ChainParams& p, int num_cus, hipStream_t s)
   if (p.B * p.M * p.V * (p.lf32 ? 4 : 2) >= ((int64_t)1 << 31)) return hipErrorNotSupported;  // byte offsets below 2^31
   if (p.M > 4096) return hipErrorNotSupported;                              // key area below 2^31 bytes
   if (p.S > (int64_t)num_cus * kWaves) return hipErrorNotSupported;
+  // rules: bf16 logits, one bias row for all, mask offsets below 2^31
+  if (p.rules && (p.lf32 || (p.rule_set.bias != nullptr && p.rule_set.bias_stride != 0) || p.mask_bytes >= ((int64_t)1 << 31)))
+    return hipErrorNotSupported;
   switch (ks) {  // rank blocks of 16 -> blocks of 32 (zero-padded)
     case 1:
     case 2: return launch_chain_k<1>(p, num_cus, s);

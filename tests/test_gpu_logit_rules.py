@@ -496,3 +496,58 @@ def test_rules_past_31_bits(native):
     assert torch.equal(out[-1:], last) and not torch.equal(last, x[-1:])
     back = rmd.process_block_logits_backward(x, x, history=hist, repetition_penalty=rep, out=out.copy_(x))
     assert torch.equal(back[-1:], rmd.process_block_logits_backward(x[-1:], x[-1:], history=hist[-1:], repetition_penalty=rep[-1:]))
+
+
+@pytest.mark.parametrize("B,M,V,L,r,bias,mask", [
+    (64, 5, 8200, 300, 256, "shared", "each"), (17, 3, 16384, 100, 64, "none", "row"), (64, 2, 131064, 40, 16, "none", "none"),
+    (33, 16, 520, 60, 32, "shared", "shared"), (5, 4, 40, 9, 8, "none", "each"), (48, 3, 4096, -1, 128, "none", "each")])
+def test_greedy_chain_under_rules(native, B, M, V, L, r, bias, mask):
+    """Shapes of the persistent greedy chain, and the same draft by steps (as
+    fp32 logits would go): its rows and tokens hold by themselves."""
+    c = _draft_case(B, M, V, L, r, BF16, BF16, bias=bias, mask=mask, bias_dtype=(F32, BF16)[B % 2])
+    ws = rmd.Workspace(B, M, V, r, sample=True, processed=True)
+    tok, rows = _draft(c, workspace=ws)
+    _check_draft(c, tok, rows)
+    again = _draft(c, workspace=ws)                  # the chain leaves the workspace ready
+    assert torch.equal(tok, again[0]) and torch.equal(rows, again[1])
+    assert rmd.read_device_error(ws) == 0
+
+
+def test_greedy_chain_counts_past_a_byte(native):
+    """Counts around 254, where the chain's byte ends, and tokens drawn at that edge."""
+    B, M, V = 4, 6, 512
+    c = _draft_case(B, M, V, 1200, 8, BF16, BF16, mask="none", bias="none")
+    c.w1.zero_()
+    c.logits.zero_()
+    c.logits[:, :, 77] = 200.0                       # drawn whatever its penalties
+    c.rep[:] = 1.0
+    c.freq[:] = [0.25, 0.125, 0.0625, 0.5]
+    c.pres[:] = 0.5
+    c.history[:] = 5
+    for b, n in enumerate((251, 253, 254, 255)):
+        c.history[b, :n] = 77
+        c.history[b, n:2 * n + 1] = 78
+    c.lengths[:], c.prompt[:] = 1200, [0, 1, 0, 0]
+    ws = rmd.Workspace(B, M, V, 8, sample=True, processed=True)
+    tok, rows = _draft(c, workspace=ws)
+    assert (tok == 77).all()
+    _check_draft(c, tok, rows)
+    again = _draft(c, workspace=ws)
+    assert torch.equal(rows, again[1])
+
+
+def test_greedy_chain_failure_is_reported(native):
+    """A chain whose workgroups do not meet (forced through the workspace's
+    hook) gives -1 tokens until the record is read; then it runs again."""
+    from rank_markov_draft_amd import _lib
+    c = _draft_case(4, 5, 4096, 20, 64, BF16, BF16, mask="none", bias="none")
+    ws = rmd.Workspace(4, 5, 4096, 64, sample=True, processed=True)
+    want = _draft(c, workspace=ws)
+    ws.set_chain_test_hook(True)
+    assert (_draft(c, workspace=ws)[0] == -1).all()
+    ws.set_chain_test_hook(False)
+    assert (_draft(c, workspace=ws)[0] == -1).all()
+    with pytest.raises(_lib.DsparkError, match="DEVICE"):
+        rmd.read_device_error(ws)
+    again = _draft(c, workspace=ws)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
