@@ -316,29 +316,34 @@ hipError_t launch_logit_rules(const RulesParams& p, bool logits_bf16, int num_cu
 
 // ---------------------------------------------------------------- left to right
 namespace {
-constexpr int kTableCols = 8192;  // columns of a workgroup's tile of the table
+constexpr int kTableCols = 4096;  // columns of a workgroup's tile of the table
 }
 
 // The table of a request's history: as above by tiles through LDS, written
 // out once.  Counts are written where the bit is set and read only there.
 __global__ __launch_bounds__(kRuleThreads) void rule_table_kernel(TableParams p, int tiles) {
   __shared__ uint32_t seen[kTableCols / 32];
-  __shared__ uint32_t counts[kTableCols];
+  __shared__ __attribute__((aligned(16))) uint32_t counts[kTableCols];
   const int64_t b = blockIdx.x / (unsigned)tiles;
   const int64_t t0 = (int64_t)(blockIdx.x % (unsigned)tiles) * kTableCols;
   const int tn = (int)(p.V - t0 < kTableCols ? p.V - t0 : kTableCols);
   const int tid = threadIdx.x;
   for (int i = tid; i < kTableCols / 32; i += kRuleThreads) seen[i] = 0u;
-  for (int i = tid; i < kTableCols; i += kRuleThreads) counts[i] = 0u;
+  for (int i = tid; i < kTableCols / 4; i += kRuleThreads) *(u32x4_t*)&counts[4 * i] = u32x4_t{0u, 0u, 0u, 0u};
   __syncthreads();
   count_history(p.r, b, t0, tn, seen, counts);
   __syncthreads();
   const int64_t W = (p.V + 31) / 32;
   uint32_t* const gs = p.seen + b * W + t0 / 32;
   uint32_t* const gc = p.counts + b * p.V + t0;
-  for (int i = tid; i < (tn + 31) / 32; i += kRuleThreads) gs[i] = seen[i];
-  for (int i = tid; i < tn; i += kRuleThreads)
-    if (seen[i >> 5] >> (i & 31) & 1u) gc[i] = counts[i];
+  for (int i = tid; i < (tn + 31) / 32; i += kRuleThreads) {
+    uint32_t bits = seen[i];
+    gs[i] = bits;
+    for (; bits; bits &= bits - 1u) {
+      const int c = 32 * i + __builtin_ctz(bits);
+      gc[c] = counts[c];
+    }
+  }
 }
 
 hipError_t launch_rule_table(const TableParams& p, hipStream_t s) {

@@ -23,6 +23,31 @@ __device__ __forceinline__ Penalty penalty_of(const RuleSet& r, int64_t b) {
                  r.frequency != nullptr || r.presence != nullptr};
 }
 
+// The same for eight values whose counts stand in a word of bytes (0: not
+// seen, n: n - 1 times among the outputs), without a branch: some of them were
+// seen.  The quotient is the product with the rounded reciprocal and one
+// correction of its residue, which rounds as a division does; the fixup puts
+// in what a division gives for infinities, NaN and zeros.
+__device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p) {
+  const float inv = 1.0f / p.repetition;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float n = (float)((uint32_t)(n8 >> (8 * i)) & 255u);
+    float y = x[i];
+    if (p.repeat) {
+      const float q = y * inv;
+      const float d = __builtin_amdgcn_div_fixupf(__builtin_fmaf(__builtin_fmaf(-q, p.repetition, y), inv, q), p.repetition, y);
+      y = y > 0.0f ? d : y * p.repetition;
+      y = n > 0.0f ? y : x[i];
+    }
+    if (p.count) {
+      const float off = p.frequency * (n - 1.0f) + p.presence;
+      y = n > 1.0f ? y - off : y;
+    }
+    x[i] = y;
+  }
+}
+
 // A processed score's order codes (16 bits for bf16 values, 32 for fp32) up to
 // these are -inf: nothing was left to draw.
 constexpr uint32_t kNothingLeft16 = 0x007Fu;

@@ -530,16 +530,20 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
           if (n8 != 0) {
             const Penalty pen{lds_pen[3 * b], lds_pen[3 * b + 1], lds_pen[3 * b + 2], p.rule_set.repetition != nullptr,
                               p.rule_set.frequency != nullptr || p.rule_set.presence != nullptr};
+            // a byte of 255 (bit 0 of a byte is left where all eight were set): that count is in memory
+            uint64_t full = n8 & (n8 >> 4);
+            full &= full >> 2;
+            if (full & (full >> 1) & 0x0101010101010101ull) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t n = (uint32_t)(n8 >> (8 * i)) & 255u;
-              if (n != 0) {
-                uint32_t c = n - 1u;
-                if (n == 255u)
-                  c = __hip_atomic_load(p.counts + (int64_t)b * V + vbeg + colw + i, __ATOMIC_RELAXED,
-                                        __HIP_MEMORY_SCOPE_AGENT);
-                x[i] = pen.apply(x[i], c);
+              for (int i = 0; i < 8; ++i) {
+                const uint32_t n = (uint32_t)(n8 >> (8 * i)) & 255u;
+                if (n != 0)
+                  x[i] = pen.apply(x[i], n < 255u ? n - 1u
+                                                  : __hip_atomic_load(p.counts + (int64_t)b * V + vbeg + colw + i,
+                                                                      __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
               }
+            } else {
+              penalise8(x, n8, pen);
             }
           }
           if (p.rule_set.bias != nullptr) {
