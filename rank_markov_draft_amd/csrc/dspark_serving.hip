@@ -354,11 +354,24 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
     if (e == hipSuccess) return DSPARK_OK;
     (void)hipGetLastError();  // not launchable here: a launch per position
   }
+  // Up to 8 rows the last workgroup of a step draws the tokens itself, by keys
+  // and a counter in the chain's area (zero between launches): 8 rows at V =
+  // 32000 56 us a draft of five, 62 us with a second launch a step.  More rows
+  // would meet in the same few lines of memory: 64 rows at V = 129280 211 us,
+  // 197 us with the second launch.
+  if (B <= 8) {
+    p.arrived = (uint32_t*)((char*)workspace + kControlBytes + dspark::kChainSyncBytes);
+    p.keys = (uint64_t*)(p.arrived + 64);
+    p.tokens_out = sampled_tokens;
+    p.seen_out = table ? seen : nullptr;
+    p.counts_out = counts;
+  }
   for (int64_t k = 0; k < M; ++k) {
     p.k = k;
     p.k_abs = (uint32_t)(position_offset + k);
     e = dspark::launch_rule_step(p, logits_dtype == DSPARK_BF16, weight_dtype == DSPARK_BF16, s);
     if (e != hipSuccess) return device_failure(e, "rule step launch");
+    if (p.keys) continue;
     e = dspark::launch_rule_choose(p.partials, dspark::rule_step_parts(V), B, M, k, V, sampled_tokens,
                                    table ? seen : nullptr, counts, s);
     if (e != hipSuccess) return device_failure(e, "token choice launch");

@@ -71,7 +71,14 @@ struct RuleStepParams {
   const void* w2;          // [V, rank]
   const uint32_t* seen;    // table, or null (no penalty)
   const uint32_t* counts;  // readable 64 bytes past its end
-  uint64_t* partials;      // [B, rule_step_parts(V)]
+  uint64_t* partials;      // [B, rule_step_parts(V)]: read by launch_rule_choose (keys null)
+  // or: the last workgroup of a row chunk to finish draws its tokens itself.
+  // Zero before the launch, left zero.
+  uint64_t* keys;          // [B]
+  uint32_t* arrived;       // one word (keys: B at most 16)
+  int64_t* tokens_out;     // [B, M] (the same as tokens)
+  uint32_t* seen_out;      // (the same as seen)
+  uint32_t* counts_out;    // (the same as counts)
   uint32_t* bad_rows;
   int64_t B;
   int64_t M;

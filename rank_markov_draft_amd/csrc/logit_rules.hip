@@ -359,6 +359,21 @@ constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
 constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
 constexpr int kStepPitch = kStepRowBytes + 16;       // its pitch in LDS
 
+// The token of row b from its best key, -1 when that is -inf; it joins the
+// row's table, which nobody else touches now, with a count of its own when its
+// bit was clear.
+__device__ __forceinline__ void draw_token(uint64_t best, int64_t b, int64_t M, int64_t k, int64_t V, int64_t* tokens,
+                                           uint32_t* seen, uint32_t* counts) {
+  const int64_t t = (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
+  tokens[b * M + k] = t;
+  if (seen && t >= 0) {
+    uint32_t* const w = seen + b * ((V + 31) / 32) + (t >> 5);
+    const uint32_t bit = 1u << (t & 31);
+    counts[b * V + t] = (*w & bit) ? counts[b * V + t] + 1u : 1u;
+    *w |= bit;
+  }
+}
+
 // 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
 template <int EB>
 __device__ __forceinline__ u32x4_t weights16(const char* row, int64_t k, int64_t rank) {
@@ -653,9 +668,29 @@ __global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_
     if (lane < 16) lds_key[wave][16 * i + lane] = best;
   }
   __syncthreads();
-  if (tid < 16 * RT && b0 + tid < p.B) {
-    const uint64_t a = max_u64(lds_key[0][tid], lds_key[1][tid]), b = max_u64(lds_key[2][tid], lds_key[3][tid]);
-    p.partials[(b0 + tid) * tiles + tile] = max_u64(a, b);
+  const bool row_ok = tid < 16 * RT && b0 + tid < p.B;
+  uint64_t best = 0;
+  if (row_ok) best = max_u64(max_u64(lds_key[0][tid], lds_key[1][tid]), max_u64(lds_key[2][tid], lds_key[3][tid]));
+  if (p.keys == nullptr) {
+    if (row_ok) p.partials[(b0 + tid) * tiles + tile] = best;
+    return;
+  }
+  // One row chunk: its keys meet in memory; whoever counts in last draws the tokens.
+  // Nobody waits: the first wave's own maxima are done before it counts in, all
+  // by device-scope atomics.
+  if (wave == 0) {
+    if (row_ok) __hip_atomic_fetch_max(p.keys + b0 + tid, best, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    uint32_t ticket = 0;
+    if (lane == 0) ticket = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(ticket) != (uint32_t)tiles - 1u) return;
+    __asm__ volatile("" ::: "memory");
+    if (row_ok) {
+      best = __hip_atomic_load(p.keys + b0 + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(p.keys + b0 + tid, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      draw_token(best, b0 + tid, p.M, p.k, V, p.tokens_out, p.seen_out, p.counts_out);
+    }
+    if (lane == 0) __hip_atomic_store(p.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 }
 
@@ -671,6 +706,7 @@ hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
 }
 template <bool WBF, bool BF>
 hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
+  if (p.keys != nullptr && p.B > 16) return hipErrorInvalidValue;  // one row chunk, one counter
   if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
   if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
   return rule_step_form<WBF, BF, 4>(p, s);
@@ -682,9 +718,7 @@ hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weig
   return logits_bf16 ? rule_step_go<false, true>(p, s) : rule_step_go<false, false>(p, s);
 }
 
-// One workgroup per row.  The row's table belongs to this workgroup alone, so
-// the drawn token joins it without atomics; its count starts here when its
-// bit was clear.
+// One workgroup per row.
 __global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_t* __restrict__ partials,
                                                                    int64_t nparts, int64_t M, int64_t k, int64_t V,
                                                                    int64_t* __restrict__ tokens, uint32_t* seen,
@@ -699,15 +733,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_
   __syncthreads();
   if (tid == 0) {
     for (int w = 0; w < kRuleThreads / 64; ++w) best = max_u64(best, lds_key[w]);
-    const int64_t t = (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
-    tokens[b * M + k] = t;
-    if (seen && t >= 0) {
-      uint32_t* const w = seen + b * ((V + 31) / 32) + (t >> 5);
-      const uint32_t bit = 1u << (t & 31);
-      const bool was = (*w & bit) != 0u;
-      counts[b * V + t] = was ? counts[b * V + t] + 1u : 1u;
-      *w |= bit;
-    }
+    draw_token(best, b, M, k, V, tokens, seen, counts);
   }
 }
 

@@ -551,3 +551,20 @@ def test_greedy_chain_failure_is_reported(native):
         rmd.read_device_error(ws)
     again = _draft(c, workspace=ws)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def test_draft_of_more_rows_than_the_keys_hold(native):
+    """70000 requests: their best keys do not fit beside the counters, so a
+    second launch reduces them; the same rows in smaller calls are the same."""
+    B, V, r = 70000, 40, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    base = torch.randn(B, 2, V, device="cuda", generator=g)
+    w1, w2 = (torch.randn(V, r, device="cuda", generator=g) * 0.1 for _ in range(2))
+    first = torch.randint(0, V, (B,), device="cuda", generator=g)
+    hist = torch.randint(0, V, (B, 5), device="cuda", generator=g)
+    rep = 1.0 + torch.rand(B, device="cuda", generator=g)
+    tok, rows = rmd.sample_block_tokens_processed(base, first, w1, w2, 0.6, history=hist, repetition_penalty=rep, seed=8)
+    for a, b in ((0, 300), (35000, 36000), (69000, 70000)):
+        t, x = rmd.sample_block_tokens_processed(base[a:b], first[a:b], w1, w2, 0.6, history=hist[a:b],
+                                                 repetition_penalty=rep[a:b], seed=8, batch_offset=a)
+        assert torch.equal(t, tok[a:b]) and torch.equal(x, rows[a:b])
