@@ -31,20 +31,23 @@ __device__ __forceinline__ uint32_t quantize1(float x, float s, bool ok) {
 __device__ __forceinline__ bool usable(float s) { return s > 0.0f && s < __builtin_inff(); }
 
 // Four integers of a row whose scale lies well inside the normal range.  The
-// quotient is x times the rounded reciprocal, corrected once by its residue,
-// which gives the division's own rounding (the residue is exact in a fused
-// product; a quotient small enough for it to underflow rounds to zero anyway);
-// at most 127 (1 + 2^-23) by the scale's own rounding.  Adding 1.5 * 2^23
-// rounds to an integer, ties to even, in the sum's low bits.  A quarter of a
-// division's instructions: the head's bf16 rows were bound by them.
+// quotient is x times the rounded reciprocal, corrected by its residue (exact
+// in a fused product) twice: once to within its last bit, then to the
+// division's own rounding; one small enough for its residue to underflow
+// rounds to zero anyway, and none is above 127 (1 + 2^-23), by the scale's own
+// rounding.  Adding 1.5 * 2^23 rounds to an integer, ties to even, in the
+// sum's low bits.  Half a division's instructions: the head's bf16 rows were
+// bound by them.
 __device__ __forceinline__ bool plain_scale(float s) { return s > 0x1p-100f && s < 0x1p100f; }
 __device__ __forceinline__ uint32_t quantize4(float x0, float x1, float x2, float x3, float s, float inv) {
   const float x[4] = {x0, x1, x2, x3};
   uint32_t u[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float q = x[e] * inv;
-    u[e] = __float_as_uint(__builtin_fmaf(__builtin_fmaf(-q, s, x[e]), inv, q) + 0x1.8p23f);
+    float q = x[e] * inv;
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x[e]), inv, q);
+    q = __builtin_fmaf(__builtin_fmaf(-q, s, x[e]), inv, q);
+    u[e] = __float_as_uint(q + 0x1.8p23f);
   }
   // the low bytes, u[0]'s first
   return __builtin_amdgcn_perm(u[1], u[0], 0x0C0C0400u) | __builtin_amdgcn_perm(u[3], u[2], 0x04000C0Cu);

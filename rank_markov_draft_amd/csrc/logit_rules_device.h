@@ -23,11 +23,12 @@ __device__ __forceinline__ Penalty penalty_of(const RuleSet& r, int64_t b) {
                  r.frequency != nullptr || r.presence != nullptr};
 }
 
-// The same for eight values whose counts stand in a word of bytes (0: not
+// The same for eight bf16 values whose counts stand in a word of bytes (0: not
 // seen, n: n - 1 times among the outputs), without a branch: some of them were
-// seen.  The quotient is the product with the rounded reciprocal and one
-// correction of its residue, which rounds as a division does; the fixup puts
-// in what a division gives for infinities, NaN and zeros.
+// seen.  The quotient is the product with the rounded reciprocal, corrected
+// once by its residue: that is the division to within its last bit of fp32
+// (and almost always to its own rounding), 2^-16 of a step of the bf16 result.
+// The fixup puts in what a division gives for infinities, NaN and zeros.
 __device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p) {
   const float inv = 1.0f / p.repetition;
 #pragma unroll
