@@ -146,7 +146,7 @@ size_t table_bits_bytes(int64_t B, int64_t V) {
   return align256(mul_sz(mul_sz((size_t)B, (size_t)dspark::rule_words(V)), 4));
 }
 size_t table_counts_bytes(int64_t B, int64_t V) {
-  return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 128));  // read in whole words of 32 columns
+  return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 256));  // read in whole groups of 64 columns
 }
 
 }  // namespace
@@ -355,13 +355,14 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
     (void)hipGetLastError();  // not launchable here: a launch per position
   }
   // Up to 8 rows the last workgroup of a step draws the tokens itself, by keys
-  // and a counter in the chain's area (zero between launches): 8 rows at V =
-  // 32000 56 us a draft of five, 62 us with a second launch a step.  More rows
-  // would meet in the same few lines of memory: 64 rows at V = 129280 211 us,
-  // 197 us with the second launch.
-  if (B <= 8) {
-    p.arrived = (uint32_t*)((char*)workspace + kControlBytes + dspark::kChainSyncBytes);
-    p.keys = (uint64_t*)(p.arrived + 64);
+  // and a counter in the control block: 8 rows at V = 32000 56 us a draft of
+  // five, 62 us with a second launch a step.  More rows would meet in the same
+  // few lines of memory: 64 rows at V = 129280 211 us, 197 us with the second
+  // launch.
+  if (B <= kStepKeys) {
+    Control* const ctl = (Control*)workspace;
+    p.arrived = &ctl->step_arrived;
+    p.keys = ctl->step_keys;
     p.tokens_out = sampled_tokens;
     p.seen_out = table ? seen : nullptr;
     p.counts_out = counts;

@@ -70,7 +70,7 @@ struct RuleStepParams {
   const void* w1;          // [V, rank]
   const void* w2;          // [V, rank]
   const uint32_t* seen;    // table, or null (no penalty)
-  const uint32_t* counts;  // readable 64 bytes past its end
+  const uint32_t* counts;  // readable 256 bytes past its end
   uint64_t* partials;      // [B, rule_step_parts(V)]: read by launch_rule_choose (keys null)
   // or: the last workgroup of a row chunk to finish draws its tokens itself.
   // Zero before the launch, left zero.

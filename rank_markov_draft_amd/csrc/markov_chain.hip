@@ -277,8 +277,12 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
       if (penalise && g4 == 0 && row_ok && t >= (int64_t)vbeg && t < (int64_t)vend) {
         uint8_t& n = lds_n[b * kCols + (int)(t - vbeg)];
         uint32_t* const big = p.counts + (int64_t)b * V + t;
-        if (n == 255) __hip_atomic_fetch_add(big, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        else if (n == 254) __hip_atomic_store(big, 254u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (n >= 254) {
+          if (n == 255) __hip_atomic_fetch_add(big, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          else __hip_atomic_store(big, 254u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          // another wave of this workgroup reads it a barrier from here
+          __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
         n = n == 0 ? 2 : n < 255 ? n + 1 : 255;
       }
     }

@@ -553,6 +553,27 @@ def test_greedy_chain_failure_is_reported(native):
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
 
 
+@pytest.mark.parametrize("B", (3, 20))
+def test_draft_by_steps_after_a_failed_chain(native, B):
+    """A failed chain leaves its own area of the workspace as it stood; drafts
+    that run step by step do not read it."""
+    from rank_markov_draft_amd import _lib
+    c = _draft_case(B, 5, 4096, 20, 64, BF16, BF16, mask="each", bias="row")
+    ws = rmd.Workspace(B, 5, 4096, 64, sample=True, processed=True)
+    greedy, drawn = _draft(c, workspace=ws), _draft(c, T=0.8, seed=3, workspace=ws)
+    plain = (c.logits.cuda(), torch.from_numpy(c.first).cuda(), c.w1.cuda(), c.w2.cuda())
+    ws.set_chain_test_hook(True)
+    assert (rmd.sample_block_tokens(*plain, 0.0, workspace=ws)[0] == -1).all()
+    ws.set_chain_test_hook(False)
+    for _ in range(2):
+        for want, got in ((greedy, _draft(c, workspace=ws)), (drawn, _draft(c, T=0.8, seed=3, workspace=ws))):
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(_lib.DsparkError, match="DEVICE"):
+        rmd.read_device_error(ws)
+    again = _draft(c, workspace=ws)
+    assert torch.equal(again[0], greedy[0]) and torch.equal(again[1], greedy[1])
+
+
 def test_draft_of_more_rows_than_the_keys_hold(native):
     """70000 requests: their best keys do not fit beside the counters, so a
     second launch reduces them; the same rows in smaller calls are the same."""

@@ -108,7 +108,13 @@ def test_process_refusals(L):
 
 def test_sample_processed_refusals(L):
     need = L.dspark_markov_processed_workspace_bytes(2, 3, 40, 8)
-    assert need == L.dspark_markov_workspace_bytes(2, 3, 40, 8, 1) + 256 + 512
+    assert need == L.dspark_markov_workspace_bytes(2, 3, 40, 8, 1) + 256 + 768
+    # the step reads the counts of a lane's 16 columns of 64 where any of them
+    # exists: up to 51 past the last row's end
+    for B, V in ((32, 65), (1, 97), (64, 1), (3, 32065)):
+        bits = -(-B * (-(-V // 32)) * 4 // 256) * 256
+        base = -(-L.dspark_markov_workspace_bytes(B, 2, V, 8, 1) // 256) * 256
+        assert L.dspark_markov_processed_workspace_bytes(B, 2, V, 8) >= base + bits + 4 * (B * V + 51)
     assert L.dspark_markov_processed_workspace_bytes(2 ** 40, 1, 2 ** 40, 8) == 2 ** 64 - 1
 
     def s(base=A[0], ldt=1, first=A[1], w1=A[2], w2=A[3], wdt=1, r_=rules(), B=2, M=3, V=40, r=8, T=0.0, tok=A[4], out=A[6],
