@@ -141,13 +141,14 @@ dspark_status_t run_rules(const void* grad, const void* logits, dspark_dtype_t d
 }
 
 // Workspace of a processed draft past the vanilla sampling layout: the table's
-// bits, then its counts.
+// bits, its counts, and the steps' keys.
 size_t table_bits_bytes(int64_t B, int64_t V) {
   return align256(mul_sz(mul_sz((size_t)B, (size_t)dspark::rule_words(V)), 4));
 }
 size_t table_counts_bytes(int64_t B, int64_t V) {
   return align256(add_sz(mul_sz(mul_sz((size_t)B, (size_t)V), 4), 256));  // read in whole groups of 64 columns
 }
+size_t step_keys_bytes(int64_t B) { return align256(mul_sz((size_t)B, dspark::kStepSlots * dspark::kStepGroups * sizeof(uint64_t))); }
 
 }  // namespace
 
@@ -251,7 +252,7 @@ dspark_status_t dspark_markov_process_block_backward(const void* grad_processed,
 size_t dspark_markov_processed_workspace_bytes(int64_t B, int64_t M, int64_t V, int64_t r) {
   const size_t base = align256(dspark_markov_workspace_bytes(B, M, V, r, 1));
   if (B < 0 || M < 0 || V < 0) return base;
-  return add_sz(base, add_sz(table_bits_bytes(B, V), table_counts_bytes(B, V)));
+  return add_sz(base, add_sz(step_keys_bytes(B), add_sz(table_bits_bytes(B, V), table_counts_bytes(B, V))));
 }
 
 dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, dspark_dtype_t logits_dtype,
@@ -293,12 +294,13 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   char* const region = (char*)workspace + align256(dspark_markov_workspace_bytes(B, M, V, r, 1));
   uint32_t* const seen = (uint32_t*)region;
   uint32_t* const counts = (uint32_t*)(region + table_bits_bytes(B, V));
+  uint64_t* const keys = (uint64_t*)((char*)counts + table_counts_bytes(B, V));
   // without penalties, or with nothing before a single position, no token is
   // ever looked up
   const bool table = dspark::rules_penalise(p.r) && (p.r.history != nullptr || M > 1);
   hipError_t e = hipSuccess;
   if (table) {
-    const dspark::TableParams t{p.r, seen, counts, B, V};
+    const dspark::TableParams t{p.r, seen, counts, keys, B, V};
     e = dspark::launch_rule_table(t, s);
     if (e != hipSuccess) return device_failure(e, "rule table launch");
   }
@@ -310,7 +312,7 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   p.w2 = w2;
   p.seen = table ? seen : nullptr;
   p.counts = counts;
-  p.partials = (uint64_t*)((char*)workspace + kDataOffset);
+  p.keys = keys;
   p.bad_rows = &((Control*)workspace)->bad_rows;
   p.B = B;
   p.M = M;
@@ -354,29 +356,18 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
     if (e == hipSuccess) return DSPARK_OK;
     (void)hipGetLastError();  // not launchable here: a launch per position
   }
-  // Up to 8 rows the last workgroup of a step draws the tokens itself, by keys
-  // and a counter in the control block: 8 rows at V = 32000 56 us a draft of
-  // five, 62 us with a second launch a step.  More rows would meet in the same
-  // few lines of memory: 64 rows at V = 129280 211 us, 197 us with the second
-  // launch.
-  if (B <= kStepKeys) {
-    Control* const ctl = (Control*)workspace;
-    p.arrived = &ctl->step_arrived;
-    p.keys = ctl->step_keys;
-    p.tokens_out = sampled_tokens;
-    p.seen_out = table ? seen : nullptr;
-    p.counts_out = counts;
+  if (!table) {
+    e = dspark::launch_fill_zero(keys, (size_t)B * dspark::kStepGroups * sizeof(uint64_t), s);
+    if (e != hipSuccess) return device_failure(e, "step keys clear");
   }
   for (int64_t k = 0; k < M; ++k) {
     p.k = k;
     p.k_abs = (uint32_t)(position_offset + k);
     e = dspark::launch_rule_step(p, logits_dtype == DSPARK_BF16, weight_dtype == DSPARK_BF16, s);
     if (e != hipSuccess) return device_failure(e, "rule step launch");
-    if (p.keys) continue;
-    e = dspark::launch_rule_choose(p.partials, dspark::rule_step_parts(V), B, M, k, V, sampled_tokens,
-                                   table ? seen : nullptr, counts, s);
-    if (e != hipSuccess) return device_failure(e, "token choice launch");
   }
+  e = dspark::launch_rule_choose(keys, B, M, sampled_tokens, s);
+  if (e != hipSuccess) return device_failure(e, "token choice launch");
   return DSPARK_OK;
 }
 

@@ -24,11 +24,7 @@ namespace host {
 // may share a workspace):
 //   [0, 256)      control block: the device error word, the
 //                 synchronisation-failure count of the persistent chain and
-//                 its test hook, each on its own 64-byte line; in the lines'
-//                 free words the keys and the counter by which a processed
-//                 draft's step picks its tokens (zero between launches, and
-//                 kept apart from the chain area, which a failed chain leaves
-//                 dirty);
+//                 its test hook, each on its own 64-byte line;
 //   chain area    arrival counters (kChainSyncBytes), then the device-wide
 //                 argmax keys per (step, key group, row): 64-byte slots for
 //                 up to kChainMaxSteps steps of 64 rows (greedy chain), or
@@ -51,16 +47,11 @@ struct Control {
   uint32_t bad_rows;       // byte 0: rows with out-of-range ids
   uint32_t pad0[15];
   uint32_t sync_failures;  // byte 64: failed device-wide waits of the persistent chain
-  uint32_t pad1[7];
-  uint32_t step_arrived;   // byte 96
-  uint32_t pad2[7];
+  uint32_t pad1[15];
   uint32_t chain_test_hook;  // byte 128: nonzero makes the chain's waits give up at once
-  uint32_t pad3[15];
-  uint64_t step_keys[8];   // byte 192
+  uint32_t pad2[15];
 };
-constexpr int64_t kStepKeys = 8;
-static_assert(offsetof(Control, chain_test_hook) == 128 && offsetof(Control, step_keys) == 192, "control block");
-static_assert(sizeof(Control) <= kControlBytes && kStepKeys * 8 == sizeof(Control::step_keys), "control block");
+static_assert(sizeof(Control) <= kControlBytes, "control block");
 
 // Size arithmetic of the workspace queries saturates at SIZE_MAX, the
 // answer for sizes that cannot be represented.

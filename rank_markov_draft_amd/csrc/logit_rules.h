@@ -53,32 +53,34 @@ struct TableParams {
   RuleSet r;
   uint32_t* seen;
   uint32_t* counts;
+  uint64_t* keys;  // of a draft's steps: its first slot is cleared
   int64_t B;
   int64_t V;
 };
 hipError_t launch_rule_table(const TableParams& p, hipStream_t s);
 
-// Step k of a left-to-right draft in one pass: the corrected logits of row
-// (b, k) (base plus the bias of its predecessor), the rules, the processed row
-// to `out`, and the row's best keys over rule_step_parts(V) blocks of columns.
+// Best keys of a draft's rows: three slots, of steps k = 0, 1, 2 modulo 3,
+// each of kStepGroups groups of columns by B rows.  Step k reads the last
+// step's slot, meets in its own and clears the next one's; the first step's
+// is clear before the draft (launch_rule_table, or a fill).
+constexpr int kStepGroups = 8;
+constexpr int kStepSlots = 3;
+
+// Step k of a left-to-right draft in one pass: the token of position k - 1
+// from its keys, written out and counted; the corrected logits of row (b, k)
+// (base plus the bias of that predecessor), the rules, the processed row to
+// `out`, and the row's best keys.
 struct RuleStepParams {
   RuleSet r;
   const void* base;        // [B, M, V]
   void* out;               // [B, M, V]
   const int64_t* first;    // [B] predecessors of position 0
-  const int64_t* tokens;   // [B, M] predecessors of the others, at k - 1
+  int64_t* tokens;         // [B, M]
   const void* w1;          // [V, rank]
   const void* w2;          // [V, rank]
-  const uint32_t* seen;    // table, or null (no penalty)
-  const uint32_t* counts;  // readable 256 bytes past its end
-  uint64_t* partials;      // [B, rule_step_parts(V)]: read by launch_rule_choose (keys null)
-  // or: the last workgroup of a row chunk to finish draws its tokens itself.
-  // Zero before the launch, left zero.
-  uint64_t* keys;          // [B]
-  uint32_t* arrived;       // one word (keys: B at most 16)
-  int64_t* tokens_out;     // [B, M] (the same as tokens)
-  uint32_t* seen_out;      // (the same as seen)
-  uint32_t* counts_out;    // (the same as counts)
+  uint32_t* seen;          // table, or null (no penalty)
+  uint32_t* counts;        // readable 256 bytes past its end
+  uint64_t* keys;          // [kStepSlots][kStepGroups][B]
   uint32_t* bad_rows;
   int64_t B;
   int64_t M;
@@ -92,12 +94,9 @@ struct RuleStepParams {
   uint32_t seed_hi;
   bool greedy;
 };
-int64_t rule_step_parts(int64_t V);
 hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, hipStream_t s);
 
-// tokens[b, k] = the column of the row's best key, -1 when its score is -inf;
-// a drawn token joins the table (seen null: no table).
-hipError_t launch_rule_choose(const uint64_t* partials, int64_t nparts, int64_t B, int64_t M, int64_t k, int64_t V,
-                              int64_t* tokens, uint32_t* seen, uint32_t* counts, hipStream_t s);
+// tokens[b, M - 1] = the column of the row's best key, -1 when its score is -inf.
+hipError_t launch_rule_choose(const uint64_t* keys, int64_t B, int64_t M, int64_t* tokens, hipStream_t s);
 
 }  // namespace dspark

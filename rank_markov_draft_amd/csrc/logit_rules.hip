@@ -328,6 +328,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_table_kernel(TableParams p,
   const int64_t t0 = (int64_t)(blockIdx.x % (unsigned)tiles) * kTableCols;
   const int tn = (int)(p.V - t0 < kTableCols ? p.V - t0 : kTableCols);
   const int tid = threadIdx.x;
+  if (t0 == 0 && tid < kStepGroups) p.keys[tid * p.B + b] = 0u;
   for (int i = tid; i < kTableCols / 32; i += kRuleThreads) seen[i] = 0u;
   for (int i = tid; i < kTableCols / 4; i += kRuleThreads) *(u32x4_t*)&counts[4 * i] = u32x4_t{0u, 0u, 0u, 0u};
   __syncthreads();
@@ -359,19 +360,14 @@ constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
 constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
 constexpr int kStepPitch = kStepRowBytes + 16;       // its pitch in LDS
 
-// The token of row b from its best key, -1 when that is -inf; it joins the
-// row's table, which nobody else touches now, with a count of its own when its
-// bit was clear.
-__device__ __forceinline__ void draw_token(uint64_t best, int64_t b, int64_t M, int64_t k, int64_t V, int64_t* tokens,
-                                           uint32_t* seen, uint32_t* counts) {
-  const int64_t t = (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
-  tokens[b * M + k] = t;
-  if (seen && t >= 0) {
-    uint32_t* const w = seen + b * ((V + 31) / 32) + (t >> 5);
-    const uint32_t bit = 1u << (t & 31);
-    counts[b * V + t] = (*w & bit) ? counts[b * V + t] + 1u : 1u;
-    *w |= bit;
-  }
+// The token of row b from the best of its keys in a slot, -1 when that is -inf.
+__device__ __forceinline__ int64_t drawn_token(const uint64_t* slot, int64_t b, int64_t B) {
+  uint64_t key[kStepGroups], best = 0;
+#pragma unroll
+  for (int g = 0; g < kStepGroups; ++g) key[g] = slot[g * B + b];
+#pragma unroll
+  for (int g = 0; g < kStepGroups; ++g) best = max_u64(best, key[g]);
+  return (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
 }
 
 // 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
@@ -393,8 +389,6 @@ __device__ __forceinline__ u32x4_t weights16(const char* row, int64_t k, int64_t
 }
 }  // namespace
 
-int64_t rule_step_parts(int64_t V) { return (V + kStepCols - 1) / kStepCols; }
-
 // A workgroup: 256 columns, all rows of the step in passes of 16 RT.  The
 // bias of a row tile is a product on the matrix cores with the vocabulary on
 // M and the rows on N (16 x 16 blocks, bf16 or fp32 as the weights are); the
@@ -408,7 +402,7 @@ int64_t rule_step_parts(int64_t V) { return (V + kStepCols - 1) / kStepCols; }
 // memory to the operands directly (each element is used by one wave of the
 // workgroup), the gathered W1 rows through LDS.
 template <bool WBF, bool BF, int RT>
-__global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_kernel(RuleStepParams p, int tiles, unsigned chunks) {
+__global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleStepParams p, int tiles, unsigned chunks) {
   constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;          // bytes of a weight, weights of a 16-byte piece
   constexpr int KI = 4 * KE;                             // rank elements of a step (32 or 16)
   constexpr int KC = kStepRowBytes / WB;                 // and of a chunk
@@ -447,10 +441,19 @@ __global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_
   if (tid < 16 * RT) {
     int64_t x = -1;
     if (b0 + tid < p.B) {
-      x = p.k == 0 ? p.first[b0 + tid] : p.tokens[(b0 + tid) * p.M + p.k - 1];
-      if (x < 0 || x >= V) {
-        if (tile == 0 && p.k == 0) atomicAdd(p.bad_rows, 1u);
-        x = -1;
+      if (p.k == 0) {
+        x = p.first[b0 + tid];
+        if (x < 0 || x >= V) {
+          if (tile == 0) atomicAdd(p.bad_rows, 1u);
+          x = -1;
+        }
+      } else {
+        x = drawn_token(p.keys + ((p.k - 1) % kStepSlots) * kStepGroups * p.B, b0 + tid, p.B);
+        if (tile == 0) p.tokens[(b0 + tid) * p.M + p.k - 1] = x;
+      }
+      if (tile == 0) {
+#pragma unroll
+        for (int g = 0; g < kStepGroups; ++g) p.keys[(((p.k + 1) % kStepSlots) * kStepGroups + g) * p.B + b0 + tid] = 0u;
       }
     }
     lds_src[tid] = x;
@@ -587,7 +590,25 @@ __global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_
   for (int i = 0; i < RT; ++i) {
     const int64_t b = b0 + 16 * i + n16;
     fetch_counts(i + 1);
-    const uint32_t s16 = own_bits(seen[i]), m16 = own_bits(mask[i]);
+    uint32_t s16 = own_bits(seen[i]);
+    const uint32_t m16 = own_bits(mask[i]);
+    if (p.seen && p.k > 0) {
+      // the token of the last position joins the table in the one lane, of all
+      // the step's workgroups, that has its column
+      const int64_t t = lds_src[16 * i + n16];
+      const int rel = (int)(t - wc0);
+      if (t >= wc0 && rel < kStepWaveCols && (BF ? rel >> 4 : rel >> 2 & 3) == g4) {
+        const int mine = BF ? rel & 15 : 4 * (rel >> 4) + (rel & 3);
+        uint32_t n = 1u;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e == mine) count[i & 1][e] = n = (s16 >> e & 1u) ? count[i & 1][e] + 1u : 1u;
+        s16 |= 1u << mine;
+        p.counts[b * V + t] = n;
+        if constexpr (BF) ((uint16_t*)(p.seen + b * W))[t >> 4] = (uint16_t)s16;
+        else p.seen[b * W + (t >> 5)] = (uint32_t)(seen[i] >> (rel & 32)) | 1u << (t & 31);
+      }
+    }
     float x[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -671,33 +692,15 @@ __global__ __launch_bounds__(256, RT == 4 ? 2 : RT == 2 ? 3 : 4) void rule_step_
   const bool row_ok = tid < 16 * RT && b0 + tid < p.B;
   uint64_t best = 0;
   if (row_ok) best = max_u64(max_u64(lds_key[0][tid], lds_key[1][tid]), max_u64(lds_key[2][tid], lds_key[3][tid]));
-  if (p.keys == nullptr) {
-    if (row_ok) p.partials[(b0 + tid) * tiles + tile] = best;
-    return;
-  }
-  // One row chunk: its keys meet in memory; whoever counts in last draws the tokens.
-  // Nobody waits: the first wave's own maxima are done before it counts in, all
-  // by device-scope atomics.
-  if (wave == 0) {
-    if (row_ok) __hip_atomic_fetch_max(p.keys + b0 + tid, best, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    uint32_t ticket = 0;
-    if (lane == 0) ticket = __hip_atomic_fetch_add(p.arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__builtin_amdgcn_readfirstlane(ticket) != (uint32_t)tiles - 1u) return;
-    __asm__ volatile("" ::: "memory");
-    if (row_ok) {
-      best = __hip_atomic_load(p.keys + b0 + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __hip_atomic_store(p.keys + b0 + tid, (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      draw_token(best, b0 + tid, p.M, p.k, V, p.tokens_out, p.seen_out, p.counts_out);
-    }
-    if (lane == 0) __hip_atomic_store(p.arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  if (row_ok)
+    __hip_atomic_fetch_max(p.keys + ((p.k % kStepSlots) * kStepGroups + tile % kStepGroups) * p.B + b0 + tid, best,
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 namespace {
 template <bool WBF, bool BF, int RT>
 hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
-  const int64_t tiles = rule_step_parts(p.V), chunks = (p.B + 16 * RT - 1) / (16 * RT);
+  const int64_t tiles = (p.V + kStepCols - 1) / kStepCols, chunks = (p.B + 16 * RT - 1) / (16 * RT);
   const int64_t groups = (tiles + 7) / 8 * 8 * chunks;
   if (groups > 0x7FFFFFFF) return hipErrorNotSupported;
   hipLaunchKernelGGL((rule_step_kernel<WBF, BF, RT>), dim3((unsigned)groups), dim3(256), 0, s, p, (int)tiles,
@@ -706,7 +709,6 @@ hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
 }
 template <bool WBF, bool BF>
 hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
-  if (p.keys != nullptr && p.B > 16) return hipErrorInvalidValue;  // one row chunk, one counter
   if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
   if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
   return rule_step_form<WBF, BF, 4>(p, s);
@@ -718,30 +720,17 @@ hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weig
   return logits_bf16 ? rule_step_go<false, true>(p, s) : rule_step_go<false, false>(p, s);
 }
 
-// One workgroup per row.
-__global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_t* __restrict__ partials,
-                                                                   int64_t nparts, int64_t M, int64_t k, int64_t V,
-                                                                   int64_t* __restrict__ tokens, uint32_t* seen,
-                                                                   uint32_t* counts) {
-  __shared__ uint64_t lds_key[kRuleThreads / 64];
-  const int64_t b = blockIdx.x;
-  const int tid = threadIdx.x;
-  uint64_t best = 0;
-  for (int64_t i = tid; i < nparts; i += kRuleThreads) best = max_u64(best, partials[b * nparts + i]);
-  best = wave_max_u64_lane63(best);
-  if ((tid & 63) == 63) lds_key[tid >> 6] = best;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 0; w < kRuleThreads / 64; ++w) best = max_u64(best, lds_key[w]);
-    draw_token(best, b, M, k, V, tokens, seen, counts);
-  }
+__global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_t* __restrict__ slot, int64_t B, int64_t M,
+                                                                   int64_t* __restrict__ tokens) {
+  const int64_t b = (int64_t)blockIdx.x * kRuleThreads + threadIdx.x;
+  if (b < B) tokens[b * M + M - 1] = drawn_token(slot, b, B);
 }
 
-hipError_t launch_rule_choose(const uint64_t* partials, int64_t nparts, int64_t B, int64_t M, int64_t k, int64_t V,
-                              int64_t* tokens, uint32_t* seen, uint32_t* counts, hipStream_t s) {
-  if (B > 0x7FFFFFFF) return hipErrorNotSupported;
-  hipLaunchKernelGGL(rule_choose_kernel, dim3((unsigned)B), dim3(kRuleThreads), 0, s, partials, nparts, M, k, V,
-                     tokens, seen, counts);
+hipError_t launch_rule_choose(const uint64_t* keys, int64_t B, int64_t M, int64_t* tokens, hipStream_t s) {
+  const int64_t groups = (B + kRuleThreads - 1) / kRuleThreads;
+  if (groups > 0x7FFFFFFF) return hipErrorNotSupported;
+  hipLaunchKernelGGL(rule_choose_kernel, dim3((unsigned)groups), dim3(kRuleThreads), 0, s,
+                     keys + ((M - 1) % kStepSlots) * kStepGroups * B, B, M, tokens);
   return hipGetLastError();
 }
 

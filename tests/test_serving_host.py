@@ -108,7 +108,7 @@ def test_process_refusals(L):
 
 def test_sample_processed_refusals(L):
     need = L.dspark_markov_processed_workspace_bytes(2, 3, 40, 8)
-    assert need == L.dspark_markov_workspace_bytes(2, 3, 40, 8, 1) + 256 + 768
+    assert need == L.dspark_markov_workspace_bytes(2, 3, 40, 8, 1) + 256 + 768 + 512
     # the step reads the counts of a lane's 16 columns of 64 where any of them
     # exists: up to 51 past the last row's end
     for B, V in ((32, 65), (1, 97), (64, 1), (3, 32065)):
