@@ -62,6 +62,8 @@ __device__ __forceinline__ void count_history(const RuleSet& r, int64_t b, int64
 // Vectors of rows that start at any element (an odd vocabulary): the hardware
 // loads and stores 16 bytes at any address.
 typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // 8 consecutive values of a row as they are stored.
 template <bool BF>
@@ -355,19 +357,24 @@ hipError_t launch_rule_table(const TableParams& p, hipStream_t s) {
 }
 
 namespace {
+constexpr int kFewRows = 4;                          // rows of the kernel for few of them
 constexpr int kStepWaveCols = 64;                    // columns of a wave
 constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
 constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
 constexpr int kStepPitch = kStepRowBytes + 16;       // its pitch in LDS
 
-// The token of row b from the best of its keys in a slot, -1 when that is -inf.
-__device__ __forceinline__ int64_t drawn_token(const uint64_t* slot, int64_t b, int64_t B) {
-  uint64_t key[kStepGroups], best = 0;
-#pragma unroll
-  for (int g = 0; g < kStepGroups; ++g) key[g] = slot[g * B + b];
+// The token of a row's best key of a slot, -1 when that is -inf.
+__device__ __forceinline__ int64_t token_of(const uint64_t (&key)[kStepGroups]) {
+  uint64_t best = 0;
 #pragma unroll
   for (int g = 0; g < kStepGroups; ++g) best = max_u64(best, key[g]);
   return (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
+}
+__device__ __forceinline__ int64_t drawn_token(const uint64_t* slot, int64_t b, int64_t B) {
+  uint64_t key[kStepGroups];
+#pragma unroll
+  for (int g = 0; g < kStepGroups; ++g) key[g] = slot[g * B + b];
+  return token_of(key);
 }
 
 // 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
@@ -697,6 +704,229 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+// The same step for up to four rows.  With the rows on the matrix
+// instruction's 16 columns most lanes would hold rows that do not exist and
+// the others 16 columns each, a long stretch of code for a lone wave of a SIMD;
+// here a wave's 64 columns by four rows are sixteen 4 x 4 blocks, and a lane
+// ends up with four consecutive columns of one row: a vector of logits and a
+// block of noise.  Both operands go to registers, two lines of 128 bytes of a
+// row ahead of the products, and nothing waits at a barrier before the keys.
+// W2 is loaded a line by eight lanes and turned through LDS: lanes loading
+// their own rows touch a line each (rank 256 in fp32, V = 129280, drafts of
+// five: 1 row 162 us so, 134 us as here, 146 us by the kernel above; 4 rows
+// 189, 140 and 136 us).  Bound by latency where W2 is short: V = 50257 at rank
+// 64 in fp32 8.3 us a step, 12.2 us by the kernel above.  For 8 rows, two such
+// sets of blocks took 52 -> 71 us a draft (V = 32000, rank 64, bf16).
+template <bool WBF, bool BF>
+__global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p) {
+  constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;  // bytes of a weight, weights of a 16-byte piece
+  constexpr int LB = BF ? 2 : 4, NP = 8;         // bytes of a logit, pieces of a line
+  typedef uint32_t base_t __attribute__((ext_vector_type(LB), aligned(2)));
+  __shared__ uint64_t lds_key[4][kFewRows];
+  __shared__ __attribute__((aligned(16))) unsigned char lds_w[4][kStepWaveCols * 128];
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63;
+  const int tile = (int)blockIdx.x;
+  const int64_t V = p.V, rank = p.rank, W = (V + 31) / 32, b = lane & 3;
+  const int wc0 = tile * kStepCols + kStepWaveCols * wave, c0 = wc0 + (lane & ~3);  // V is at most 2^30
+  const int left = (int)V - c0, have = left < 0 ? 0 : left < 4 ? left : 4;
+  const int whole = (int)(rank / KE), lines = (whole + NP - 1) / NP;
+  uint64_t key[kStepGroups];
+  int64_t x = -1;  // the row's predecessor
+  if (b < p.B) {
+    if (p.k == 0) {
+      x = p.first[b];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStepGroups; ++i) key[i] = p.keys[(((p.k - 1) % kStepSlots) * kStepGroups + i) * p.B + b];
+    }
+  }
+  // W2, its first lines ahead of everything that waits: load i of a line takes
+  // rows 8 i .. 8 i + 7 of the wave's (past V: the last row)
+  auto row_of = [&](int i) __attribute__((always_inline)) -> const char* {
+    const int64_t v = wc0 + i < V ? wc0 + i : V - 1;
+    return (const char*)p.w2 + v * rank * WB;
+  };
+  const int pc = lane & 7, r8 = lane >> 3;
+  u32x4_t w[2][NP], e[2][NP];
+  auto fetch_w = [&](int l, u32x4_t (&d)[NP]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      d[i] = u32x4_t{0u, 0u, 0u, 0u};
+      if (NP * l + pc < whole) d[i] = *(const u32x4_any_t*)(row_of(8 * i + r8) + (NP * l + pc) * 16);
+    }
+  };
+  // the pieces of the lane's own row out of a line's loads, through the wave's
+  // own LDS (a wave's LDS accesses keep their order)
+  unsigned char* const mine = lds_w[wave];
+  auto turn = [&](const u32x4_t (&d)[NP], u32x4_t (&a)[NP]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) *(u32x4_t*)(mine + (8 * i + r8) * 128 + 16 * (pc ^ r8)) = d[i];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int q = 0; q < NP; ++q) a[q] = *(const u32x4_t*)(mine + lane * 128 + 16 * (q ^ (lane & 7)));
+    __builtin_amdgcn_wave_barrier();
+  };
+  fetch_w(0, w[0]);
+  fetch_w(1, w[1]);
+  // base logits and what the rules need of the lane's columns
+  uint32_t raw[4] = {0u, 0u, 0u, 0u}, seen = 0u, mask = ~0u, word = 0u;
+  float bias[8];
+  Penalty pen{};
+  if (b < p.B && have > 0) {
+    const char* const at = (const char*)p.base + ((b * p.M + p.k) * V + c0) * LB;
+    if (have == 4) {
+      const base_t d = __builtin_nontemporal_load((const base_t*)at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = BF ? (i & 1 ? d[i >> 1] >> 16 : d[i >> 1] & 0xFFFFu) : d[i & (LB - 1)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < have) raw[i] = BF ? ((const uint16_t*)at)[i] : ((const uint32_t*)at)[i];
+    }
+    if (p.seen) {
+      word = p.seen[b * W + (c0 >> 5)];
+      pen = penalty_of(p.r, b);
+    }
+    if (p.r.mask) mask = p.r.mask[b * p.r.mask_stride_b + p.k * p.r.mask_stride_m + (c0 >> 5)];
+    if (p.r.bias) bias8<4>(p.r, b * p.r.bias_stride + c0, have, bias);
+  }
+  // the predecessor, and the next step's slot
+  if (b < p.B) {
+    const bool writer = tile == 0 && tid < kFewRows;
+    if (p.k == 0) {
+      if (x < 0 || x >= V) {
+        if (writer) atomicAdd(p.bad_rows, 1u);
+        x = -1;
+      }
+    } else {
+      x = token_of(key);
+      if (writer) p.tokens[b * p.M + p.k - 1] = x;
+    }
+    if (writer) {
+#pragma unroll
+      for (int i = 0; i < kStepGroups; ++i) p.keys[(((p.k + 1) % kStepSlots) * kStepGroups + i) * p.B + b] = 0u;
+    }
+  }
+  const char* const erow = (const char*)p.w1 + (x < 0 ? 0 : x) * rank * WB;
+  auto fetch_e = [&](int l, u32x4_t (&d)[NP]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      d[q] = u32x4_t{0u, 0u, 0u, 0u};
+      if (NP * l + q < whole && x >= 0) d[q] = *(const u32x4_any_t*)(erow + (NP * l + q) * 16);
+    }
+  };
+  fetch_e(0, e[0]);
+  fetch_e(1, e[1]);
+  // counts of the lane's columns that stand in the table, and the last
+  // position's token, which joins it in the one lane of all the step's
+  // workgroups that has its column
+  uint32_t count[4];
+  seen = word >> (c0 & 31) & 15u;
+  if (seen) {
+    const u32x4_t n = *(const u32x4_any_t*)(p.counts + b * V + c0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) count[i] = n[i];
+  }
+  if (p.seen && p.k > 0 && x >= c0 && x < c0 + 4) {
+    const int at = (int)x - c0;
+    uint32_t n = 1u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i == at) count[i] = n = (seen >> i & 1u) ? count[i] + 1u : 1u;
+    seen |= 1u << at;
+    p.counts[b * V + x] = n;
+    p.seen[b * W + (c0 >> 5)] = word | 1u << (x & 31);
+  }
+  f32x4_t acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](int q, const u32x4_t& wp, const u32x4_t& ep) __attribute__((always_inline)) {
+    if constexpr (WBF) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const u32x2_t w2 = {wp[2 * h], wp[2 * h + 1]}, e2 = {ep[2 * h], ep[2 * h + 1]};
+        f32x4_t& d = acc[(2 * q + h) & 3];
+        d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, w2), __builtin_bit_cast(s16x4_t, e2), d, 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(wp[i]), __uint_as_float(ep[i]), acc[i], 0, 0, 0);
+    }
+  };
+  for (int l = 0; l < lines; l += 2) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (l + h < lines) {
+        u32x4_t a[NP];
+        turn(w[h], a);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) multiply(q, a[q], e[h][q]);
+        if (l + h + 2 < lines) {
+          fetch_w(l + h + 2, w[h]);
+          fetch_e(l + h + 2, e[h]);
+        }
+      }
+  }
+  if (whole * KE < rank)  // the last elements of a rank that is no whole number of pieces
+    multiply(0, weights16<WB>(row_of(lane), (int64_t)whole * KE, rank),
+             x >= 0 ? weights16<WB>(erow, (int64_t)whole * KE, rank) : u32x4_t{0u, 0u, 0u, 0u});
+  uint64_t best = 0;
+  if (b < p.B && have > 0) {
+    const f32x4_t sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    float y[4], noise[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!p.greedy) {
+      const Philox4 q = philox4x32_10((uint32_t)(c0 >> 2), p.k_abs, (uint32_t)p.batch_offset + (uint32_t)b, 0u, p.seed_lo,
+                                      p.seed_hi);
+      noise[0] = gumbel2_from_word(q.x0);
+      noise[1] = gumbel2_from_word(q.x1);
+      noise[2] = gumbel2_from_word(q.x2);
+      noise[3] = gumbel2_from_word(q.x3);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float product = WBF || BF ? bf16_rne(sum[i]) : sum[i];
+      y[i] = BF ? bf16_rne(bf16_lo(raw[i]) + product) : __uint_as_float(raw[i]) + product;
+      if (seen >> i & 1u) y[i] = pen.apply(y[i], count[i]);
+      if (p.r.bias) y[i] += bias[i];
+      y[i] = (mask >> ((c0 & 31) + i) & 1u) ? y[i] : -__builtin_inff();
+      if (BF) y[i] = bf16_rne(y[i]);
+      const float sc = p.greedy ? y[i] : __builtin_fmaf(y[i], p.kappa, noise[i]);
+      if (i < have) best = max_u64(best, argmax_key(sc, (uint32_t)(c0 + i)));
+    }
+    char* const at = (char*)p.out + ((b * p.M + p.k) * V + c0) * LB;
+    if (have == 4) {
+      base_t d;
+      if constexpr (BF) {
+        d[0] = join_bf16(y[0], y[1]);
+        d[1] = join_bf16(y[2], y[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(y[i]);
+      }
+      __builtin_nontemporal_store(d, (base_t*)at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < have) {
+          if constexpr (BF) ((uint16_t*)at)[i] = (uint16_t)(__float_as_uint(y[i]) >> 16);
+          else ((float*)at)[i] = y[i];
+        }
+    }
+  }
+  best = max_u64(best, __shfl_xor(best, 4));
+  best = max_u64(best, __shfl_xor(best, 8));
+  best = max_row_lanes(best);
+  if (lane < kFewRows) lds_key[wave][lane] = best;
+  __syncthreads();
+  if (tid < kFewRows && tid < p.B)
+    __hip_atomic_fetch_max(p.keys + ((p.k % kStepSlots) * kStepGroups + tile % kStepGroups) * p.B + tid,
+                           max_u64(max_u64(lds_key[0][tid], lds_key[1][tid]), max_u64(lds_key[2][tid], lds_key[3][tid])),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 namespace {
 template <bool WBF, bool BF, int RT>
 hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
@@ -708,7 +938,16 @@ hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 template <bool WBF, bool BF>
+hipError_t rule_few_form(const RuleStepParams& p, hipStream_t s) {
+  hipLaunchKernelGGL((rule_few_kernel<WBF, BF>), dim3((unsigned)((p.V + kStepCols - 1) / kStepCols)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+template <bool WBF, bool BF>
 hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
+  // Row tiles a workgroup, for five steps at V = 129280, rank 256, in bf16: 16
+  // rows 102 us with one, 115 with four; 32 rows 127 with two, 133 with four;
+  // 64 rows 245, 217 and 174 us with one, two and four.
+  if (p.B <= kFewRows) return rule_few_form<WBF, BF>(p, s);
   if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
   if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
   return rule_step_form<WBF, BF, 4>(p, s);

@@ -346,6 +346,18 @@ def test_draft_under_rules(native, B, M, V, L, r, ldt, wdt, T):
     _check_draft(c, tok, rows, T, 77, 2, 5)
 
 
+@pytest.mark.parametrize("T", [0.0, 0.9])
+@pytest.mark.parametrize("B,M,V,L,r,ldt,wdt", [
+    (4, 4, 777, 30, 33, BF16, BF16), (1, 3, 2050, 20, 1, F32, F32), (2, 3, 515, 9, 130, F32, F32), (4, 3, 1030, 40, 1000, F32, BF16),
+    (3, 3, 65, 9, 258, BF16, F32), (4, 5, 3, 6, 7, F32, F32), (5, 3, 1001, 20, 10, BF16, BF16), (7, 3, 999, 30, 64, F32, F32),
+    (16, 2, 2000, 30, 300, F32, BF16), (9, 2, 520, 8, 40, BF16, F32), (12, 4, 97, 5, 13, F32, F32), (5, 2, 9000, 64, 512, BF16, BF16),
+    (20, 3, 265, 7, 300, F32, F32), (32, 2, 1999, 20, 72, BF16, F32), (40, 3, 1001, 20, 130, F32, F32), (70, 2, 130, 9, 24, BF16, F32)])
+def test_draft_of_more_sizes_under_rules(native, B, M, V, L, r, ldt, wdt, T):
+    c = _draft_case(B, M, V, L, r, ldt, wdt, mask=("each", "row", "none")[(B + M) % 3], bias=("row", "shared", "none")[V % 3])
+    tokens, rows = _draft(c, T=T, seed=5, position_offset=2, batch_offset=1)
+    _check_draft(c, tokens, rows, T=T, seed=5, pos=2, bat=1)
+
+
 def test_draft_without_rules_is_the_plain_draft(native):
     c = _draft_case(4, 5, 4096, -1, 64, BF16, BF16, mask="none", bias="none", penalties=False)
     for T in (0.0, 0.9):
