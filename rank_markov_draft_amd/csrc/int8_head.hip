@@ -196,17 +196,23 @@ typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // rows of the output 
 // Otherwise (tiles bound by the head's stream) all of a chunk's fragments are
 // read at once, so that their latency is paid once a chunk.
 //
-// DIRECT needs rows of the head in whole 16-byte pieces; otherwise its pieces
-// go through registers by unaligned loads.
-template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, bool DIRECT, bool OBF>
+// PIECE: the head goes straight to LDS 16 bytes a lane where its rows are
+// whole 16-byte pieces, else 4 bytes a lane where they are whole words, else
+// through registers by unaligned loads, a chunk ahead (0).  Whole calls, in us,
+// by pieces of 16 bytes, words and registers: 37 rows at V = 32003, d = 2056
+// (2048 for the first) 19, 20, 26; at V = 129280, d = 5124 (5120) 1 row 114,
+// 148, 159; 128 rows 141, 181, 211; 320 rows 228, 278, 388.
+template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, int PIECE, bool OBF>
 __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams p, int row_tiles, int tiles) {
   constexpr int NW = WM * WN, THREADS = 64 * NW;
   constexpr int BM = 32 * MI * WM, BN = 32 * NJ * WN, BK = (int)kInt8K;
   constexpr int STAGE = (BM + BN) * BK;
-  // load instructions of a chunk, 8 rows each, per wave
-  constexpr int PA = BM / 8 / NW, PB = DIRECT ? BN / 8 / NW : 0, PER = PA + PB;
+  constexpr bool DIRECT = PIECE != 0;
+  // load instructions of a chunk per wave, of 8 rows each (2 of the head's by words)
+  constexpr int RB = PIECE == 4 ? 2 : 8, PA = BM / 8 / NW, PB = DIRECT ? BN / RB / NW : 0, PER = PA + PB;
   constexpr int REGS = DIRECT ? 1 : BN * 8 / THREADS;    // pieces of the head a thread moves itself
   static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "whole load instructions per wave");
+  static_assert(PIECE != 4 || RB * NW % 8 == 0, "a lane's swizzle is the same for all its rows");
   static_assert(DIRECT || (STAGES == 2 && !AHEAD), "register pieces are one chunk ahead");
   static_assert((STAGES - 1) * PER < 64, "wait count");
   // a wave's part of the output on its way to memory: ER rows x 32 NJ columns
@@ -243,19 +249,27 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
   // the position l % 8 of row l / 8 (which holds piece l % 8 ^ row % 8)
   const uint32_t row8 = 8u * (uint32_t)wave + (uint32_t)(lane >> 3);
   const uint32_t q16 = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
-  const uint32_t offa = row8 * (uint32_t)p.ldx + q16, offb = row8 * (uint32_t)p.d + q16;
+  const uint32_t offa = row8 * (uint32_t)p.ldx + q16;
+  // by words: rows 2 (wave + j NW) and the next, lane l word l % 32 of a row
+  const uint32_t row2 = 2u * (uint32_t)wave + (uint32_t)(lane >> 5);
+  const uint32_t offb = PIECE == 4 ? row2 * (uint32_t)p.d + 16u * ((uint32_t)(lane >> 2 & 7) ^ (row2 & 7)) + 4u * (uint32_t)(lane & 3)
+                                   : row8 * (uint32_t)p.d + q16;
   u32x4_t held[REGS];
   auto issue = [&](int g) __attribute__((always_inline)) {  // chunk g of the stream, in order
     const bool live = g < total;
     const uint32_t k0 = (uint32_t)lc * BK;
-    const uint32_t stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]) + 1024u * (uint32_t)wave;
+    const uint32_t stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]);
 #pragma unroll
     for (int j = 0; j < PA; ++j)
-      load_lds16(ba, live ? offa + (uint32_t)(8 * NW * j) * (uint32_t)p.ldx + k0 : kBufferOob, stage + 1024u * NW * j);
+      load_lds16(ba, live ? offa + (uint32_t)(8 * NW * j) * (uint32_t)p.ldx + k0 : kBufferOob,
+                 stage + 1024u * (uint32_t)(wave + NW * j));
 #pragma unroll
-    for (int j = 0; j < PB; ++j)
-      load_lds16(bb, live ? offb + (uint32_t)(8 * NW * j) * (uint32_t)p.d + k0 : kBufferOob,
-                 stage + BM * BK + 1024u * NW * j);
+    for (int j = 0; j < PB; ++j) {
+      const uint32_t off = live ? offb + (uint32_t)(RB * NW * j) * (uint32_t)p.d + k0 : kBufferOob;
+      const uint32_t to = stage + BM * BK + (uint32_t)(RB * BK) * (uint32_t)(wave + NW * j);
+      if constexpr (PIECE == 4) load_lds4(bb, off, to);
+      else load_lds16(bb, off, to);
+    }
     if constexpr (!DIRECT) {
 #pragma unroll
       for (int j = 0; j < REGS; ++j) {
@@ -433,7 +447,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_head_kernel(Int8HeadParams 
 }
 
 namespace {
-template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, bool DIRECT>
+template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, int PIECE>
 hipError_t head_go(const Int8HeadParams& p, bool obf, int groups, hipStream_t s) {
   constexpr int BM = 32 * MI * WM, BN = 32 * NJ * WN;
   const int64_t rt = (p.rows + BM - 1) / BM, tiles = rt * ((p.V + BN - 1) / BN);
@@ -442,10 +456,10 @@ hipError_t head_go(const Int8HeadParams& p, bool obf, int groups, hipStream_t s)
   if ((tiles / groups + 1) * (p.ldx / kInt8K) > 0x3FFFFFFF) return hipErrorNotSupported;
   const dim3 grid((unsigned)(tiles < groups ? tiles : groups)), block(64 * WM * WN);
   if (obf)
-    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, DIRECT, true>), grid, block, 0, s, p, (int)rt,
+    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, PIECE, true>), grid, block, 0, s, p, (int)rt,
                        (int)tiles);
   else
-    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, DIRECT, false>), grid, block, 0, s, p, (int)rt,
+    hipLaunchKernelGGL((int8_head_kernel<MI, NJ, WM, WN, STAGES, AHEAD, PIECE, false>), grid, block, 0, s, p, (int)rt,
                        (int)tiles);
   return hipGetLastError();
 }
@@ -487,24 +501,30 @@ int pick_form(const Form (&forms)[N], int64_t rows, int64_t V, int num_cus) {
 }
 }  // namespace
 
+namespace {
+template <int PIECE>
+hipError_t head_direct(const Int8HeadParams& p, bool out_bf16, int num_cus, hipStream_t s) {
+  switch (pick_form(kDirect, p.rows, p.V, num_cus)) {
+    case 0: return head_go<1, 1, 1, 4, 4, false, PIECE>(p, out_bf16, num_cus, s);
+    case 1: return head_go<1, 1, 2, 4, 4, false, PIECE>(p, out_bf16, num_cus, s);
+    case 2: return head_go<1, 2, 2, 4, 3, false, PIECE>(p, out_bf16, num_cus, s);
+    case 3: return head_go<2, 2, 2, 4, 3, true, PIECE>(p, out_bf16, num_cus, s);
+    case 4: return head_go<3, 2, 2, 4, 2, true, PIECE>(p, out_bf16, num_cus, s);
+    case 5: return head_go<4, 2, 2, 4, 2, true, PIECE>(p, out_bf16, num_cus, s);
+    default: return head_go<5, 2, 2, 4, 2, true, PIECE>(p, out_bf16, num_cus, s);
+  }
+}
+}  // namespace
+
 hipError_t launch_int8_head(const Int8HeadParams& p, bool out_bf16, int num_cus, hipStream_t s) {
   if (num_cus < 1 || p.d > kInt8MaxInner || p.ldx % kInt8K != 0 || p.ldx < p.d) return hipErrorNotSupported;
-  if (p.d % 16 == 0 && (uintptr_t)p.wq % 16 == 0) {
-    switch (pick_form(kDirect, p.rows, p.V, num_cus)) {
-      case 0: return head_go<1, 1, 1, 4, 4, false, true>(p, out_bf16, num_cus, s);
-      case 1: return head_go<1, 1, 2, 4, 4, false, true>(p, out_bf16, num_cus, s);
-      case 2: return head_go<1, 2, 2, 4, 3, false, true>(p, out_bf16, num_cus, s);
-      case 3: return head_go<2, 2, 2, 4, 3, true, true>(p, out_bf16, num_cus, s);
-      case 4: return head_go<3, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
-      case 5: return head_go<4, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
-      default: return head_go<5, 2, 2, 4, 2, true, true>(p, out_bf16, num_cus, s);
-    }
-  }
+  if (p.d % 16 == 0 && (uintptr_t)p.wq % 16 == 0) return head_direct<16>(p, out_bf16, num_cus, s);
+  if (p.d % 4 == 0 && (uintptr_t)p.wq % 4 == 0) return head_direct<4>(p, out_bf16, num_cus, s);
   switch (pick_form(kStaged, p.rows, p.V, num_cus)) {
-    case 0: return head_go<1, 1, 2, 4, 2, false, false>(p, out_bf16, 2 * num_cus, s);
-    case 1: return head_go<2, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
-    case 2: return head_go<3, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
-    default: return head_go<4, 2, 2, 4, 2, false, false>(p, out_bf16, num_cus, s);
+    case 0: return head_go<1, 1, 2, 4, 2, false, 0>(p, out_bf16, 2 * num_cus, s);
+    case 1: return head_go<2, 2, 2, 4, 2, false, 0>(p, out_bf16, num_cus, s);
+    case 2: return head_go<3, 2, 2, 4, 2, false, 0>(p, out_bf16, num_cus, s);
+    default: return head_go<4, 2, 2, 4, 2, false, 0>(p, out_bf16, num_cus, s);
   }
 }
 

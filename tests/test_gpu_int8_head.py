@@ -96,7 +96,7 @@ def test_quantize_rows_views_and_outputs(native):
     (1, 1, 1), (1, 129, 16), (2, 7, 5), (3, 300, 130), (1, 1000, 5120), (16, 257, 64), (31, 128, 128), (32, 127, 144),
     (33, 515, 272), (64, 256, 256), (65, 1001, 2064), (96, 640, 384), (128, 129, 128), (129, 511, 640), (160, 300, 400),
     (192, 520, 128), (200, 999, 96), (256, 256, 1024), (257, 700, 48), (320, 1030, 176), (330, 257, 1232),
-    (513, 383, 80), (700, 130, 16), (37, 2003, 2056), (5, 1300, 33), (130, 140, 4099), (1, 40000, 96)])
+    (513, 383, 80), (700, 130, 16), (2, 9, 4), (33, 200, 12), (70, 131, 516), (150, 1000, 124), (400, 259, 2052), (37, 2003, 2056), (5, 1300, 33), (130, 140, 4099), (1, 40000, 96)])
 def test_head_against_64_bits(native, rows, V, d, out):
     x = _rows(rows, d, BF16 if (rows + d) % 2 else F32, rows + V + d)
     hq, hs = _head(V, d, V * 3 + d)
@@ -141,13 +141,14 @@ def test_head_views_outputs_and_workspace(native):
     buf = torch.full((25, V), 5.0, device="cuda")
     got = rmd.lm_head_logits_int8(x.cuda().view(4, 6, d), hq.cuda(), hs.cuda(), out=buf[:24].view(4, 6, V), workspace=ws)
     assert got.data_ptr() == buf.data_ptr() and torch.equal(buf[:24], want) and (buf[24] == 5).all()
-    # a strided head, and one that starts at an odd byte
+    # a strided head, and ones that start at an odd byte and at a word
     wide = torch.zeros(V, d + 32, dtype=torch.int8, device="cuda")
     wide[:, :d] = hq.cuda()
     assert torch.equal(rmd.lm_head_logits_int8(x.cuda(), wide[:, :d], hs.cuda()), want)
-    odd = torch.zeros(V * d + 1, dtype=torch.int8, device="cuda")
-    odd[1:] = hq.cuda().view(-1)
-    assert torch.equal(rmd.lm_head_logits_int8(x.cuda(), odd[1:].view(V, d), hs.cuda()), want)
+    for off in (1, 4):
+        odd = torch.zeros(V * d + off, dtype=torch.int8, device="cuda")
+        odd[off:] = hq.cuda().view(-1)
+        assert torch.equal(rmd.lm_head_logits_int8(x.cuda(), odd[off:].view(V, d), hs.cuda()), want)
     # an output that starts at an odd element
     flat = torch.empty(24 * V + 1, device="cuda", dtype=BF16)
     got = rmd.lm_head_logits_int8(x.cuda(), hq.cuda(), hs.cuda(), out=flat[1:].view(24, V))
@@ -238,13 +239,13 @@ def test_int8_head_feeds_the_draft(native):
     assert torch.equal(proc.cpu().argmax(-1), tok.cpu())
 
 
-@pytest.mark.parametrize("d", [144, 151])
+@pytest.mark.parametrize("d", [144, 148, 151])
 @pytest.mark.parametrize("rows,V", [(5, 200), (40, 300), (64, 70000), (65, 70000), (192, 70001), (250, 70000), (320, 70100),
                                     (512, 33000), (321, 70000)])
 def test_every_tile_form(native, rows, V, d):
     """Sizes on both sides of the rule that picks the tile, heads read straight
-    into LDS (d a multiple of 16) and through registers; several tiles a
-    workgroup, and the last of them partial."""
+    into LDS by pieces (d a multiple of 16) or words (of 4) and through
+    registers; several tiles a workgroup, and the last of them partial."""
     x = _rows(rows, d, BF16, rows + d).cuda()
     hq, hs = (t.cuda() for t in _head(V, d, V))
     for out in (F32, BF16):
