@@ -307,7 +307,8 @@ dspark_status_t dspark_markov_quantize_rows(const void* x, dspark_dtype_t dtype,
  *   logits         device, [B, M, V] output, logits_dtype; must not overlap
  *                  an input.
  * Any d from 1 to 131072 (the integer sum's range; above: DSPARK_ERR_UNSUPPORTED), any V and alignment;
- * heads with d a multiple of 16 and a 16-byte aligned head_q are read fastest.
+ * heads with d a multiple of 16 and a 16-byte aligned head_q are read fastest,
+ * then those with d a multiple of 4 and a 4-byte aligned one.
  * B*M*V == 0 is a successful no-op.  The workspace must hold
  * dspark_markov_lm_head_int8_workspace_bytes(...) bytes (no zero fill needed). */
 size_t dspark_markov_lm_head_int8_workspace_bytes(int64_t B, int64_t M, int64_t d);
@@ -389,6 +390,12 @@ dspark_status_t dspark_markov_process_block_backward(const void* grad_processed,
  * offsets as in dspark_markov_sample_block.  A row with nothing above -inf to
  * draw from gets token -1; its next position then has an id outside [0, V) as
  * predecessor, so no bias.  M = 1 is the single-token form.
+ * Greedy calls in bf16 with B <= 64, M <= 16, at most 512 columns a compute
+ * unit and no per-request biases run as one persistent launch, as
+ * dspark_markov_sample_block's do, and share its failure behaviour: if its
+ * workgroups do not meet within a second (another stream holds compute units)
+ * every token is -1, dspark_markov_read_device_error reports it, and until
+ * then such calls on this workspace return -1 tokens.
  *   processed_logits  device, [B, M, V] output (the processed rows); must not
  *                     overlap an input.
  * V up to 2^30.  The workspace must hold

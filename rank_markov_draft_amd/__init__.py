@@ -659,14 +659,20 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
                                   logit_bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
                                   seed: int = 0, position_offset: int = 0, batch_offset: int = 0,
                                   tokens_out: torch.Tensor | None = None, logits_out: torch.Tensor | None = None,
-                                  workspace: Workspace | None = None):
+                                  workspace: Workspace | None = None, check: bool = False):
     """sample_block_tokens under the rules of process_block_logits: position k
     draws from the processed corrected logits, and the tokens drawn before it
     count as outputs beside ``history`` (which ends with
     first_prev_token_ids).  Returns ``(tokens [B, M], processed [B, M, V])``.
     A row left with nothing above -inf gets token -1 (the position after it
     then has no bias).  M = 1 with ``position_offset`` is the single-token
-    form, for masks that depend on the tokens drawn."""
+    form, for masks that depend on the tokens drawn.
+
+    Greedy bf16 drafts of up to 64 rows without per-request biases run as one
+    persistent launch that needs every compute unit within a second, as
+    sample_block_tokens' do: if another stream holds some for longer, every
+    token is -1 and read_device_error(workspace) raises.  ``check=True``
+    synchronises after the call and raises at once."""
     _check_weights(w1, w2)
     B, M, V = _block(base_logits, None, "base_logits")
     if tuple(first_prev_token_ids.shape) != (B,):
@@ -701,4 +707,6 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
                wtag, rules, B, M, V, r, T, int(seed) & (2**64 - 1), int(position_offset), int(batch_offset),
                _ptr(tokens_out), _ptr(logits_out), workspace.ptr, workspace.nbytes)
     _lib.check(st, "sample_block_tokens_processed")
+    if check:
+        read_device_error(workspace)
     return tokens_out, logits_out

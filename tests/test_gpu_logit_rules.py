@@ -556,11 +556,14 @@ def test_greedy_chain_failure_is_reported(native):
     ws = rmd.Workspace(4, 5, 4096, 64, sample=True, processed=True)
     want = _draft(c, workspace=ws)
     ws.set_chain_test_hook(True)
+    with pytest.raises(_lib.DsparkError, match="DEVICE"):
+        _draft(c, workspace=ws, check=True)
     assert (_draft(c, workspace=ws)[0] == -1).all()
     ws.set_chain_test_hook(False)
     assert (_draft(c, workspace=ws)[0] == -1).all()
     with pytest.raises(_lib.DsparkError, match="DEVICE"):
         rmd.read_device_error(ws)
+    assert torch.equal(_draft(c, workspace=ws, check=True)[0], want[0])
     again = _draft(c, workspace=ws)
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
 
