@@ -23,14 +23,20 @@ __device__ __forceinline__ Penalty penalty_of(const RuleSet& r, int64_t b) {
                  r.frequency != nullptr || r.presence != nullptr};
 }
 
-// The same for eight bf16 values whose counts stand in a word of bytes (0: not
-// seen, n: n - 1 times among the outputs), without a branch: some of them were
-// seen.  The quotient is the product with the rounded reciprocal, corrected
-// once by its residue: that is the division to within its last bit of fp32
-// (and almost always to its own rounding), 2^-16 of a step of the bf16 result.
-// The fixup puts in what a division gives for infinities, NaN and zeros.
-__device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p) {
-  const float inv = 1.0f / p.repetition;
+// The reciprocal that penalise8 divides by; zero where it must not be used (a
+// penalty so far from one that residues would overflow or underflow).
+__device__ __forceinline__ float quotient_factor(float repetition) {
+  return repetition > 0x1p-100f && repetition < 0x1p100f ? 1.0f / repetition : 0.0f;
+}
+
+// Penalty::apply for eight bf16 values whose counts stand in a word of bytes
+// (0: not seen, n: n - 1 times among the outputs), without a branch: some of
+// them were seen.  The quotient is the product with the rounded reciprocal,
+// corrected once by its residue: that is the division to within its last bit
+// of fp32 (and almost always to its own rounding), 2^-16 of a step of the bf16
+// result.  The fixup puts in what a division gives for infinities, NaN and
+// zeros.
+__device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p, float inv) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float n = (float)((uint32_t)(n8 >> (8 * i)) & 255u);

@@ -134,7 +134,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   __shared__ __attribute__((aligned(16))) uint8_t lds_n[RULES ? kMaxRows * kCols : 16];
   __shared__ __attribute__((aligned(16))) float lds_bias[RULES ? kCols : 4];
   __shared__ __attribute__((aligned(16))) uint32_t lds_mask[RULES ? kMaxGroups * kGroupRows * kWaves : 4];
-  __shared__ float lds_pen[RULES ? kMaxRows * 3 : 1];
+  __shared__ float lds_pen[RULES ? kMaxRows * 4 : 1];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar branches
@@ -326,9 +326,11 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
     static_assert(kMaxRows * kWaves == kThreads, "one table word per thread");
     for (int i = tid; i < kMaxRows * kCols / 16; i += kThreads) *(u32x4_t*)&lds_n[16 * i] = u32x4_t{0u, 0u, 0u, 0u};
     if (tid < B) {
-      lds_pen[3 * tid] = p.rule_set.repetition ? p.rule_set.repetition[tid] : 1.0f;
-      lds_pen[3 * tid + 1] = p.rule_set.frequency ? p.rule_set.frequency[tid] : 0.0f;
-      lds_pen[3 * tid + 2] = p.rule_set.presence ? p.rule_set.presence[tid] : 0.0f;
+      const Penalty pen = penalty_of(p.rule_set, tid);
+      lds_pen[4 * tid] = pen.repetition;
+      lds_pen[4 * tid + 1] = pen.frequency;
+      lds_pen[4 * tid + 2] = pen.presence;
+      lds_pen[4 * tid + 3] = quotient_factor(pen.repetition);
     }
     if (tid < kCols) {
       const uint32_t v = vbeg + (uint32_t)tid;
@@ -532,12 +534,13 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
           for (int i = 0; i < 8; ++i) x[i] = (i & 1) ? bf16_hi(ow[i >> 1]) : bf16_lo(ow[i >> 1]);
           const uint64_t n8 = *(const uint64_t*)&lds_n[b * kCols + colw];
           if (n8 != 0) {
-            const Penalty pen{lds_pen[3 * b], lds_pen[3 * b + 1], lds_pen[3 * b + 2], p.rule_set.repetition != nullptr,
+            const float factor = lds_pen[4 * b + 3];
+            const Penalty pen{lds_pen[4 * b], lds_pen[4 * b + 1], lds_pen[4 * b + 2], p.rule_set.repetition != nullptr,
                               p.rule_set.frequency != nullptr || p.rule_set.presence != nullptr};
             // a byte of 255 (bit 0 of a byte is left where all eight were set): that count is in memory
             uint64_t full = n8 & (n8 >> 4);
             full &= full >> 2;
-            if (full & (full >> 1) & 0x0101010101010101ull) {
+            if ((full & (full >> 1) & 0x0101010101010101ull) || factor == 0.0f) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const uint32_t n = (uint32_t)(n8 >> (8 * i)) & 255u;
@@ -547,21 +550,23 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
                                                                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
               }
             } else {
-              penalise8(x, n8, pen);
+              penalise8(x, n8, pen, factor);
             }
           }
           if (p.rule_set.bias != nullptr) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] += lds_bias[colw + i];
           }
-          if (p.rule_set.mask != nullptr) {
-            const uint32_t m8 = ((const uint8_t*)&lds_mask[gc * kGroupRows * kWaves + n16 * kWaves])[colw >> 3];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (m8 >> i & 1u) ? x[i] : -__builtin_inff();
-          }
+          const bool masked = p.rule_set.mask != nullptr;
+          const uint32_t m8 = masked ? ((const uint8_t*)&lds_mask[gc * kGroupRows * kWaves + n16 * kWaves])[colw >> 3] : 0u;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             ow[q] = pack_bf16x2(x[2 * q], x[2 * q + 1]);
+            if (masked) {  // -inf into the halves whose bit is clear
+              const uint32_t keep = ((uint32_t)__builtin_amdgcn_sbfe((int)m8, 2 * q, 1) & 0xFFFFu) |
+                                    ((uint32_t)__builtin_amdgcn_sbfe((int)m8, 2 * q + 1, 1) & 0xFFFF0000u);
+              ow[q] = (ow[q] & keep) | (0xFF80FF80u & ~keep);
+            }
             __asm__("" : "+v"(ow[q]));
             sum += x[2 * q] + x[2 * q + 1];
             const uint32_t c2 = pair_order_codes(ow[q]);

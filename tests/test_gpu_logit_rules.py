@@ -525,6 +525,24 @@ def test_greedy_chain_under_rules(native, B, M, V, L, r, bias, mask):
     assert rmd.read_device_error(ws) == 0
 
 
+def test_greedy_chain_with_penalties_far_from_one(native):
+    """Repetition penalties whose reciprocal is no number to divide by: with no
+    bias in the way the chain's rows are those of the rules alone."""
+    rep = torch.tensor([1e-39, 1e-35, 1e35, 3e38, float("inf"), 0.0, 1e-45, 2.0], device="cuda")
+    B, M, V, r = len(rep), 1, 1024, 16
+    g = torch.Generator(device="cuda").manual_seed(11)
+    base = torch.randn(B, M, V, device="cuda", generator=g).to(BF16)
+    base[:, :, ::7] = torch.tensor([float("inf"), -float("inf"), 0.0, -0.0, 3e38, 1e-38, float("nan")], device="cuda").to(BF16).repeat(21)
+    w = torch.zeros(V, r, dtype=BF16, device="cuda")
+    first = torch.zeros(B, dtype=torch.int64, device="cuda")
+    kw = dict(history=torch.arange(0, V, 2, device="cuda").repeat(B, 1), repetition_penalty=rep,
+              presence_penalty=torch.full((B,), 0.5, device="cuda"))
+    _, rows = rmd.sample_block_tokens_processed(base, first, w, w, 0.0, **kw)
+    want = rmd.process_block_logits(base, **kw)
+    same = (rows == want) | (torch.isnan(rows) & torch.isnan(want))
+    assert same.all(), (~same).nonzero()[:5]
+
+
 def test_greedy_chain_counts_past_a_byte(native):
     """Counts around 254, where the chain's byte ends, and tokens drawn at that edge."""
     B, M, V = 4, 6, 512
