@@ -131,9 +131,13 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   // Rules: counts and biases of the workgroup's columns, mask words of each
   // group's staged rows, and each row's penalties.
   constexpr int kCols = 32 * kWaves;
-  __shared__ __attribute__((aligned(16))) uint8_t lds_n[RULES ? kMaxRows * kCols : 16];
+  // (rows of counts 8 words further round the banks, so that 16 rows are read
+  // without conflict; a block of four rows' mask words by columns, then rows,
+  // and the blocks four words apart, for the same)
+  constexpr int kNPitch = kCols + 32, kMaskBlock = 4 * kWaves + 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds_n[RULES ? kMaxRows * kNPitch : 16];
   __shared__ __attribute__((aligned(16))) float lds_bias[RULES ? kCols : 4];
-  __shared__ __attribute__((aligned(16))) uint32_t lds_mask[RULES ? kMaxGroups * kGroupRows * kWaves : 4];
+  __shared__ __attribute__((aligned(16))) uint32_t lds_mask[RULES ? kMaxGroups * kGroupRows / 4 * kMaskBlock : 4];
   __shared__ float lds_pen[RULES ? kMaxRows * 4 : 1];
 
   const int tid = threadIdx.x;
@@ -238,11 +242,11 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   if constexpr (RULES) bw_mask = buffer_words(p.rule_set.mask, p.rule_set.mask != nullptr ? (uint32_t)p.mask_bytes : 0u);
   auto load_mask = [&](int gg, int kd) __attribute__((always_inline)) {
     if constexpr (RULES) {
-      const int row = 4 * (wave - 4) + (lane >> 4), word = (int)(vbeg / 32u) + (lane & 15), b = gg * rpg + row;
+      const int row = 4 * (wave - 4) + (lane & 3), word = (int)(vbeg / 32u) + (lane >> 2), b = gg * rpg + row;
       const bool ok = row < rpg && b < B && kd < M && word < (V + 31) / 32;
       const uint32_t off = 4u * ((uint32_t)b * (uint32_t)p.rule_set.mask_stride_b + (uint32_t)kd * (uint32_t)p.rule_set.mask_stride_m +
                                  (uint32_t)word);
-      load_lds4(bw_mask, ok ? off : kBufferOob, lds_address(&lds_mask[gg * kGroupRows * kWaves + 64 * (wave - 4)]));
+      load_lds4(bw_mask, ok ? off : kBufferOob, lds_address(&lds_mask[(gg * kGroupRows / 4 + wave - 4) * kMaskBlock]));
     }
   };
 
@@ -275,7 +279,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
     if (g == 0 && g4 == 0 && row_ok) p.tokens[(uint32_t)(b * M + kt)] = t;
     if constexpr (RULES) {
       if (penalise && g4 == 0 && row_ok && t >= (int64_t)vbeg && t < (int64_t)vend) {
-        uint8_t& n = lds_n[b * kCols + (int)(t - vbeg)];
+        uint8_t& n = lds_n[b * kNPitch + (int)(t - vbeg)];
         uint32_t* const big = p.counts + (int64_t)b * V + t;
         if (n >= 254) {
           if (n == 255) __hip_atomic_fetch_add(big, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -324,7 +328,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   if constexpr (RULES) {
     // a thread a word of the table: 32 columns of a row
     static_assert(kMaxRows * kWaves == kThreads, "one table word per thread");
-    for (int i = tid; i < kMaxRows * kCols / 16; i += kThreads) *(u32x4_t*)&lds_n[16 * i] = u32x4_t{0u, 0u, 0u, 0u};
+    for (int i = tid; i < kMaxRows * kNPitch / 16; i += kThreads) *(u32x4_t*)&lds_n[16 * i] = u32x4_t{0u, 0u, 0u, 0u};
     if (tid < B) {
       const Penalty pen = penalty_of(p.rule_set, tid);
       lds_pen[4 * tid] = pen.repetition;
@@ -350,7 +354,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
         for (int i = 0; i < 32; ++i)
           if (bits >> i & 1u) {
             const uint32_t n = c[i >> 2][i & 3];
-            lds_n[b * kCols + 32 * (tid % kWaves) + i] = (uint8_t)(n < 254u ? n + 1u : 255u);
+            lds_n[b * kNPitch + 32 * (tid % kWaves) + i] = (uint8_t)(n < 254u ? n + 1u : 255u);
           }
       }
     }
@@ -532,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
           float x[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[i] = (i & 1) ? bf16_hi(ow[i >> 1]) : bf16_lo(ow[i >> 1]);
-          const uint64_t n8 = *(const uint64_t*)&lds_n[b * kCols + colw];
+          const uint64_t n8 = *(const uint64_t*)&lds_n[b * kNPitch + colw];
           if (n8 != 0) {
             const float factor = lds_pen[4 * b + 3];
             const Penalty pen{lds_pen[4 * b], lds_pen[4 * b + 1], lds_pen[4 * b + 2], p.rule_set.repetition != nullptr,
@@ -558,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
             for (int i = 0; i < 8; ++i) x[i] += lds_bias[colw + i];
           }
           const bool masked = p.rule_set.mask != nullptr;
-          const uint32_t m8 = masked ? ((const uint8_t*)&lds_mask[gc * kGroupRows * kWaves + n16 * kWaves])[colw >> 3] : 0u;
+          const uint32_t m8 = masked ? ((const uint8_t*)&lds_mask[(gc * kGroupRows / 4 + (n16 >> 2)) * kMaskBlock + 4 * (colw >> 5) + (n16 & 3)])[colw >> 3 & 3] : 0u;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             ow[q] = pack_bf16x2(x[2 * q], x[2 * q + 1]);
@@ -589,7 +593,16 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
             key = max(key, max(klo, khi));
           }
         }
-        if (vbeg + (uint32_t)colw < vend) atomicMax(&lds_key[gc][n16], key);
+        int row = n16;
+        if constexpr (RULES) {
+          // Counted anew: as a value kept through the loop the address goes to
+          // scratch, and its reload waits for every load and store in flight
+          // (64 x 5 rows without a rule 85 us so, 73 us as here).
+          uint32_t all;
+          __asm__ volatile("s_mov_b32 %0, -1" : "=s"(all));
+          row = (int)(__builtin_amdgcn_mbcnt_hi(all, __builtin_amdgcn_mbcnt_lo(all, 0u)) & 15u);
+        }
+        if (vbeg + (uint32_t)colw < vend) atomicMax(&lds_key[gc][row], key);
       }
     }
 
