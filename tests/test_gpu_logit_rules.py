@@ -495,6 +495,47 @@ def test_rules_and_draft_in_a_graph(native):
         assert torch.equal(got[0], eager) and torch.equal(got[1], et) and torch.equal(got[2], er)
 
 
+@pytest.mark.parametrize("B", [3, 20])
+def test_two_graphs_share_a_workspace(native, B):
+    """The 8-bit head and a greedy draft in the chain as one graph, a draft by
+    steps (no penalty: no table) as another, replayed in turn on one workspace
+    with eager calls between."""
+    M, V, L, r, d = 4, 2048, 64, 16, 192
+    c = _draft_case(B, M, V, L, r, BF16, BF16, mask="each", bias="shared")
+    kw, first, w1, w2 = c.kw(), torch.from_numpy(c.first).cuda(), c.w1.cuda(), c.w2.cuda()
+    plain = dict(token_mask=kw["token_mask"], logit_bias=kw["logit_bias"])
+    g = torch.Generator(device="cuda").manual_seed(B)
+    hidden = torch.randn(B, M, d, device="cuda", generator=g).to(BF16)
+    hq, hs = rmd.quantize_rows(torch.randn(V, d, device="cuda", generator=g) * 0.2)
+    ws = rmd.Workspace(B, M, V, r, sample=True, processed=True, int8_hidden=d)
+
+    def one(h, **more):
+        base = rmd.lm_head_logits_int8(h, hq, hs, out_dtype=BF16, **more)
+        return (base,) + rmd.sample_block_tokens_processed(base, first, w1, w2, 0.0, **kw, **more)
+
+    def two(h, **more):
+        base = rmd.lm_head_logits_int8(h, hq, hs, out_dtype=torch.float32, **more)
+        return (base,) + rmd.sample_block_tokens_processed(base, first, w1, w2, 0.6, seed=4, **plain, **more)
+
+    graphs = []
+    for f in (one, two):
+        f(hidden, workspace=ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = f(hidden, workspace=ws)
+        graphs.append((f, graph, out))
+    for k in range(6):
+        hidden.copy_(torch.randn(hidden.shape, device="cuda", generator=g))
+        kw["history"].copy_(torch.randint(0, V, (B, L), device="cuda", generator=g))
+        f, graph, out = graphs[(k + k // 3) % 2]
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(out, f(hidden.clone())):
+            assert torch.equal(got, want)
+        f(hidden, workspace=ws)
+    assert rmd.read_device_error(ws) == 0
+
+
 def test_rules_past_31_bits(native):
     """More than 2^31 logits: the last rows are right."""
     B, M, V = 520, 4, 1040001
