@@ -363,7 +363,7 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   for (int64_t k = 0; k < M; ++k) {
     p.k = k;
     p.k_abs = (uint32_t)(position_offset + k);
-    e = dspark::launch_rule_step(p, logits_dtype == DSPARK_BF16, weight_dtype == DSPARK_BF16, s);
+    e = dspark::launch_rule_step(p, logits_dtype == DSPARK_BF16, weight_dtype == DSPARK_BF16, cus > 0 ? cus : 1, s);
     if (e != hipSuccess) return device_failure(e, "rule step launch");
   }
   e = dspark::launch_rule_choose(keys, B, M, sampled_tokens, s);

@@ -94,7 +94,7 @@ struct RuleStepParams {
   uint32_t seed_hi;
   bool greedy;
 };
-hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, hipStream_t s);
+hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, int num_cus, hipStream_t s);
 
 // tokens[b, M - 1] = the column of the row's best key, -1 when its score is -inf.
 hipError_t launch_rule_choose(const uint64_t* keys, int64_t B, int64_t M, int64_t* tokens, hipStream_t s);

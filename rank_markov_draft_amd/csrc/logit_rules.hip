@@ -371,7 +371,7 @@ hipError_t launch_rule_table(const TableParams& p, hipStream_t s) {
 }
 
 namespace {
-constexpr int kFewRows = 4;                          // rows of the kernel for few of them
+constexpr int kFewRows = 4;                          // rows of a workgroup of the small form
 constexpr int kStepWaveCols = 64;                    // columns of a wave
 constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
 constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
@@ -718,7 +718,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The same step for up to four rows.  With the rows on the matrix
+// The same step by four rows a workgroup.  With the rows on the matrix
 // instruction's 16 columns most lanes would hold rows that do not exist and
 // the others 16 columns each, a long stretch of code for a lone wave of a SIMD;
 // here a wave's 64 columns by four rows are sixteen 4 x 4 blocks, and a lane
@@ -729,10 +729,11 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
 // their own rows touch a line each (rank 256 in fp32, V = 129280, drafts of
 // five: 1 row 162 us so, 134 us as here, 146 us by the kernel above; 4 rows
 // 189, 140 and 136 us).  Bound by latency where W2 is short: V = 50257 at rank
-// 64 in fp32 8.3 us a step, 12.2 us by the kernel above.  For 8 rows, two such
-// sets of blocks took 52 -> 71 us a draft (V = 32000, rank 64, bf16).
+// 64 in fp32 8.3 us a step, 12.2 us by the kernel above.  More rows take more
+// workgroups, each reading its columns of W2, from the XCD's L2; two sets of
+// blocks in one wave took 52 -> 71 us a draft instead (8 rows, V = 32000).
 template <bool WBF, bool BF>
-__global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p) {
+__global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int tiles, unsigned chunks) {
   constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;  // bytes of a weight, weights of a 16-byte piece
   constexpr int LB = BF ? 2 : 4, NP = 8;         // bytes of a logit, pieces of a line
   typedef uint32_t base_t __attribute__((ext_vector_type(LB), aligned(2)));
@@ -741,8 +742,10 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lane = tid & 63;
-  const int tile = (int)blockIdx.x;
-  const int64_t V = p.V, rank = p.rank, W = (V + 31) / 32, b = lane & 3;
+  const int tile = (int)(blockIdx.x / (8u * chunks)) * 8 + (int)(blockIdx.x % 8u);
+  const int64_t b0 = (int64_t)(blockIdx.x / 8u % chunks) * kFewRows;
+  if (tile >= tiles) return;
+  const int64_t V = p.V, rank = p.rank, W = (V + 31) / 32, b = b0 + (lane & 3);
   const int wc0 = tile * kStepCols + kStepWaveCols * wave, c0 = wc0 + (lane & ~3);  // V is at most 2^30
   const int left = (int)V - c0, have = left < 0 ? 0 : left < 4 ? left : 4;
   const int whole = (int)(rank / KE), lines = (whole + NP - 1) / NP;
@@ -935,8 +938,8 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p) {
   best = max_row_lanes(best);
   if (lane < kFewRows) lds_key[wave][lane] = best;
   __syncthreads();
-  if (tid < kFewRows && tid < p.B)
-    __hip_atomic_fetch_max(p.keys + ((p.k % kStepSlots) * kStepGroups + tile % kStepGroups) * p.B + tid,
+  if (tid < kFewRows && b0 + tid < p.B)
+    __hip_atomic_fetch_max(p.keys + ((p.k % kStepSlots) * kStepGroups + tile % kStepGroups) * p.B + b0 + tid,
                            max_u64(max_u64(lds_key[0][tid], lds_key[1][tid]), max_u64(lds_key[2][tid], lds_key[3][tid])),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -953,24 +956,34 @@ hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
 }
 template <bool WBF, bool BF>
 hipError_t rule_few_form(const RuleStepParams& p, hipStream_t s) {
-  hipLaunchKernelGGL((rule_few_kernel<WBF, BF>), dim3((unsigned)((p.V + kStepCols - 1) / kStepCols)), dim3(256), 0, s, p);
+  const int64_t tiles = (p.V + kStepCols - 1) / kStepCols, chunks = (p.B + kFewRows - 1) / kFewRows;
+  hipLaunchKernelGGL((rule_few_kernel<WBF, BF>), dim3((unsigned)((tiles + 7) / 8 * 8 * chunks)), dim3(256), 0, s, p, (int)tiles,
+                     (unsigned)chunks);
   return hipGetLastError();
 }
 template <bool WBF, bool BF>
-hipError_t rule_step_go(const RuleStepParams& p, hipStream_t s) {
+hipError_t rule_step_go(const RuleStepParams& p, int num_cus, hipStream_t s) {
+  // Four rows a workgroup while the device holds all of them at once (two a
+  // CU), or there are no more rows; otherwise the fewer readers of W2.  In us,
+  // drafts of five, so and by the kernel for row tiles: 250 workgroups (8 rows,
+  // V = 32000, rank 64, bf16) 40, 52; 256 (64 rows, V = 4000, rank 64, fp32)
+  // 47, 178; 500 (16 rows, V = 32000) 46, 55; 1010 (8 rows, V = 129280) 74, 58.
+  // Batches of more than a drafter's 64 rows keep the row tiles, and so one
+  // order of a row's sums however such a batch is cut.
+  const int64_t groups = (p.V + kStepCols - 1) / kStepCols * ((p.B + kFewRows - 1) / kFewRows);
+  if (p.B <= kFewRows || (p.B <= 64 && groups <= 2 * (int64_t)num_cus)) return rule_few_form<WBF, BF>(p, s);
   // Row tiles a workgroup, for five steps at V = 129280, rank 256, in bf16: 16
   // rows 102 us with one, 115 with four; 32 rows 127 with two, 133 with four;
   // 64 rows 245, 217 and 174 us with one, two and four.
-  if (p.B <= kFewRows) return rule_few_form<WBF, BF>(p, s);
   if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
   if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
   return rule_step_form<WBF, BF, 4>(p, s);
 }
 }  // namespace
 
-hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, hipStream_t s) {
-  if (weights_bf16) return logits_bf16 ? rule_step_go<true, true>(p, s) : rule_step_go<true, false>(p, s);
-  return logits_bf16 ? rule_step_go<false, true>(p, s) : rule_step_go<false, false>(p, s);
+hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, int num_cus, hipStream_t s) {
+  if (weights_bf16) return logits_bf16 ? rule_step_go<true, true>(p, num_cus, s) : rule_step_go<true, false>(p, num_cus, s);
+  return logits_bf16 ? rule_step_go<false, true>(p, num_cus, s) : rule_step_go<false, false>(p, num_cus, s);
 }
 
 __global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_t* __restrict__ slot, int64_t B, int64_t M,

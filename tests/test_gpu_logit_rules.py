@@ -358,6 +358,19 @@ def test_draft_of_more_sizes_under_rules(native, B, M, V, L, r, ldt, wdt, T):
     _check_draft(c, tokens, rows, T=T, seed=5, pos=2, bat=1)
 
 
+@pytest.mark.parametrize("T", [0.0, 0.8])
+@pytest.mark.parametrize("B,M,V,L,r,ldt,wdt", [
+    (16, 2, 33001, 20, 10, BF16, BF16), (8, 2, 66001, 30, 16, F32, F32), (13, 2, 40002, 9, 40, F32, BF16), (16, 2, 33000, 5, 13, BF16, F32),
+    (32, 2, 16510, 20, 72, BF16, F32), (20, 2, 26305, 9, 33, F32, F32), (32, 2, 16640, 9, 520, F32, BF16), (40, 2, 13201, 7, 24, BF16, BF16),
+    (64, 2, 8501, 9, 130, F32, BF16), (70, 3, 8001, 5, 7, F32, F32), (33, 2, 15003, 30, 300, BF16, F32)])
+def test_draft_of_many_columns_and_rows(native, B, M, V, L, r, ldt, wdt, T):
+    """Sizes that more than fill the device four rows a workgroup: they run by row tiles."""
+    assert -(-V // 256) * -(-B // 4) > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    c = _draft_case(B, M, V, L, r, ldt, wdt, mask=("each", "row", "none")[(B + M) % 3], bias=("row", "shared", "none")[V % 3])
+    tokens, rows = _draft(c, T=T, seed=6, position_offset=1, batch_offset=3)
+    _check_draft(c, tokens, rows, T=T, seed=6, pos=1, bat=3)
+
+
 def test_draft_without_rules_is_the_plain_draft(native):
     c = _draft_case(4, 5, 4096, -1, 64, BF16, BF16, mask="none", bias="none", penalties=False)
     for T in (0.0, 0.9):
