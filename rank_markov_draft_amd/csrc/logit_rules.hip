@@ -963,6 +963,8 @@ hipError_t rule_few_form(const RuleStepParams& p, hipStream_t s) {
 }
 template <bool WBF, bool BF>
 hipError_t rule_step_go(const RuleStepParams& p, int num_cus, hipStream_t s) {
+  // whether the device holds all workgroups of so many rows at once
+  auto fits = [&](int64_t rows) { return (p.V + kStepCols - 1) / kStepCols * ((p.B + rows - 1) / rows) <= 2 * (int64_t)num_cus; };
   // Four rows a workgroup while the device holds all of them at once (two a
   // CU), or there are no more rows; otherwise the fewer readers of W2.  In us,
   // drafts of five, so and by the kernel for row tiles: 250 workgroups (8 rows,
@@ -970,13 +972,16 @@ hipError_t rule_step_go(const RuleStepParams& p, int num_cus, hipStream_t s) {
   // 47, 178; 500 (16 rows, V = 32000) 46, 55; 1010 (8 rows, V = 129280) 74, 58.
   // Batches of more than a drafter's 64 rows keep the row tiles, and so one
   // order of a row's sums however such a batch is cut.
-  const int64_t groups = (p.V + kStepCols - 1) / kStepCols * ((p.B + kFewRows - 1) / kFewRows);
-  if (p.B <= kFewRows || (p.B <= 64 && groups <= 2 * (int64_t)num_cus)) return rule_few_form<WBF, BF>(p, s);
-  // Row tiles a workgroup, for five steps at V = 129280, rank 256, in bf16: 16
-  // rows 102 us with one, 115 with four; 32 rows 127 with two, 133 with four;
-  // 64 rows 245, 217 and 174 us with one, two and four.
-  if (p.B <= 16) return rule_step_form<WBF, BF, 1>(p, s);
-  if (p.B <= 32) return rule_step_form<WBF, BF, 2>(p, s);
+  if (p.B <= kFewRows || (p.B <= 64 && fits(kFewRows))) return rule_few_form<WBF, BF>(p, s);
+  // Row tiles a workgroup: the fewest with which the device holds all
+  // workgroups at once, as each waits for the same loads however few its
+  // tiles; at most four, and no more than there are.  In us, drafts of five at
+  // rank 256 in bf16 with one, two and four: 32 rows, V = 32000 72, 100, 105;
+  // 64 rows, V = 32000 93, 101, 157, V = 65536 157, 122, 160, V = 100000 220,
+  // 204, 176; 256 rows, V = 16000 157, 130, 161; 54 rows, V = 29826 in fp32
+  // 143, 145, 247.
+  if (p.B <= 16 || fits(16)) return rule_step_form<WBF, BF, 1>(p, s);
+  if (p.B <= 32 || fits(32)) return rule_step_form<WBF, BF, 2>(p, s);
   return rule_step_form<WBF, BF, 4>(p, s);
 }
 }  // namespace

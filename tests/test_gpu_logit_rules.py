@@ -362,7 +362,8 @@ def test_draft_of_more_sizes_under_rules(native, B, M, V, L, r, ldt, wdt, T):
 @pytest.mark.parametrize("B,M,V,L,r,ldt,wdt", [
     (16, 2, 33001, 20, 10, BF16, BF16), (8, 2, 66001, 30, 16, F32, F32), (13, 2, 40002, 9, 40, F32, BF16), (16, 2, 33000, 5, 13, BF16, F32),
     (32, 2, 16510, 20, 72, BF16, F32), (20, 2, 26305, 9, 33, F32, F32), (32, 2, 16640, 9, 520, F32, BF16), (40, 2, 13201, 7, 24, BF16, BF16),
-    (64, 2, 8501, 9, 130, F32, BF16), (70, 3, 8001, 5, 7, F32, F32), (33, 2, 15003, 30, 300, BF16, F32)])
+    (64, 2, 8501, 9, 130, F32, BF16), (70, 3, 8001, 5, 7, F32, F32), (33, 2, 15003, 30, 300, BF16, F32),
+    (64, 2, 70001, 9, 8, BF16, BF16), (300, 2, 16385, 5, 16, F32, BF16), (130, 2, 16400, 5, 9, BF16, F32), (100, 2, 33001, 5, 8, F32, F32)])
 def test_draft_of_many_columns_and_rows(native, B, M, V, L, r, ldt, wdt, T):
     """Sizes that more than fill the device four rows a workgroup: they run by row tiles."""
     assert -(-V // 256) * -(-B // 4) > 2 * torch.cuda.get_device_properties(0).multi_processor_count
