@@ -154,8 +154,8 @@ __device__ __forceinline__ void bias8(const RuleSet& r, int64_t i, int n, float 
 
 }  // namespace
 
-// A workgroup: T columns of one request, its positions in groups of R, a
-// thread 8 columns of a group's rows (and U such columns) at a time, so that
+// A workgroup: T columns of one request, a span of its positions in groups of
+// R, a thread 8 columns of a group's rows (and U such columns) at a time, so that
 // R * U vectors are in flight while the bias and the table's bits of a column
 // are read once for its R rows.
 //
@@ -163,14 +163,17 @@ __device__ __forceinline__ void bias8(const RuleSet& r, int64_t i, int n, float 
 // its first row join the table for good; the few within it only set their
 // bit in `any`, and a column whose bit is set looks them up one by one.
 template <bool BF, bool BWD, int R, int U>
-__global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p, int T, int tiles, bool track,
-                                                                   bool keep_counts) {
+__global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p, int T, int tiles, int64_t span,
+                                                                   bool track, bool keep_counts) {
   extern __shared__ uint32_t rule_lds[];
   uint32_t* const any = rule_lds;                                        // T / 32 words
   uint32_t* const seen = rule_lds + T / 32;                              // T / 32 words
   uint32_t* const counts = keep_counts ? rule_lds + T / 16 : nullptr;    // T words
   __shared__ uint32_t blk[R];  // columns of the group's tokens k0 + 1 .. k0 + R - 1 relative to the tile, at 1 .. R - 1
-  const int64_t b = blockIdx.x / (unsigned)tiles;
+  // request, and positions kb .. ke - 1 of it (spans of a multiple of R)
+  const unsigned spans = (unsigned)((p.M + span - 1) / span), which = blockIdx.x / (unsigned)tiles;
+  const int64_t b = which / spans;
+  const int64_t kb = (int64_t)(which % spans) * span, ke = p.M - kb < span ? p.M : kb + span;
   const int64_t t0 = (int64_t)(blockIdx.x % (unsigned)tiles) * T;
   const int tn = (int)(p.V - t0 < T ? p.V - t0 : T);
   const int tid = threadIdx.x;
@@ -190,26 +193,35 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         m8[u][q] = 0xFFu;
-        if (c < tn && k0 + q < p.M) {
+        if (c < tn && k0 + q < ke) {
           raw[u][q] = load8<BF, true>(in + (q * p.V + c) * ES, tn - c);
           if (mask) m8[u][q] = mask[4 * q * p.r.mask_stride_m + c / 8];
         }
       }
     }
   };
-  fetch(0, 8 * tid);  // in flight while the history is walked
+  fetch(kb, 8 * tid);  // in flight while the history is walked
   if (track) {
     const int words = keep_counts ? T / 16 + T : T / 16;
     for (int i = tid; i < words; i += kRuleThreads) rule_lds[i] = 0u;
     __syncthreads();
     count_history(p.r, b, t0, tn, seen, counts);
+    // the block's tokens before those that the first group takes below
+    for (int64_t i = ids ? 1 + tid : kb; i <= kb - R; i += kRuleThreads) {
+      const int64_t id = ids[i];
+      const uint64_t c = (uint64_t)id - (uint64_t)t0;
+      if (id >= 0 && c < (uint64_t)tn) {
+        atomicOr(&seen[c >> 5], 1u << (c & 31));
+        if (counts) atomicAdd(&counts[c], 1u);
+      }
+    }
     __syncthreads();
     for (int i = tid; i < T / 32; i += kRuleThreads) any[i] = seen[i];
     __syncthreads();
   }
-  for (int64_t k0 = 0; k0 < p.M; k0 += R) {
+  for (int64_t k0 = kb; k0 < ke; k0 += R) {
     if (ids) {
-      if (k0 > 0) __syncthreads();
+      if (k0 > kb) __syncthreads();
       for (int j = tid; j < 2 * R - 1; j += kRuleThreads) {  // tokens k0 - R + 1 .. k0 + R - 1
         const int64_t at = k0 - R + 1 + j;
         const int64_t id = at >= 1 && at < p.M ? ids[at] : -1;
@@ -225,12 +237,12 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
       }
       __syncthreads();
     }
-    const int rows = (int)(p.M - k0 < R ? p.M - k0 : R);
+    const int rows = (int)(ke - k0 < R ? ke - k0 : R);
     const int64_t first = (b * p.M + k0) * p.V + t0;
     const char* const lg = (const char*)p.logits + first * ES;
     char* const out = (char*)p.out + first * ES;
     for (int c0 = 8 * tid; c0 < tn; c0 += U * 8 * kRuleThreads) {
-      if (k0 > 0 || c0 > 8 * tid) fetch(k0, c0);
+      if (k0 > kb || c0 > 8 * tid) fetch(k0, c0);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int c = c0 + u * 8 * kRuleThreads;
@@ -305,20 +317,29 @@ hipError_t rules_go(const RulesParams& p, int num_cus, hipStream_t s) {
   while (T < 8192 && (double)T * p.M * (BF ? 2 : 4) < 0.4 * (8.0 * (track ? p.r.history_len : 0) + 36864)) T *= 2;
   while (T > 2048 && p.B * ((p.V + T - 1) / T) < 4 * (int64_t)num_cus) T /= 2;
   const int64_t tiles = (p.V + T - 1) / T;
-  if (p.B * tiles > 0x7FFFFFFF) return hipErrorNotSupported;
+  const int R = p.M == 1 ? 1 : (BWD && !BF) || p.M <= 4 ? 4 : 8;
+  // Few requests of many positions: spans of positions in workgroups of their
+  // own, each of which counts the tokens before it, up to four workgroups a CU
+  // (1 x 512 rows of 129280 in bf16, 1000 ids: 676 us as one span, 71 us so;
+  // the gradient 542 and 68; 4 x 256 rows of 32000 351 and 38).
+  int64_t spans = 4 * (int64_t)num_cus / (p.B * tiles);
+  spans = spans < 1 ? 1 : spans;
+  int64_t span = ((p.M + spans - 1) / spans + R - 1) / R * R;
+  spans = (p.M + span - 1) / span;
+  if (p.B > 0x7FFFFFFF / tiles || p.B * tiles > 0x7FFFFFFF / spans) return hipErrorNotSupported;
   const size_t lds = track ? (size_t)(T / 16 + (keep_counts ? T : 0)) * 4 : 0;
-  const dim3 grid((unsigned)(p.B * tiles)), block(kRuleThreads);
+  const dim3 grid((unsigned)(p.B * tiles * spans)), block(kRuleThreads);
   // Positions at a time (and vectors of columns): 1 (four), 4, 8, in us at V =
   // 129280 and 1024 ids: 256 x 1 bf16 43, 56, 56; 64 x 3 bf16 33, 30, 30; 128
   // x 8 bf16 138, 118, 110.  The gradient holds the logits of a hit beside
   // its values, which in fp32 leaves eight positions too few waves: 64 x 5 84,
   // 80, 89 and 128 x 8 244, 236, 253; in bf16 52, 47, 46 and 139, 110, 115.
-  if (p.M == 1)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 1, 4>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
-  else if ((BWD && !BF) || p.M <= 4)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 4, 1>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
+  if (R == 1)
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 1, 4>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
+  else if (R == 4)
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 4, 1>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
   else if constexpr (!BWD || BF)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 8, 1>), grid, block, lds, s, p, T, (int)tiles, track, keep_counts);
+    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 8, 1>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
   return hipGetLastError();
 }
 }  // namespace

@@ -82,7 +82,8 @@ class Case:
 
 
 SIZES = [(1, 1, 1, 0), (1, 1, 7, 1), (1, 1, 2048, 50), (2, 3, 2051, 5), (3, 2, 4096, 300), (5, 4, 1001, 64),
-         (4, 5, 8200, 2100), (1, 8, 16385, 9), (40, 2, 8191, 33), (130, 1, 8193, 20), (3, 3, 33, 2049), (600, 1, 40, 3)]
+         (4, 5, 8200, 2100), (1, 8, 16385, 9), (40, 2, 8191, 33), (130, 1, 8193, 20), (3, 3, 33, 2049), (600, 1, 40, 3),
+         (1, 67, 301, 20), (2, 33, 97, 4), (3, 300, 40, 5), (1, 515, 65, 3), (1100, 17, 50, 6)]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
