@@ -66,7 +66,9 @@ __device__ __forceinline__ void lds_barrier() {
 // inline assembly so that the compiler does not track these loads: it would
 // otherwise make later LDS reads of every wave wait for all of them.  Their
 // completion is waited for explicitly (wait_vmcnt) before the data is used.
-// M0 is saved and restored around the load.
+// M0 is saved and restored around the load, which may read it one wait state
+// after its write at the earliest: the compiler does not insert those into an
+// assembly string, so the strings hold an s_nop.
 struct BufferWords {
   u32x4_t w;  // V# of a raw buffer: base, stride 0, size in bytes, 32-bit data format
 };
@@ -81,18 +83,18 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // uniform value the compiler keeps in a vector register still reaches m0.
 __device__ __forceinline__ void load_lds16(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 // The same with 4 bytes a lane (lane l's at lds + 4 l).
 __device__ __forceinline__ void load_lds4(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 __device__ __forceinline__ void load_lds16_coherent(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc1 lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc1 lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(lds) : "memory");
 }
 
