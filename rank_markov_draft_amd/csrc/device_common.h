@@ -66,9 +66,11 @@ __device__ __forceinline__ void lds_barrier() {
 // inline assembly so that the compiler does not track these loads: it would
 // otherwise make later LDS reads of every wave wait for all of them.  Their
 // completion is waited for explicitly (wait_vmcnt) before the data is used.
-// M0 is saved and restored around the load, which may read it one wait state
-// after its write at the earliest: the compiler does not insert those into an
-// assembly string, so the strings hold an s_nop.
+// M0 is saved and restored around the load.  The load may read M0 one wait
+// state after its write at the earliest, and its buffer's words five after a
+// vector instruction wrote them, as one that reads a spilled word back from a
+// lane does right ahead of the string; the compiler does not insert those into
+// a string, so it holds them: two scalar moves and an s_nop of three.
 struct BufferWords {
   u32x4_t w;  // V# of a raw buffer: base, stride 0, size in bytes, 32-bit data format
 };
@@ -83,18 +85,18 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 // uniform value the compiler keeps in a vector register still reaches m0.
 __device__ __forceinline__ void load_lds16(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 // The same with 4 bytes a lane (lane l's at lds + 4 l).
 __device__ __forceinline__ void load_lds4(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dword %1, %2, 0 offen lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
 }
 __device__ __forceinline__ void load_lds16_coherent(const BufferWords& r, uint32_t off, uint32_t lds) {
   uint32_t saved;
-  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc1 lds\n\ts_mov_b32 m0, %0"
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 2\n\tbuffer_load_dwordx4 %1, %2, 0 offen sc1 lds\n\ts_mov_b32 m0, %0"
                    : "=&s"(saved) : "v"(off), "s"(r.w), "s"(lds) : "memory");
 }
 

@@ -16,6 +16,9 @@ from rank_markov_draft_amd import _lib
 OBJDUMP = "/opt/rocm/llvm/bin/llvm-objdump"
 # wait states between an instruction that writes M0 and a load to LDS, which reads it
 M0_STATES = 1
+# and between a vector instruction that writes a scalar register (a spilled one read back from a
+# lane) and a memory instruction that reads it, as the words of its buffer
+SCALAR_STATES = 5
 
 
 def _wait_states(ins):
@@ -71,3 +74,16 @@ def test_loads_to_lds_follow_the_write_of_m0(kernels):
             assert states is None or states >= M0_STATES, f"{where[1]}: {body[i - 1]}; {ins}"
             loads += 1
     assert loads > 0
+
+
+def test_loads_to_lds_follow_their_buffer_words(kernels):
+    for where, body in kernels.items():
+        for i, ins in _lds_loads(body):
+            first, last = (int(n) for n in re.search(r"s\[(\d+):(\d+)\]", ins).groups())
+
+            def writes(p):
+                lane = re.match(r"v_read(?:first)?lane_b32 s(\d+),", p)
+                return lane and first <= int(lane[1]) <= last
+
+            states = _states_since(body, i, writes)
+            assert states is None or states >= SCALAR_STATES, f"{where[1]}: {body[max(0, i - 6):i + 1]}"
