@@ -23,28 +23,48 @@ __device__ __forceinline__ Penalty penalty_of(const RuleSet& r, int64_t b) {
                  r.frequency != nullptr || r.presence != nullptr};
 }
 
-// The reciprocal that penalise8 divides by; zero where it must not be used (a
-// penalty so far from one that residues would overflow or underflow).
-__device__ __forceinline__ float quotient_factor(float repetition) {
-  return repetition > 0x1p-100f && repetition < 0x1p100f ? 1.0f / repetition : 0.0f;
+// The quotient of a bf16 value y and a penalty from the penalty's reciprocal in
+// two words: y * high + y * low with one rounding at the end.  That is the
+// division's own rounding for all 2^30 pairs of significands of y and of the
+// penalty but two, whose penalties are left out.  Where no step leaves the
+// normal range it does not depend on the exponents either: penalties within
+// 2^-20 .. 2^20, and values that are zero or within 2^-50 .. 2^100, so that
+// quotients stay below 2^120, the products with the low word above 2^-126, and
+// neither infinities nor NaN come up.  Others are divided.
+struct Reciprocal {
+  float high, low;  // high: zero for a penalty to divide by
+};
+__device__ __forceinline__ Reciprocal reciprocal_of(float repetition) {
+  const uint32_t s = __float_as_uint(repetition) & 0x7FFFFFu;
+  if (!(repetition >= 0x1p-20f && repetition <= 0x1p20f) || s == 0x50AB43u || s == 0x792863u) return {0.0f, 0.0f};
+  const float high = 1.0f / repetition;
+  return {high, __builtin_fmaf(-repetition, high, 1.0f) / repetition};
+}
+
+// Whether all of eight packed bf16 values are in that range.
+__device__ __forceinline__ bool plain_dividends(const uint32_t (&w)[4]) {
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  constexpr uint32_t kLow = (127 - 50) << 7, kHigh = (127 + 100) << 7;
+  u16x2_t low = {0xFFFF, 0xFFFF}, high = {0, 0};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const u16x2_t m = __builtin_bit_cast(u16x2_t, w[q] & 0x7FFF7FFFu);
+    low = __builtin_elementwise_min(low, (u16x2_t)(m - (uint16_t)1));  // zeros come last
+    high = __builtin_elementwise_max(high, m);
+  }
+  return min((uint32_t)low[0], (uint32_t)low[1]) >= kLow - 1 && max((uint32_t)high[0], (uint32_t)high[1]) <= kHigh;
 }
 
 // Penalty::apply for eight bf16 values whose counts stand in a word of bytes
 // (0: not seen, n: n - 1 times among the outputs), without a branch: some of
-// them were seen.  The quotient is the product with the rounded reciprocal,
-// corrected once by its residue: that is the division to within its last bit
-// of fp32 (and almost always to its own rounding), 2^-16 of a step of the bf16
-// result.  The fixup puts in what a division gives for infinities, NaN and
-// zeros.
-__device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p, float inv) {
+// them were seen.  For plain_dividends, and a reciprocal that is not zero.
+__device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Penalty& p, const Reciprocal& r) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float n = (float)((uint32_t)(n8 >> (8 * i)) & 255u);
     float y = x[i];
     if (p.repeat) {
-      const float q = y * inv;
-      const float d = __builtin_amdgcn_div_fixupf(__builtin_fmaf(__builtin_fmaf(-q, p.repetition, y), inv, q), p.repetition, y);
-      y = y > 0.0f ? d : y * p.repetition;
+      y = y > 0.0f ? __builtin_fmaf(y, r.high, y * r.low) : y * p.repetition;
       y = n > 0.0f ? y : x[i];
     }
     if (p.count) {

@@ -138,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
   __shared__ __attribute__((aligned(16))) uint8_t lds_n[RULES ? kMaxRows * kNPitch : 16];
   __shared__ __attribute__((aligned(16))) float lds_bias[RULES ? kCols : 4];
   __shared__ __attribute__((aligned(16))) uint32_t lds_mask[RULES ? kMaxGroups * kGroupRows / 4 * kMaskBlock : 4];
-  __shared__ float lds_pen[RULES ? kMaxRows * 4 : 1];
+  __shared__ float lds_pen[RULES ? kMaxRows * 5 : 1];
 
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);  // uniform: scalar branches
@@ -334,7 +334,9 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
       lds_pen[4 * tid] = pen.repetition;
       lds_pen[4 * tid + 1] = pen.frequency;
       lds_pen[4 * tid + 2] = pen.presence;
-      lds_pen[4 * tid + 3] = quotient_factor(pen.repetition);
+      const Reciprocal factor = reciprocal_of(pen.repetition);
+      lds_pen[4 * tid + 3] = factor.high;
+      lds_pen[4 * kMaxRows + tid] = factor.low;
     }
     if (tid < kCols) {
       const uint32_t v = vbeg + (uint32_t)tid;
@@ -538,13 +540,13 @@ __global__ __launch_bounds__(kThreads) void markov_chain_greedy_bf16(ChainParams
           for (int i = 0; i < 8; ++i) x[i] = (i & 1) ? bf16_hi(ow[i >> 1]) : bf16_lo(ow[i >> 1]);
           const uint64_t n8 = *(const uint64_t*)&lds_n[b * kNPitch + colw];
           if (n8 != 0) {
-            const float factor = lds_pen[4 * b + 3];
+            const Reciprocal factor{lds_pen[4 * b + 3], lds_pen[4 * kMaxRows + b]};
             const Penalty pen{lds_pen[4 * b], lds_pen[4 * b + 1], lds_pen[4 * b + 2], p.rule_set.repetition != nullptr,
                               p.rule_set.frequency != nullptr || p.rule_set.presence != nullptr};
             // a byte of 255 (bit 0 of a byte is left where all eight were set): that count is in memory
             uint64_t full = n8 & (n8 >> 4);
             full &= full >> 2;
-            if ((full & (full >> 1) & 0x0101010101010101ull) || factor == 0.0f) {
+            if ((full & (full >> 1) & 0x0101010101010101ull) || factor.high == 0.0f || !plain_dividends(ow)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const uint32_t n = (uint32_t)(n8 >> (8 * i)) & 255u;
