@@ -412,6 +412,13 @@ __device__ __forceinline__ int64_t drawn_token(const uint64_t* slot, int64_t b, 
   return token_of(key);
 }
 
+// The score of a processed value at a temperature.  Infinite values stay as
+// they are: their product with a kappa of zero (an infinite temperature) would
+// be NaN, and outrank every other score.
+__device__ __forceinline__ float score_of(float x, float kappa, float noise) {
+  return __builtin_fabsf(x) == __builtin_inff() ? x : __builtin_fmaf(x, kappa, noise);
+}
+
 // 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
 template <int EB>
 __device__ __forceinline__ u32x4_t weights16(const char* row, int64_t k, int64_t rank) {
@@ -722,7 +729,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float sc = p.greedy ? x[4 * j + e] : __builtin_fmaf(x[4 * j + e], p.kappa, g[e]);
+          const float sc = p.greedy ? x[4 * j + e] : score_of(x[4 * j + e], p.kappa, g[e]);
           if (4 * j % VC + e < have[4 * j / VC]) best = max_u64(best, argmax_key(sc, (uint32_t)(v + e)));
         }
       }
@@ -931,7 +938,7 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
       if (p.r.bias) y[i] += bias[i];
       y[i] = (mask >> ((c0 & 31) + i) & 1u) ? y[i] : -__builtin_inff();
       if (BF) y[i] = bf16_rne(y[i]);
-      const float sc = p.greedy ? y[i] : __builtin_fmaf(y[i], p.kappa, noise[i]);
+      const float sc = p.greedy ? y[i] : score_of(y[i], p.kappa, noise[i]);
       if (i < have) best = max_u64(best, argmax_key(sc, (uint32_t)(c0 + i)));
     }
     char* const at = (char*)p.out + ((b * p.M + p.k) * V + c0) * LB;
