@@ -320,7 +320,8 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   p.rank = r;
   p.batch_offset = batch_offset;
   p.greedy = temperature < 1e-5;
-  p.kappa = p.greedy ? 0.0f : (float)(1.4426950408889634 / temperature);
+  // above zero at any temperature, so that an infinite logit's score is not NaN
+  p.kappa = p.greedy ? 0.0f : std::fmax((float)(1.4426950408889634 / temperature), 0x1p-149f);
   p.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
   p.seed_hi = (uint32_t)(seed >> 32);
   // Greedy drafts with bf16 logits and weights that the persistent chain can

@@ -88,7 +88,7 @@ struct RuleStepParams {
   int64_t rank;
   int64_t k;
   int64_t batch_offset;
-  float kappa;             // (float)(log2(e) / T); unused when greedy
+  float kappa;             // (float)(log2(e) / T), above zero; unused when greedy
   uint32_t k_abs;
   uint32_t seed_lo;
   uint32_t seed_hi;
@@ -96,7 +96,7 @@ struct RuleStepParams {
 };
 hipError_t launch_rule_step(const RuleStepParams& p, bool logits_bf16, bool weights_bf16, int num_cus, hipStream_t s);
 
-// tokens[b, M - 1] = the column of the row's best key, -1 when its score is -inf.
+// tokens[b, M - 1] = the column of the row's best key, -1 when it has none.
 hipError_t launch_rule_choose(const uint64_t* keys, int64_t B, int64_t M, int64_t* tokens, hipStream_t s);
 
 }  // namespace dspark

@@ -398,25 +398,20 @@ constexpr int kStepCols = 4 * kStepWaveCols;         // and of a workgroup
 constexpr int kStepRowBytes = 512;                   // gathered bytes of a W1 row in a chunk of the rank
 constexpr int kStepPitch = kStepRowBytes + 16;       // its pitch in LDS
 
-// The token of a row's best key of a slot, -1 when that is -inf.
+// The token of a row's best key of a slot.  Columns at -inf give no key, so
+// none (-1) means that nothing was left; a finite value whose score at a low
+// temperature is -inf gives one like any other.
 __device__ __forceinline__ int64_t token_of(const uint64_t (&key)[kStepGroups]) {
   uint64_t best = 0;
 #pragma unroll
   for (int g = 0; g < kStepGroups; ++g) best = max_u64(best, key[g]);
-  return (uint32_t)(best >> 32) > kNothingLeft32 ? key_index(best) : -1;
+  return best != 0 ? key_index(best) : -1;
 }
 __device__ __forceinline__ int64_t drawn_token(const uint64_t* slot, int64_t b, int64_t B) {
   uint64_t key[kStepGroups];
 #pragma unroll
   for (int g = 0; g < kStepGroups; ++g) key[g] = slot[g * B + b];
   return token_of(key);
-}
-
-// The score of a processed value at a temperature.  Infinite values stay as
-// they are: their product with a kappa of zero (an infinite temperature) would
-// be NaN, and outrank every other score.
-__device__ __forceinline__ float score_of(float x, float kappa, float noise) {
-  return __builtin_fabsf(x) == __builtin_inff() ? x : __builtin_fmaf(x, kappa, noise);
 }
 
 // 16 bytes of a weight row from element k on (EB bytes an element), zeros past its end.
@@ -729,8 +724,9 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float sc = p.greedy ? x[4 * j + e] : score_of(x[4 * j + e], p.kappa, g[e]);
-          if (4 * j % VC + e < have[4 * j / VC]) best = max_u64(best, argmax_key(sc, (uint32_t)(v + e)));
+          const float sc = p.greedy ? x[4 * j + e] : __builtin_fmaf(x[4 * j + e], p.kappa, g[e]);
+          if (4 * j % VC + e < have[4 * j / VC] && x[4 * j + e] != -__builtin_inff())
+            best = max_u64(best, argmax_key(sc, (uint32_t)(v + e)));
         }
       }
     }
@@ -938,8 +934,8 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
       if (p.r.bias) y[i] += bias[i];
       y[i] = (mask >> ((c0 & 31) + i) & 1u) ? y[i] : -__builtin_inff();
       if (BF) y[i] = bf16_rne(y[i]);
-      const float sc = p.greedy ? y[i] : score_of(y[i], p.kappa, noise[i]);
-      if (i < have) best = max_u64(best, argmax_key(sc, (uint32_t)(c0 + i)));
+      const float sc = p.greedy ? y[i] : __builtin_fmaf(y[i], p.kappa, noise[i]);
+      if (i < have && y[i] != -__builtin_inff()) best = max_u64(best, argmax_key(sc, (uint32_t)(c0 + i)));
     }
     char* const at = (char*)p.out + ((b * p.M + p.k) * V + c0) * LB;
     if (have == 4) {

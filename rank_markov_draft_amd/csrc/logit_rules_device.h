@@ -75,9 +75,8 @@ __device__ __forceinline__ void penalise8(float (&x)[8], uint64_t n8, const Pena
   }
 }
 
-// A processed score's order codes (16 bits for bf16 values, 32 for fp32) up to
-// these are -inf: nothing was left to draw.
+// The greedy chain's order codes (16 bits) up to this are -inf: nothing was
+// left to draw.
 constexpr uint32_t kNothingLeft16 = 0x007Fu;
-constexpr uint32_t kNothingLeft32 = 0x007FFFFFu;
 
 }  // namespace dspark

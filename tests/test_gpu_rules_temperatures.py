@@ -72,3 +72,22 @@ def test_infinities_are_drawn_first(native, B, V, T):
         assert np.array_equal(got[want != -2], want[want != -2])
 
 
+@pytest.mark.parametrize("T", [0.0, 0.1, 0.7, 1.5])
+@pytest.mark.parametrize("ldt,wdt", [(F32, F32), (BF16, BF16), (BF16, F32)])
+@pytest.mark.parametrize("B,V", SIZES)
+def test_the_types_lowest_value_can_be_drawn(native, B, V, ldt, wdt, T):
+    """Rows whose allowed tokens all hold the type's lowest value (an upstream
+    mask of that value): they are above -inf, so one of them is drawn, the
+    first, as the noise is lost beside them; one that holds more is drawn
+    before them."""
+    M, low = 2, torch.finfo(ldt).min
+    _, allowed, mask = _masked(B, M, V, ldt, B + V + 1)
+    x = torch.full((B, M, V), low, device="cuda").to(ldt)
+    x[0, 1, V // 2] = -4.0
+    w = torch.zeros(V, 8, dtype=wdt, device="cuda")
+    first = torch.zeros(B, dtype=torch.int64, device="cuda")
+    tok, rows = rmd.sample_block_tokens_processed(x, first, w, w, T, token_mask=mask, seed=5)
+    want = np.where(allowed.any(-1), allowed.argmax(-1), -1)
+    want[0, 1] = V // 2
+    assert np.array_equal(tok.cpu().numpy(), want)
+    assert torch.equal(rows > -float("inf"), torch.from_numpy(allowed).cuda())
