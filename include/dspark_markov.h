@@ -389,7 +389,9 @@ dspark_status_t dspark_markov_process_block_backward(const void* grad_processed,
  * outputs besides the history (which ends with first_prev).  Scores, noise and
  * offsets as in dspark_markov_sample_block, with the smallest positive number
  * for a log2(e)/T that rounds to zero; a processed logit of -inf is never
- * drawn.  A row with nothing above -inf to draw from gets token -1; its next position then has an id outside [0, V) as
+ * drawn.  A row's result does not depend on the others: a batch split across
+ * calls reproduces one whole call to the bit.  A row with nothing above -inf to
+ * draw from gets token -1; its next position then has an id outside [0, V) as
  * predecessor, so no bias.  M = 1 is the single-token form.
  * Greedy calls in bf16 with B <= 64, M <= 16, at most 512 columns a compute
  * unit and no per-request biases run as one persistent launch, as

@@ -65,8 +65,6 @@ __device__ __forceinline__ void count_history(const RuleSet& r, int64_t b, int64
 // Vectors of rows that start at any element (an odd vocabulary): the hardware
 // loads and stores 16 bytes at any address.
 typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 // 8 consecutive values of a row as they are stored.
 template <bool BF>
@@ -745,21 +743,28 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
 // The same step by four rows a workgroup.  With the rows on the matrix
 // instruction's 16 columns most lanes would hold rows that do not exist and
 // the others 16 columns each, a long stretch of code for a lone wave of a SIMD;
-// here a wave's 64 columns by four rows are sixteen 4 x 4 blocks, and a lane
-// ends up with four consecutive columns of one row: a vector of logits and a
-// block of noise.  Both operands go to registers, two lines of 128 bytes of a
-// row ahead of the products, and nothing waits at a barrier before the keys.
+// here a lane ends up with four consecutive columns of one row: a vector of
+// logits and a block of noise.  A row's sums are those of the kernel above to
+// the bit, so that a batch may be cut anywhere.  In bf16 that takes the same
+// instruction, whose order of the sum within its 32 elements no smaller one
+// has: the four rows stand four times on its columns, and a lane takes the
+// block of its own columns.  The fp32 instruction above sums its four elements
+// one after the other, as 4 x 4 blocks do that go through them in that order.
+// Both operands go to registers, two lines of 128 bytes of a row ahead of the
+// products, and nothing waits at a barrier before the keys.
 // W2 is loaded a line by eight lanes and turned through LDS: lanes loading
 // their own rows touch a line each (rank 256 in fp32, V = 129280, drafts of
-// five: 1 row 162 us so, 134 us as here, 146 us by the kernel above; 4 rows
-// 189, 140 and 136 us).  Bound by latency where W2 is short: V = 50257 at rank
-// 64 in fp32 8.3 us a step, 12.2 us by the kernel above.  More rows take more
+// five: 1 row 162 us so, 139 us as here, 146 us by the kernel above; 4 rows
+// 189, 143 and 136 us; in bf16 97 us a draft by 4 x 4 x 4 products, 83 us as
+// here).  Bound by latency where W2 is short: V = 50257 at rank 64 in fp32
+// 8.3 us a step, 12.2 us by the kernel above.  More rows take more
 // workgroups, each reading its columns of W2, from the XCD's L2; two sets of
 // blocks in one wave took 52 -> 71 us a draft instead (8 rows, V = 32000).
-template <bool WBF, bool BF>
+template <bool WBF, bool BF, bool RAGGED>
 __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int tiles, unsigned chunks) {
-  constexpr int WB = WBF ? 2 : 4, KE = 16 / WB;  // bytes of a weight, weights of a 16-byte piece
-  constexpr int LB = BF ? 2 : 4, NP = 8;         // bytes of a logit, pieces of a line
+  constexpr int WB = WBF ? 2 : 4, KE = 16 / WB, KI = 4 * KE;  // as above
+  constexpr int LB = BF ? 2 : 4, NP = 8;                      // bytes of a logit, pieces of a line (two steps of KI)
+  constexpr int NE = WBF ? 2 : NP;                            // pieces of a row's line that a lane supplies
   typedef uint32_t base_t __attribute__((ext_vector_type(LB), aligned(2)));
   __shared__ uint64_t lds_key[4][kFewRows];
   __shared__ __attribute__((aligned(16))) unsigned char lds_w[4][kStepWaveCols * 128];
@@ -772,7 +777,17 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
   const int64_t V = p.V, rank = p.rank, W = (V + 31) / 32, b = b0 + (lane & 3);
   const int wc0 = tile * kStepCols + kStepWaveCols * wave, c0 = wc0 + (lane & ~3);  // V is at most 2^30
   const int left = (int)V - c0, have = left < 0 ? 0 : left < 4 ? left : 4;
-  const int whole = (int)(rank / KE), lines = (whole + NP - 1) / NP;
+  const int steps = (int)((rank + KI - 1) / KI), lines = (steps + 1) / 2, pieces = (int)((rank + KE - 1) / KE);
+  // The last piece of a rank that is no whole number of them is loaded as the
+  // row's last 16 bytes and moved down when it is used, with zeros behind it.
+  auto piece_at = [&](int piece) __attribute__((always_inline)) { return RAGGED ? min(16 * piece, (int)rank * WB - 16) : 16 * piece; };
+  auto settle = [&](const u32x4_t& d, int piece) __attribute__((always_inline)) -> u32x4_t {
+    const int bits = 8 * (16 * piece - piece_at(piece)), n = bits & 63;
+    const uint64_t lo = bits < 64 ? (uint64_t)d[1] << 32 | d[0] : (uint64_t)d[3] << 32 | d[2];
+    const uint64_t hi = bits < 64 ? (uint64_t)d[3] << 32 | d[2] : 0u;
+    const uint64_t a = n ? lo >> n | hi << (64 - n) : lo, b = hi >> n;
+    return u32x4_t{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)};
+  };
   uint64_t key[kStepGroups];
   int64_t x = -1;  // the row's predecessor
   if (b < p.B) {
@@ -789,24 +804,30 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
     const int64_t v = wc0 + i < V ? wc0 + i : V - 1;
     return (const char*)p.w2 + v * rank * WB;
   };
-  const int pc = lane & 7, r8 = lane >> 3;
-  u32x4_t w[2][NP], e[2][NP];
+  const int pc = lane & 7, r8 = lane >> 3, n16 = lane & 15, g4 = lane >> 4;
+  u32x4_t w[2][NP], e[2][NE];
   auto fetch_w = [&](int l, u32x4_t (&d)[NP]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       d[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (NP * l + pc < whole) d[i] = *(const u32x4_any_t*)(row_of(8 * i + r8) + (NP * l + pc) * 16);
+      if (NP * l + pc < pieces) d[i] = *(const u32x4_any_t*)(row_of(8 * i + r8) + piece_at(NP * l + pc));
     }
   };
-  // the pieces of the lane's own row out of a line's loads, through the wave's
-  // own LDS (a wave's LDS accesses keep their order)
+  // a line's operands out of its loads, through the wave's own LDS (a wave's
+  // LDS accesses keep their order): bf16, piece 4 h + g4 of the rows that stand
+  // at n16 in blocks t = 0 .. 3, at 4 h + t; fp32, the lane's own row.  Pieces
+  // are swizzled so that rows read together fall on different banks.
   unsigned char* const mine = lds_w[wave];
+  auto block_row = [&](int t) __attribute__((always_inline)) { return 16 * (n16 >> 2) + 4 * t + (n16 & 3); };
   auto turn = [&](const u32x4_t (&d)[NP], u32x4_t (&a)[NP]) __attribute__((always_inline)) {
+    auto place = [&](int row, int piece) __attribute__((always_inline)) {
+      return (u32x4_t*)(mine + row * 128 + 16 * (piece ^ (WBF ? (row & 3) | (row >> 4 & 1) << 2 : row & 7)));
+    };
 #pragma unroll
-    for (int i = 0; i < NP; ++i) *(u32x4_t*)(mine + (8 * i + r8) * 128 + 16 * (pc ^ r8)) = d[i];
+    for (int i = 0; i < NP; ++i) *place(8 * i + r8, pc) = d[i];
     __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int q = 0; q < NP; ++q) a[q] = *(const u32x4_t*)(mine + lane * 128 + 16 * (q ^ (lane & 7)));
+    for (int q = 0; q < NP; ++q) a[q] = WBF ? *place(block_row(q & 3), 4 * (q >> 2) + g4) : *place(lane, q);
     __builtin_amdgcn_wave_barrier();
   };
   fetch_w(0, w[0]);
@@ -851,11 +872,12 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
     }
   }
   const char* const erow = (const char*)p.w1 + (x < 0 ? 0 : x) * rank * WB;
-  auto fetch_e = [&](int l, u32x4_t (&d)[NP]) __attribute__((always_inline)) {
+  auto fetch_e = [&](int l, u32x4_t (&d)[NE]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
+    for (int q = 0; q < NE; ++q) {
+      const int piece = NP * l + (WBF ? 4 * q + g4 : q);
       d[q] = u32x4_t{0u, 0u, 0u, 0u};
-      if (NP * l + q < whole && x >= 0) d[q] = *(const u32x4_any_t*)(erow + (NP * l + q) * 16);
+      if (piece < pieces && x >= 0) d[q] = *(const u32x4_any_t*)(erow + piece_at(piece));
     }
   };
   fetch_e(0, e[0]);
@@ -880,21 +902,23 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
     p.counts[b * V + x] = n;
     p.seen[b * W + (c0 >> 5)] = word | 1u << (x & 31);
   }
-  f32x4_t acc[4];
+  constexpr int NA = WBF ? 4 : 1;  // blocks of sums
+  f32x4_t acc[NA];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  auto multiply = [&](int q, const u32x4_t& wp, const u32x4_t& ep) __attribute__((always_inline)) {
+  for (int i = 0; i < NA; ++i) acc[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // a step of KI: in fp32 element j of each of its pieces in turn, as above
+  auto multiply = [&](const u32x4_t* wp, const u32x4_t* ep) __attribute__((always_inline)) {
     if constexpr (WBF) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const u32x2_t w2 = {wp[2 * h], wp[2 * h + 1]}, e2 = {ep[2 * h], ep[2 * h + 1]};
-        f32x4_t& d = acc[(2 * q + h) & 3];
-        d = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(s16x4_t, w2), __builtin_bit_cast(s16x4_t, e2), d, 0, 0, 0);
-      }
+      for (int t = 0; t < 4; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wp[t]),
+                                                         __builtin_bit_cast(bf16x8_t, ep[0]), acc[t], 0, 0, 0);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(wp[i]), __uint_as_float(ep[i]), acc[i], 0, 0, 0);
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          acc[0] = __builtin_amdgcn_mfma_f32_4x4x1f32(__uint_as_float(wp[g][j]), __uint_as_float(ep[g][j]), acc[0], 0, 0, 0);
     }
   };
   for (int l = 0; l < lines; l += 2) {
@@ -902,21 +926,28 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
     for (int h = 0; h < 2; ++h)
       if (l + h < lines) {
         u32x4_t a[NP];
-        turn(w[h], a);
+        if (RAGGED && l + h == lines - 1) {
 #pragma unroll
-        for (int q = 0; q < NP; ++q) multiply(q, a[q], e[h][q]);
+          for (int i = 0; i < NP; ++i)
+            if (NP * (l + h) + pc == pieces - 1) w[h][i] = settle(w[h][i], pieces - 1);
+#pragma unroll
+          for (int q = 0; q < NE; ++q)
+            if (NP * (l + h) + (WBF ? 4 * q + g4 : q) == pieces - 1) e[h][q] = settle(e[h][q], pieces - 1);
+        }
+        turn(w[h], a);
+        multiply(a, e[h]);
+        if (2 * (l + h) + 1 < steps) multiply(a + 4, e[h] + NE / 2);
         if (l + h + 2 < lines) {
           fetch_w(l + h + 2, w[h]);
           fetch_e(l + h + 2, e[h]);
         }
       }
   }
-  if (whole * KE < rank)  // the last elements of a rank that is no whole number of pieces
-    multiply(0, weights16<WB>(row_of(lane), (int64_t)whole * KE, rank),
-             x >= 0 ? weights16<WB>(erow, (int64_t)whole * KE, rank) : u32x4_t{0u, 0u, 0u, 0u});
   uint64_t best = 0;
   if (b < p.B && have > 0) {
-    const f32x4_t sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    f32x4_t sum = acc[0];  // of the block whose columns are the lane's
+#pragma unroll
+    for (int t = 1; t < NA; ++t) sum = n16 >> 2 == t ? acc[t] : sum;
     float y[4], noise[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (!p.greedy) {
       const Philox4 q = philox4x32_10((uint32_t)(c0 >> 2), p.k_abs, (uint32_t)p.batch_offset + (uint32_t)b, 0u, p.seed_lo,
@@ -981,8 +1012,11 @@ hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
 template <bool WBF, bool BF>
 hipError_t rule_few_form(const RuleStepParams& p, hipStream_t s) {
   const int64_t tiles = (p.V + kStepCols - 1) / kStepCols, chunks = (p.B + kFewRows - 1) / kFewRows;
-  hipLaunchKernelGGL((rule_few_kernel<WBF, BF>), dim3((unsigned)((tiles + 7) / 8 * 8 * chunks)), dim3(256), 0, s, p, (int)tiles,
-                     (unsigned)chunks);
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8 * chunks)), block(256);
+  if (p.rank % (WBF ? 8 : 4) == 0)
+    hipLaunchKernelGGL((rule_few_kernel<WBF, BF, false>), grid, block, 0, s, p, (int)tiles, (unsigned)chunks);
+  else
+    hipLaunchKernelGGL((rule_few_kernel<WBF, BF, true>), grid, block, 0, s, p, (int)tiles, (unsigned)chunks);
   return hipGetLastError();
 }
 template <bool WBF, bool BF>
@@ -992,11 +1026,11 @@ hipError_t rule_step_go(const RuleStepParams& p, int num_cus, hipStream_t s) {
   // Four rows a workgroup while the device holds all of them at once (two a
   // CU), or there are no more rows; otherwise the fewer readers of W2.  In us,
   // drafts of five, so and by the kernel for row tiles: 250 workgroups (8 rows,
-  // V = 32000, rank 64, bf16) 40, 52; 256 (64 rows, V = 4000, rank 64, fp32)
-  // 47, 178; 500 (16 rows, V = 32000) 46, 55; 1010 (8 rows, V = 129280) 74, 58.
-  // Batches of more than a drafter's 64 rows keep the row tiles, and so one
-  // order of a row's sums however such a batch is cut.
-  if (p.B <= kFewRows || (p.B <= 64 && fits(kFewRows))) return rule_few_form<WBF, BF>(p, s);
+  // V = 32000, rank 64, bf16) 39, 52; 256 (64 rows, V = 4000, rank 64, fp32)
+  // 47, 178; 500 (16 rows, V = 32000) 41, 55; 1010 (8 rows, V = 129280) 74, 58.
+  // Beyond a drafter's 64 rows it is not measured; rows of less than 16 bytes
+  // have no whole piece to load.  The form does not change a row's sums.
+  if (p.rank >= (WBF ? 8 : 4) && (p.B <= kFewRows || (p.B <= 64 && fits(kFewRows)))) return rule_few_form<WBF, BF>(p, s);
   // Row tiles a workgroup: the fewest with which the device holds all
   // workgroups at once, as each waits for the same loads however few its
   // tiles; at most four, and no more than there are.  In us, drafts of five at

@@ -2,8 +2,8 @@
 built library's gfx950 code (CPU only).
 
 The compiler inserts the wait states its own instructions need, and does not
-look into an assembly string.  The loads to LDS of device_common.h are such
-strings."""
+look into an assembly string.  The loads to LDS and the rounding conversion of
+device_common.h are such strings."""
 import os
 import re
 import shutil
@@ -19,6 +19,9 @@ M0_STATES = 1
 # and between a vector instruction that writes a scalar register (a spilled one read back from a
 # lane) and a memory instruction that reads it, as the words of its buffer
 SCALAR_STATES = 5
+# and between a matrix instruction of 2, 8 or 16 passes and a vector instruction that reads its
+# result, as the conversion in bf16_rne may
+MATRIX_STATES = {"4x4": 5, "16x16": 11, "32x32": 19}
 
 
 def _wait_states(ins):
@@ -87,3 +90,34 @@ def test_loads_to_lds_follow_their_buffer_words(kernels):
 
             states = _states_since(body, i, writes)
             assert states is None or states >= SCALAR_STATES, f"{where[1]}: {body[max(0, i - 6):i + 1]}"
+
+
+def _vectors(operands):
+    """Vector registers named in a text of operands."""
+    found = set()
+    for first, last, one in re.findall(r"\bv\[(\d+):(\d+)\]|\bv(\d+)\b", operands):
+        found.update(range(int(first), int(last) + 1) if first else [int(one)])
+    return found
+
+
+def test_conversions_follow_the_matrix_results_they_read(kernels):
+    conversions = 0
+    for where, body in kernels.items():
+        pending = []  # [registers, wait states since, wait states needed] in straight-line order
+        for ins in body:
+            name, _, operands = ins.partition(" ")
+            target, _, sources = operands.partition(",")
+            if name == "v_cvt_pk_bf16_f32" and sources.split(",")[0].strip() == "0":
+                conversions += 1
+                for regs, states, needed in pending:
+                    assert states >= needed or not regs & _vectors(sources), f"{where[1]}: {ins} after {states} wait states"
+            if name.startswith("v_") and not name.startswith("v_mfma"):
+                for p in pending:
+                    p[0] -= _vectors(target)
+            pending = [[r, s + _wait_states(ins), n] for r, s, n in pending if r and s < n]
+            shape = re.match(r"v_mfma_\w+?_(\d+x\d+)x", name)
+            if shape:
+                pending.append([_vectors(target), 0, MATRIX_STATES[shape[1]]])
+            if name in ("s_branch", "s_endpgm", "s_setpc_b64"):
+                pending = []
+    assert conversions > 0
