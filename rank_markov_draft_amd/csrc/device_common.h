@@ -53,6 +53,11 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// Workgroups of 256 threads that one launch takes: its threads are counted in
+// 32 bits, and a grid past that wraps around without an error.  Launchers cut
+// longer ones.
+constexpr int64_t kLaunchGroups = 0xFFFFFFFFll / 256;
+
 // Workgroup barrier for LDS data only.  __syncthreads() also orders global
 // memory at workgroup scope, which would wait for every load in flight.
 // Here each wave finishes its own LDS accesses (lgkmcnt); the buffer loads

@@ -300,7 +300,13 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   const bool table = dspark::rules_penalise(p.r) && (p.r.history != nullptr || M > 1);
   hipError_t e = hipSuccess;
   if (table) {
-    const dspark::TableParams t{p.r, seen, counts, keys, B, V};
+    dspark::TableParams t{};
+    t.r = p.r;
+    t.seen = seen;
+    t.counts = counts;
+    t.keys = keys;
+    t.B = B;
+    t.V = V;
     e = dspark::launch_rule_table(t, s);
     if (e != hipSuccess) return device_failure(e, "rule table launch");
   }

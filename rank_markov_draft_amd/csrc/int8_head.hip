@@ -150,12 +150,28 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_rows_any_kernel(Quanti
 }
 
 namespace {
+// `launch(part)` for parts of at most kLaunchGroups workgroups of `per` rows.
+template <bool BF, typename F>
+hipError_t by_launches(const QuantizeParams& p, int per, F launch) {
+  for (int64_t r0 = 0; r0 < p.rows; r0 += per * kLaunchGroups) {
+    QuantizeParams part = p;
+    part.x = (const char*)p.x + r0 * p.d * (BF ? 2 : 4);
+    part.q = p.q + r0 * p.ldq;
+    part.scale = p.scale + r0;
+    part.rows = p.rows - r0 < per * kLaunchGroups ? p.rows - r0 : per * kLaunchGroups;
+    launch(part);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 template <bool BF, int LANES, int NV>
 hipError_t quantize_go(const QuantizeParams& p, hipStream_t s) {
   constexpr int per = kQuantThreads / LANES;
-  hipLaunchKernelGGL((quantize_rows_kernel<BF, LANES, NV>), dim3((unsigned)((p.rows + per - 1) / per)),
-                     dim3(kQuantThreads), 0, s, p);
-  return hipGetLastError();
+  return by_launches<BF>(p, per, [&](const QuantizeParams& part) {
+    hipLaunchKernelGGL((quantize_rows_kernel<BF, LANES, NV>), dim3((unsigned)((part.rows + per - 1) / per)),
+                       dim3(kQuantThreads), 0, s, part);
+  });
 }
 template <bool BF>
 hipError_t quantize_pick(const QuantizeParams& p, hipStream_t s) {
@@ -168,8 +184,9 @@ hipError_t quantize_pick(const QuantizeParams& p, hipStream_t s) {
   if (vec && p.ldq <= 2048) return quantize_go<BF, 64, 4>(p, s);
   if (vec && p.ldq <= 4096) return quantize_go<BF, 256, 2>(p, s);
   if (vec && p.ldq <= 8192) return quantize_go<BF, 256, 4>(p, s);
-  hipLaunchKernelGGL(quantize_rows_any_kernel<BF>, dim3((unsigned)p.rows), dim3(kQuantThreads), 0, s, p);
-  return hipGetLastError();
+  return by_launches<BF>(p, 1, [&](const QuantizeParams& part) {
+    hipLaunchKernelGGL(quantize_rows_any_kernel<BF>, dim3((unsigned)part.rows), dim3(kQuantThreads), 0, s, part);
+  });
 }
 }  // namespace
 

@@ -54,6 +54,7 @@ struct TableParams {
   uint32_t* seen;
   uint32_t* counts;
   uint64_t* keys;  // of a draft's steps: its first slot is cleared
+  int64_t b0;      // first request of a launch (set by the launcher)
   int64_t B;
   int64_t V;
 };
@@ -82,6 +83,7 @@ struct RuleStepParams {
   uint32_t* counts;        // readable 256 bytes past its end
   uint64_t* keys;          // [kStepSlots][kStepGroups][B]
   uint32_t* bad_rows;
+  int64_t b0;              // first row of a launch (set by the launcher)
   int64_t B;
   int64_t M;
   int64_t V;

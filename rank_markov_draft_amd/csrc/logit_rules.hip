@@ -302,6 +302,26 @@ __global__ __launch_bounds__(kRuleThreads) void logit_rules_kernel(RulesParams p
 }
 
 namespace {
+// The call's requests from b0 on.
+RulesParams requests_from(RulesParams p, int64_t b0, int64_t element) {
+  const int64_t at = b0 * p.M * p.V * element;
+  auto later = [](auto*& t, int64_t n) { t = t ? t + n : nullptr; };
+  p.logits = (const char*)p.logits + at;
+  p.grad = p.grad ? (const char*)p.grad + at : nullptr;
+  p.out = (char*)p.out + at;
+  p.B -= b0;
+  later(p.token_ids, b0 * p.M);
+  later(p.r.history, b0 * p.r.history_stride);
+  later(p.r.lengths, b0);
+  later(p.r.prompt_lengths, b0);
+  later(p.r.repetition, b0);
+  later(p.r.frequency, b0);
+  later(p.r.presence, b0);
+  later(p.r.mask, b0 * p.r.mask_stride_b);
+  if (p.r.bias) p.r.bias = (const char*)p.r.bias + b0 * p.r.bias_stride * (p.r.bias_bf16 ? 2 : 4);
+  return p;
+}
+
 template <bool BF, bool BWD>
 hipError_t rules_go(const RulesParams& p, int num_cus, hipStream_t s) {
   const bool track = rules_penalise(p.r) && (p.r.history != nullptr || (p.token_ids != nullptr && p.M > 1));
@@ -324,21 +344,26 @@ hipError_t rules_go(const RulesParams& p, int num_cus, hipStream_t s) {
   spans = spans < 1 ? 1 : spans;
   int64_t span = ((p.M + spans - 1) / spans + R - 1) / R * R;
   spans = (p.M + span - 1) / span;
-  if (p.B > 0x7FFFFFFF / tiles || p.B * tiles > 0x7FFFFFFF / spans) return hipErrorNotSupported;
   const size_t lds = track ? (size_t)(T / 16 + (keep_counts ? T : 0)) * 4 : 0;
-  const dim3 grid((unsigned)(p.B * tiles * spans)), block(kRuleThreads);
+  const int64_t per = kLaunchGroups / (tiles * spans);  // requests of a launch
   // Positions at a time (and vectors of columns): 1 (four), 4, 8, in us at V =
   // 129280 and 1024 ids: 256 x 1 bf16 43, 56, 56; 64 x 3 bf16 33, 30, 30; 128
   // x 8 bf16 138, 118, 110.  The gradient holds the logits of a hit beside
   // its values, which in fp32 leaves eight positions too few waves: 64 x 5 84,
   // 80, 89 and 128 x 8 244, 236, 253; in bf16 52, 47, 46 and 139, 110, 115.
-  if (R == 1)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 1, 4>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
-  else if (R == 4)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 4, 1>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
-  else if constexpr (!BWD || BF)
-    hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 8, 1>), grid, block, lds, s, p, T, (int)tiles, span, track, keep_counts);
-  return hipGetLastError();
+  for (int64_t b0 = 0; b0 < p.B; b0 += per) {
+    const RulesParams q = requests_from(p, b0, BF ? 2 : 4);
+    const dim3 grid((unsigned)((q.B < per ? q.B : per) * tiles * spans)), block(kRuleThreads);
+    if (R == 1)
+      hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 1, 4>), grid, block, lds, s, q, T, (int)tiles, span, track, keep_counts);
+    else if (R == 4)
+      hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 4, 1>), grid, block, lds, s, q, T, (int)tiles, span, track, keep_counts);
+    else if constexpr (!BWD || BF)
+      hipLaunchKernelGGL((logit_rules_kernel<BF, BWD, 8, 1>), grid, block, lds, s, q, T, (int)tiles, span, track, keep_counts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 }  // namespace
 
@@ -359,7 +384,7 @@ constexpr int kTableCols = 4096;  // columns of a workgroup's tile of the table
 __global__ __launch_bounds__(kRuleThreads) void rule_table_kernel(TableParams p, int tiles) {
   __shared__ uint32_t seen[kTableCols / 32];
   __shared__ __attribute__((aligned(16))) uint32_t counts[kTableCols];
-  const int64_t b = blockIdx.x / (unsigned)tiles;
+  const int64_t b = p.b0 + blockIdx.x / (unsigned)tiles;
   const int64_t t0 = (int64_t)(blockIdx.x % (unsigned)tiles) * kTableCols;
   const int tn = (int)(p.V - t0 < kTableCols ? p.V - t0 : kTableCols);
   const int tid = threadIdx.x;
@@ -384,9 +409,15 @@ __global__ __launch_bounds__(kRuleThreads) void rule_table_kernel(TableParams p,
 
 hipError_t launch_rule_table(const TableParams& p, hipStream_t s) {
   const int64_t tiles = (p.V + kTableCols - 1) / kTableCols;
-  if (p.B * tiles > 0x7FFFFFFF) return hipErrorNotSupported;
-  hipLaunchKernelGGL(rule_table_kernel, dim3((unsigned)(p.B * tiles)), dim3(kRuleThreads), 0, s, p, (int)tiles);
-  return hipGetLastError();
+  const int64_t per = kLaunchGroups / tiles;
+  TableParams q = p;
+  for (q.b0 = 0; q.b0 < p.B; q.b0 += per) {
+    const int64_t n = p.B - q.b0 < per ? p.B - q.b0 : per;
+    hipLaunchKernelGGL(rule_table_kernel, dim3((unsigned)(n * tiles)), dim3(kRuleThreads), 0, s, q, (int)tiles);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 namespace {
@@ -459,7 +490,7 @@ __global__ __launch_bounds__(256, RT == 1 ? 3 : 2) void rule_step_kernel(RuleSte
   // the row chunks of a column tile lie eight workgroups apart: on one XCD,
   // whose L2 then holds the tile's W2 for all of them
   const int tile = (int)(blockIdx.x / (8u * chunks)) * 8 + (int)(blockIdx.x % 8u);
-  const int64_t b0 = (int64_t)(blockIdx.x / 8u % chunks) * 16 * RT;
+  const int64_t b0 = p.b0 + (int64_t)(blockIdx.x / 8u % chunks) * 16 * RT;
   if (tile >= tiles) return;
   const int64_t V = p.V, rank = p.rank;
   const int wc0 = tile * kStepCols + kStepWaveCols * wave;  // the wave's first column (V is at most 2^30)
@@ -1002,12 +1033,17 @@ __global__ __launch_bounds__(256, 2) void rule_few_kernel(RuleStepParams p, int 
 namespace {
 template <bool WBF, bool BF, int RT>
 hipError_t rule_step_form(const RuleStepParams& p, hipStream_t s) {
-  const int64_t tiles = (p.V + kStepCols - 1) / kStepCols, chunks = (p.B + 16 * RT - 1) / (16 * RT);
-  const int64_t groups = (tiles + 7) / 8 * 8 * chunks;
-  if (groups > 0x7FFFFFFF) return hipErrorNotSupported;
-  hipLaunchKernelGGL((rule_step_kernel<WBF, BF, RT>), dim3((unsigned)groups), dim3(256), 0, s, p, (int)tiles,
-                     (unsigned)chunks);
-  return hipGetLastError();
+  const int64_t tiles = (p.V + kStepCols - 1) / kStepCols, columns = (tiles + 7) / 8 * 8;
+  const int64_t per = kLaunchGroups / columns * 16 * RT;  // rows of a launch
+  RuleStepParams q = p;
+  for (q.b0 = 0; q.b0 < p.B; q.b0 += per) {
+    const int64_t chunks = ((p.B - q.b0 < per ? p.B - q.b0 : per) + 16 * RT - 1) / (16 * RT);
+    hipLaunchKernelGGL((rule_step_kernel<WBF, BF, RT>), dim3((unsigned)(columns * chunks)), dim3(256), 0, s, q, (int)tiles,
+                       (unsigned)chunks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 template <bool WBF, bool BF>
 hipError_t rule_few_form(const RuleStepParams& p, hipStream_t s) {
@@ -1057,7 +1093,7 @@ __global__ __launch_bounds__(kRuleThreads) void rule_choose_kernel(const uint64_
 
 hipError_t launch_rule_choose(const uint64_t* keys, int64_t B, int64_t M, int64_t* tokens, hipStream_t s) {
   const int64_t groups = (B + kRuleThreads - 1) / kRuleThreads;
-  if (groups > 0x7FFFFFFF) return hipErrorNotSupported;
+  if (groups > kLaunchGroups) return hipErrorNotSupported;
   hipLaunchKernelGGL(rule_choose_kernel, dim3((unsigned)groups), dim3(kRuleThreads), 0, s,
                      keys + ((M - 1) % kStepSlots) * kStepGroups * B, B, M, tokens);
   return hipGetLastError();
