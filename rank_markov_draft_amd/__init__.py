@@ -94,6 +94,8 @@ class Workspace:
                  hidden: int | None = None, backward: bool = False, int8_hidden: int | None = None,
                  processed: bool = False):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if device.type != "cuda":
+            raise ValueError(f"the head runs on a GPU; the workspace would be on {device}")
         self.nbytes = max(workspace_bytes(B, M, V, r, sample, hidden), 256)
         if backward:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_backward_workspace_bytes(B, M, V, r)))
