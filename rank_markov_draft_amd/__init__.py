@@ -96,6 +96,8 @@ class Workspace:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.type != "cuda":
             raise ValueError(f"the head runs on a GPU; the workspace would be on {device}")
+        if device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
         self.nbytes = max(workspace_bytes(B, M, V, r, sample, hidden), 256)
         if backward:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_backward_workspace_bytes(B, M, V, r)))
@@ -103,9 +105,10 @@ class Workspace:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(B, M, int8_hidden)))
         if processed:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_processed_workspace_bytes(B, M, V, r)))
+        self.device = device
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        _lib.check(_lib.load().dspark_markov_workspace_init(
-            _ptr(self.buffer), self.nbytes, _stream_handle(device)), "workspace_init")
+        _lib.check(_call(device, _lib.load().dspark_markov_workspace_init, _ptr(self.buffer), self.nbytes),
+                   "workspace_init")
 
     @property
     def ptr(self):
@@ -123,8 +126,9 @@ def read_device_error(ws: Workspace) -> int:
     Raises DeviceError when a persistent sampling launch on ``ws`` failed since
     the last read (its tokens were -1); the record is cleared either way."""
     n = ctypes.c_int64(0)
-    _lib.check(_lib.load().dspark_markov_read_device_error(
-        ws.ptr, _stream_handle(ws.buffer.device), ctypes.byref(n)), "read_device_error")
+    with torch.cuda.device(ws.device):
+        _lib.check(_lib.load().dspark_markov_read_device_error(
+            ws.ptr, _stream_handle(ws.device), ctypes.byref(n)), "read_device_error")
     return int(n.value)
 
 
@@ -703,8 +707,7 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
     w1c, w2c = w1.contiguous(), w2.contiguous()
     r = w1.shape[1]
     if workspace is None:
-        with torch.cuda.device(dev):
-            workspace = Workspace(B, M, V, r, sample=True, device=dev, processed=True)
+        workspace = Workspace(B, M, V, r, sample=True, device=dev, processed=True)
     st = _call(dev, _lib.load().dspark_markov_sample_block_processed, _ptr(base), tag, _ptr(first), _ptr(w1c), _ptr(w2c),
                wtag, rules, B, M, V, r, T, int(seed) & (2**64 - 1), int(position_offset), int(batch_offset),
                _ptr(tokens_out), _ptr(logits_out), workspace.ptr, workspace.nbytes)
