@@ -48,7 +48,7 @@ hipError_t launch_logit_rules(const RulesParams& p, bool logits_bf16, int num_cu
 // The tokens of each row's history as a table: a bit per token that stands in
 // it (rule_words(V) words a row), and its count among the outputs where the
 // bit is set (V words a row; other counts are left unwritten).
-inline int64_t rule_words(int64_t V) { return (V + 31) / 32; }
+inline int64_t rule_words(int64_t V) { return V / 32 + (V % 32 != 0); }
 struct TableParams {
   RuleSet r;
   uint32_t* seen;
