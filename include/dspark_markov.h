@@ -393,8 +393,9 @@ dspark_status_t dspark_markov_process_block_backward(const void* grad_processed,
  * calls reproduces one whole call to the bit.  A row with nothing above -inf to
  * draw from gets token -1; its next position then has an id outside [0, V) as
  * predecessor, so no bias.  M = 1 is the single-token form.
- * Greedy calls in bf16 with B <= 64, M <= 16, at most 512 columns a compute
- * unit and no per-request biases run as one persistent launch, as
+ * Greedy calls in bf16 with B <= 64, M <= 16, r a multiple of 8 up to 256, V
+ * one of 8 up to 512 columns a compute unit, 16-byte aligned logits and weights
+ * and no per-request biases run as one persistent launch, as
  * dspark_markov_sample_block's do, and share its failure behaviour: if its
  * workgroups do not meet within a second (another stream holds compute units)
  * every token is -1, dspark_markov_read_device_error reports it, and until

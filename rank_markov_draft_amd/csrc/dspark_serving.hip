@@ -331,7 +331,15 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
   p.seed_lo = (uint32_t)(seed & 0xFFFFFFFFu);
   p.seed_hi = (uint32_t)(seed >> 32);
   // Greedy drafts with bf16 logits and weights that the persistent chain can
-  // hold run as one launch (per-request biases do not fit in its LDS).
+  // hold run as one launch (per-request biases do not fit in its LDS).  The
+  // rows and tokens are the steps' own either way.  Whole calls in us, drafts
+  // of five by the chain and by steps (and single positions), with penalties
+  // and masks: V = 129280 at rank 256, 4 rows 57, 83 (29, 21), 16 rows 68, 99
+  // (32, 25), 64 rows 107, 206 (48, 46); V = 32000 at rank 256, 4 rows 44, 50
+  // (22, 19), 64 rows 69, 96 (30, 24); at rank 64, 4 rows 41, 38 (20, 19), 64
+  // rows 64, 72 (27, 20); V = 4000 at rank 64, 4 rows 43, 36 (19, 19), 64 rows
+  // 60, 39 (23, 19).  So the chain pays where W2 is long and read again; the
+  // short and the single ones it takes too cost up to half as much again.
   const int cus = device_cus();
   if (p.greedy && cus > 0 && tile_path(logits_dtype, weight_dtype, V, r, base_logits, processed_logits, w1, w2) &&
       B <= dspark::chain_max_rows() && M <= kChainMaxSteps && (V + 31) / 32 <= (int64_t)cus * dspark::chain_waves_per_group() &&
