@@ -311,7 +311,7 @@ __global__ __launch_bounds__(512) void markov_bwd_de_bf16(BwdParams p) {
 // de[n][j] = rnd_W(sum of the S slices' partial sums, in slice order).
 template <bool W_BF16>
 __global__ __launch_bounds__(256) void markov_bwd_de_finish(BwdParams p) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   const int64_t total = p.rows * p.r;
   if (t >= total) return;
   float part[16];
@@ -355,7 +355,7 @@ struct KahanSum {
 // dW2w[v][j], one thread each, rows in order.
 template <bool L_BF16, bool W_BF16>
 __global__ __launch_bounds__(256) void markov_bwd_dw2_scalar(BwdParams p) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   if (t >= p.V * p.r) return;
   const int64_t v = t / p.r, j = t % p.r;
   KahanSum k;
@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256) void markov_bwd_dw2_scalar(BwdParams p) {
 // de[n][j], one thread each, columns in order.
 template <bool L_BF16, bool W_BF16>
 __global__ __launch_bounds__(256) void markov_bwd_de_scalar(BwdParams p) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   if (t >= p.rows * p.r) return;
   const int64_t n = t / p.r, j = t % p.r;
   KahanSum k;
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(256) void markov_bwd_de_scalar(BwdParams p) {
 // compare the ids 64 at a time; a ballot finds an earlier equal id and a
 // wave minimum the next one.
 __global__ __launch_bounds__(256) void markov_bwd_link(BwdParams p) {
-  const int64_t n = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t n = long_grid_index() * 4 + (threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   if (n >= p.rows) return;
   const int64_t x = p.ids[n];
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256) void markov_bwd_link(BwdParams p) {
 // order (fp32), rounded to W.  dW1 is zero-filled before.
 template <bool W_BF16>
 __global__ __launch_bounds__(256) void markov_bwd_dw1(BwdParams p) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   if (t >= p.rows * p.r) return;
   const int64_t n = t / p.r, j = t % p.r;
   if (p.link[n] == -2) return;
@@ -449,7 +449,7 @@ hipError_t launch_bwd_fast(const BwdParams& p, hipStream_t s) {
   hipLaunchKernelGGL((markov_bwd_de_bf16<JB, LF32>), dim3((unsigned)p.S * groups), dim3(512), 0, s, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((markov_bwd_de_finish<true>), dim3((unsigned)((p.rows * p.r + 255) / 256)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL((markov_bwd_de_finish<true>), long_grid((p.rows * p.r + 255) / 256), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 }  // namespace
@@ -480,7 +480,7 @@ hipError_t launch_backward(const BwdParams& p, bool logits_bf16, bool weights_bf
       default: e = f ? launch_bwd_fast<16, true>(p, s) : launch_bwd_fast<16, false>(p, s); break;
     }
   } else {
-    const dim3 g2((unsigned)((p.V * p.r + 255) / 256)), ge((unsigned)((p.rows * p.r + 255) / 256));
+    const dim3 g2 = long_grid((p.V * p.r + 255) / 256), ge = long_grid((p.rows * p.r + 255) / 256);
     if (logits_bf16 && weights_bf16) {
       hipLaunchKernelGGL((markov_bwd_dw2_scalar<true, true>), g2, dim3(256), 0, s, p);
       hipLaunchKernelGGL((markov_bwd_de_scalar<true, true>), ge, dim3(256), 0, s, p);
@@ -497,12 +497,12 @@ hipError_t launch_backward(const BwdParams& p, bool logits_bf16, bool weights_bf
     e = hipGetLastError();
   }
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(markov_bwd_link, dim3((unsigned)((p.rows + 3) / 4)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(markov_bwd_link, long_grid((p.rows + 3) / 4), dim3(256), 0, s, p);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   e = launch_fill_zero(p.dw1, (size_t)(p.V * p.r) * (weights_bf16 ? 2 : 4), s);
   if (e != hipSuccess) return e;
-  const dim3 ge((unsigned)((p.rows * p.r + 255) / 256));
+  const dim3 ge = long_grid((p.rows * p.r + 255) / 256);
   if (weights_bf16)
     hipLaunchKernelGGL((markov_bwd_dw1<true>), ge, dim3(256), 0, s, p);
   else

@@ -193,7 +193,7 @@ __global__ __launch_bounds__(1024) void markov_gate_bf16(GateParams g) {
 // Latent elements from the split partial sums, added in split order.
 template <bool W_BF16>
 __global__ __launch_bounds__(256) void markov_gate_finish(GateParams g) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   const int64_t rows = g.rows, r = g.r;
   if (t >= rows * r) return;
   float part[16];
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(256) void markov_gate_finish(GateParams g) {
 // the hidden values rounded to W first; without hidden states u = e.
 template <bool W_BF16, bool HF32>
 __global__ __launch_bounds__(256) void markov_gate_scalar(GateParams g) {
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t t = long_grid_index() * 256 + threadIdx.x;
   const int64_t r = g.r, d = g.d, K = d + r;
   if (t >= g.rows * r) return;
   const int64_t n = t / r, j = t % r;
@@ -278,10 +278,10 @@ hipError_t launch_gate(const GateParams& g, bool weights_bf16, bool hidden_f32, 
       hipLaunchKernelGGL((markov_gate_bf16<false>), grid, dim3(1024), 0, s, q);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || q.S == 1) return e;
-    hipLaunchKernelGGL((markov_gate_finish<true>), dim3((unsigned)((g.rows * g.r + 255) / 256)), dim3(256), 0, s, q);
+    hipLaunchKernelGGL((markov_gate_finish<true>), long_grid((g.rows * g.r + 255) / 256), dim3(256), 0, s, q);
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)((g.rows * g.r + 255) / 256));
+  const dim3 grid = long_grid((g.rows * g.r + 255) / 256);
   if (weights_bf16 && hidden_f32)
     hipLaunchKernelGGL((markov_gate_scalar<true, true>), grid, dim3(256), 0, s, g);
   else if (weights_bf16)

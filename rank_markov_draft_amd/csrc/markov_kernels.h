@@ -65,6 +65,17 @@ struct LmHeadParams {
 };
 hipError_t launch_lm_head(const LmHeadParams& p, int num_cus, hipStream_t s);
 
+// A grid of any number of workgroups of up to 256 threads, in two dimensions
+// past what the threads of one (32 bits) hold, and a workgroup's index in it:
+// those behind the last have nothing to do.
+constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;  // of one dimension; more wrap around without an error
+inline dim3 long_grid(int64_t groups) {
+  const int64_t most = kLaunchThreads / 256, x = groups < most ? groups : most;
+  return dim3((unsigned)x, (unsigned)((groups + x - 1) / x));
+}
+__device__ __forceinline__ int64_t long_grid_index() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
+
 // The gate of the gated head, one launch per call (apply) or per step
 // (sampling): the latent rows u = rnd_W(rnd_W(sigmoid(rnd_W(z + b))) * e),
 // z = gate_proj's product with [h; e], e = W1[predecessor] (zero for

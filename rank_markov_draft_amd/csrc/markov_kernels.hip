@@ -595,10 +595,11 @@ __global__ __launch_bounds__(kFwThreads) void markov_rows_mfma_f32w(KernelParams
 // One workgroup per batch row: the token of step k is the index in the
 // largest of the row's slice keys.
 __global__ __launch_bounds__(256) void reduce_row_keys(const uint64_t* __restrict__ partials,
-                                                       int64_t nparts, int64_t M, int64_t k,
+                                                       int64_t nparts, int64_t B, int64_t M, int64_t k,
                                                        int64_t* __restrict__ tokens) {
   __shared__ uint64_t lds_key[4];
-  const int64_t b = blockIdx.x;
+  const int64_t b = long_grid_index();
+  if (b >= B) return;
   const int tid = threadIdx.x;
   uint64_t key = 0;
   for (int64_t i = tid; i < nparts; i += 256) key = max_u64(key, partials[b * nparts + i]);
@@ -622,6 +623,7 @@ __global__ void fill_zero_kernel(u32x4_t* __restrict__ p, int64_t n16, unsigned 
 // ---------------------------------------------------------------- launchers
 template <int MODE>
 static hipError_t launch_tile_mode(const KernelParams& p, int ks, hipStream_t s) {
+  if ((p.V + 127) / 128 * 256 > kLaunchThreads) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((p.V + 127) / 128));
   const dim3 block(256);
   switch (ks) {
@@ -662,6 +664,7 @@ template <int MODE, bool LBF, bool WBF>
 static hipError_t launch_rows_fma(const KernelParams& p, hipStream_t s) {
   const int64_t chunks = (p.rows + kFmaRows - 1) / kFmaRows;
   const unsigned tiles = (unsigned)((p.V + kFmaCols - 1) / kFmaCols);
+  if ((int64_t)tiles * 256 > kLaunchThreads) return hipErrorInvalidValue;
   for (int64_t c0 = 0; c0 < chunks; c0 += 65535) {  // grid.y holds at most 65535 row chunks
     const int64_t nc = chunks - c0 < 65535 ? chunks - c0 : 65535;
     hipLaunchKernelGGL((markov_rows_fma<MODE, LBF, WBF>), dim3(tiles, (unsigned)nc), dim3(256), 0, s, p, c0);
@@ -673,7 +676,8 @@ static hipError_t launch_rows_fma(const KernelParams& p, hipStream_t s) {
 
 // The matrix-core kernel for fp32 weights when the shapes allow 16-byte
 // vectors: r, V (and the latent row pitch) multiples of 4, operands 16-byte
-// aligned; hipErrorNotSupported otherwise (the FMA kernel takes the call).
+// aligned, and V one launch's; hipErrorNotSupported otherwise (the FMA kernel
+// takes the call).
 template <int MODE, bool LBF>
 static hipError_t launch_rows_mfma_f32w(const KernelParams& p, hipStream_t s) {
   const void* erow = p.latent != nullptr ? p.latent : p.w1;
@@ -682,6 +686,7 @@ static hipError_t launch_rows_mfma_f32w(const KernelParams& p, hipStream_t s) {
   if (!a16(p.w2) || !a16(erow) || !a16(p.base) || (p.out != nullptr && !a16(p.out))) return hipErrorNotSupported;
   const int64_t chunks = (p.rows + kFwRows - 1) / kFwRows;
   const unsigned tiles = (unsigned)((p.V + kFwCols - 1) / kFwCols);
+  if ((int64_t)tiles * kFwThreads > kLaunchThreads) return hipErrorNotSupported;
   for (int64_t c0 = 0; c0 < chunks; c0 += 65535) {  // grid.y holds at most 65535 row chunks
     const int64_t nc = chunks - c0 < 65535 ? chunks - c0 : 65535;
     if (p.r <= kFwWholeK)
@@ -718,8 +723,7 @@ hipError_t launch_generic(const KernelParams& p, bool logits_bf16, bool weights_
 
 hipError_t launch_reduce(const uint64_t* partials, int64_t nparts, int64_t B, int64_t M, int64_t k,
                          int64_t* tokens, hipStream_t s) {
-  hipLaunchKernelGGL(reduce_row_keys, dim3((unsigned)B), dim3(256), 0, s, partials, nparts, M, k,
-                     tokens);
+  hipLaunchKernelGGL(reduce_row_keys, long_grid(B), dim3(256), 0, s, partials, nparts, B, M, k, tokens);
   return hipGetLastError();
 }
 
