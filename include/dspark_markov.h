@@ -318,6 +318,45 @@ dspark_status_t dspark_markov_lm_head_int8(const void* hidden_states, dspark_dty
                                            int64_t V, void* logits, dspark_dtype_t logits_dtype, void* workspace,
                                            size_t workspace_bytes, void* stream);
 
+/* Blocks of 32 numbers in microscaled 4-bit floating point: block b of a row
+ * x holds e = floor(log2 max|x|) - 2 (at least -127, which a block of zeros has)
+ * as the byte scales[b] = e + 127, and its numbers as codes of 4 bits, sign
+ * first, of the value 0, 1/2, 1, 3/2, 2, 3, 4, 6 nearest to |x| / 2^e, ties to
+ * the even code, at most 6; two a byte, the first in the low half.  A block
+ * that holds an infinity or NaN has the byte 255 (and codes of zero), so that
+ * what is computed from it is NaN.  A row of d numbers takes
+ * n = 4 ceil(d / 128) blocks, filled up with zeros past d.
+ *   x       device, [rows, d], dtype (F32 or BF16).
+ *   codes   device, [rows, 16 n] bytes, 16-byte aligned; scales device,
+ *           [rows, n] bytes, 4-byte aligned.
+ * rows >= 0, d from 0 to 2^20.  Outputs must not overlap an input or each
+ * other. */
+dspark_status_t dspark_markov_quantize_fp4(const void* x, dspark_dtype_t dtype, int64_t rows, int64_t d, uint8_t* codes,
+                                           uint8_t* scales, void* stream);
+
+/* The numbers that codes and scales stand for, rounded to dtype (which only
+ * rounds below its normal range). */
+dspark_status_t dspark_markov_dequantize_fp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t d,
+                                             void* x, dspark_dtype_t dtype, void* stream);
+
+/* The vocabulary head in microscaled 4-bit floating point: the hidden states
+ * are quantised as above and multiplied with the head's blocks,
+ *     logits[n, v] = round_O( sum over blocks of 2^(e[n, b] + f[v, b]) sum_i c[n, b, i] h[v, b, i] ),
+ * products and sums in fp32 on the matrix cores.
+ *   hidden_states  device, [B, M, d], hidden_dtype (F32 or BF16), d from 1 to 2^20.
+ *   head_codes, head_scales   device, rows as dspark_markov_quantize_fp4 makes
+ *                  them of the head's weight [V, d], aligned as there.
+ *   logits         device, [B, M, V] output, logits_dtype; must not overlap
+ *                  an input.
+ * B*M*V == 0 is a successful no-op.  The workspace must hold
+ * dspark_markov_lm_head_fp4_workspace_bytes(...) bytes (no zero fill needed). */
+size_t dspark_markov_lm_head_fp4_workspace_bytes(int64_t B, int64_t M, int64_t d);
+
+dspark_status_t dspark_markov_lm_head_fp4(const void* hidden_states, dspark_dtype_t hidden_dtype, int64_t d,
+                                          const uint8_t* head_codes, const uint8_t* head_scales, int64_t B, int64_t M,
+                                          int64_t V, void* logits, dspark_dtype_t logits_dtype, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
 /* Rules on logits: penalties for repeated tokens, biases and grammar masks.
  * All pointers are device memory; a null pointer turns its rule off.  With c
  * the number of times token v stands among the counted outputs of row b, and

@@ -35,6 +35,7 @@ is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -42,7 +43,8 @@ from . import _lib
 
 __all__ = ["apply_block_logits", "sample_block_tokens", "apply_block_logits_gated",
            "sample_block_tokens_gated", "apply_block_logits_backward", "apply_block_logits_lm_head",
-           "quantize_rows", "lm_head_logits_int8", "process_block_logits", "process_block_logits_backward",
+           "quantize_rows", "lm_head_logits_int8", "quantize_blocks_fp4", "dequantize_blocks_fp4",
+           "lm_head_logits_fp4", "process_block_logits", "process_block_logits_backward",
            "sample_block_tokens_processed", "Workspace",
            "read_device_error", "workspace_bytes"]
 
@@ -84,15 +86,16 @@ def workspace_bytes(B: int, M: int, V: int, r: int, sample: bool, hidden: int | 
 class Workspace:
     """Device workspace for a family of calls of at most the given sizes
     (``hidden``: the hidden size of gated calls; ``backward``: sized for the
-    backward as well; ``int8_hidden``: the hidden size of 8-bit head calls;
-    ``processed``: sized for sampling under logit rules as well).
+    backward as well; ``int8_hidden``, ``fp4_hidden``: the hidden size of 8-bit
+    and 4-bit head calls; ``processed``: sized for sampling under logit rules
+    as well).
 
     Zero-filled once at creation; the library leaves it ready for the next
     call.  Calls sharing one workspace must be ordered on one stream."""
 
     def __init__(self, B: int, M: int, V: int, r: int, sample: bool, device=None,
                  hidden: int | None = None, backward: bool = False, int8_hidden: int | None = None,
-                 processed: bool = False):
+                 processed: bool = False, fp4_hidden: int | None = None):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.type != "cuda":
             raise ValueError(f"the head runs on a GPU; the workspace would be on {device}")
@@ -103,6 +106,8 @@ class Workspace:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_backward_workspace_bytes(B, M, V, r)))
         if int8_hidden is not None:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(B, M, int8_hidden)))
+        if fp4_hidden is not None:
+            self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_fp4_workspace_bytes(B, M, fp4_hidden)))
         if processed:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_processed_workspace_bytes(B, M, V, r)))
         self.device = device
@@ -506,6 +511,114 @@ def lm_head_logits_int8(hidden_states: torch.Tensor, head_q: torch.Tensor, head_
     st = _call(dev, _lib.load().dspark_markov_lm_head_int8, _ptr(h), tag, d, _ptr(hq), _ptr(hs), rows, 1, V, _ptr(out),
                out_tag, _ptr(buffer), nbytes)
     _lib.check(st, "lm_head_logits_int8")
+    return out
+
+
+def _fp4_blocks(d: int) -> int:
+    """Blocks of 32 that a row of d numbers takes: whole groups of four."""
+    return (d + 127) // 128 * 4
+
+
+def _at(t: torch.Tensor, alignment: int) -> torch.Tensor:
+    """``t`` contiguous, at an address that is a multiple of ``alignment``."""
+    t = t.contiguous()
+    return t if t.data_ptr() % alignment == 0 else t.clone()
+
+
+def quantize_blocks_fp4(x: torch.Tensor, *, out: torch.Tensor | None = None, scale_out: torch.Tensor | None = None):
+    """Blocks of 32 numbers in microscaled 4-bit floating point (e2m1 codes
+    with an e8m0 scale): x [..., d] gives ``(codes [..., 16 n], scales [..., n])``,
+    both uint8, for n = 4 ceil(d / 128) blocks, filled up with zeros past d.  A
+    block's scale is 2^(byte - 127) = 2^(floor(log2 max|x|) - 2); a code is the
+    value 0, 1/2, 1, 3/2, 2, 3, 4 or 6 nearest to |x| / scale (ties to the even
+    code, at most 6) with its sign in bit 3, the first of two in a byte's low
+    half.  A block with an infinity or NaN has the byte 255, so that what is
+    computed from it is NaN."""
+    if x.dim() < 1:
+        raise ValueError("x must be [..., d]")
+    _check_device(x.device, None, out=out, scale_out=scale_out)
+    tag = _dtype_tag(x)
+    d = x.shape[-1]
+    n = _fp4_blocks(d)
+    lead = tuple(x.shape[:-1])
+    for name, t, shape, align in (("out", out, lead + (16 * n,), 16), ("scale_out", scale_out, lead + (n,), 4)):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.uint8 or not t.is_contiguous()
+                              or t.data_ptr() % align):
+            raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}, {align}-byte aligned")
+    if out is None:
+        out = torch.empty(lead + (16 * n,), dtype=torch.uint8, device=x.device)
+    if scale_out is None:
+        scale_out = torch.empty(lead + (n,), dtype=torch.uint8, device=x.device)
+    xc = x.contiguous()
+    rows = math.prod(lead)
+    st = _call(x.device, _lib.load().dspark_markov_quantize_fp4, _ptr(xc), tag, rows, d, _ptr(out), _ptr(scale_out))
+    _lib.check(st, "quantize_blocks_fp4")
+    return out, scale_out
+
+
+def dequantize_blocks_fp4(codes: torch.Tensor, scales: torch.Tensor, size: int, *,
+                          dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The numbers [..., size] that quantize_blocks_fp4's codes and scales of
+    rows of ``size`` numbers stand for, in float32 or bfloat16."""
+    n = _fp4_blocks(size)
+    if size < 0 or codes.dim() < 1 or codes.dtype != torch.uint8 or codes.shape[-1] != 16 * n:
+        raise ValueError(f"codes must be uint8 [..., {16 * n}] for rows of {size}, got {codes.dtype} {tuple(codes.shape)}")
+    lead = tuple(codes.shape[:-1])
+    if scales.dtype != torch.uint8 or tuple(scales.shape) != lead + (n,):
+        raise ValueError(f"scales must be uint8 {lead + (n,)}, got {scales.dtype} {tuple(scales.shape)}")
+    _check_device(codes.device, None, scales=scales, out=out)
+    if out is None:
+        out = torch.empty(lead + (size,), dtype=dtype, device=codes.device)
+    elif tuple(out.shape) != lead + (size,) or out.dtype != dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {dtype} tensor of shape {lead + (size,)}")
+    tag = _dtype_tag(out)
+    c, s = _at(codes, 16), _at(scales, 4)
+    st = _call(codes.device, _lib.load().dspark_markov_dequantize_fp4, _ptr(c), _ptr(s), math.prod(lead), size, _ptr(out),
+               tag)
+    _lib.check(st, "dequantize_blocks_fp4")
+    return out
+
+
+def lm_head_logits_fp4(hidden_states: torch.Tensor, head_codes: torch.Tensor, head_scales: torch.Tensor, *,
+                       out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                       workspace: Workspace | None = None) -> torch.Tensor:
+    """Base logits [..., V] of hidden_states [..., d] through a vocabulary head
+    held in 4-bit blocks: head_codes [V, 16 n] and head_scales [V, n] as
+    quantize_blocks_fp4 gives them for the head's Linear weight [V, d].  The
+    hidden states are quantised the same way in the call; products and sums in
+    fp32 on the matrix cores.  ``out_dtype``: float32 (default) or bfloat16."""
+    if hidden_states.dim() < 1:
+        raise ValueError("hidden_states must be [..., d]")
+    d = hidden_states.shape[-1]
+    n = _fp4_blocks(d)
+    if head_codes.dim() != 2 or head_codes.shape[1] != 16 * n or head_codes.dtype != torch.uint8:
+        raise ValueError(f"head_codes must be uint8 [V, {16 * n}], got {head_codes.dtype} {tuple(head_codes.shape)}")
+    V = head_codes.shape[0]
+    if tuple(head_scales.shape) != (V, n) or head_scales.dtype != torch.uint8:
+        raise ValueError(f"head_scales must be uint8 [{V}, {n}], got {head_scales.dtype} {tuple(head_scales.shape)}")
+    dev = hidden_states.device
+    _check_device(dev, workspace, head_codes=head_codes, head_scales=head_scales, out=out)
+    tag = _dtype_tag(hidden_states)
+    shape = tuple(hidden_states.shape[:-1]) + (V,)
+    if out_dtype is None:
+        out_dtype = torch.float32 if out is None else out.dtype
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != out_dtype or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {out_dtype} tensor of shape {shape}")
+    out_tag = _dtype_tag(out)
+    if out.numel() == 0:
+        return out
+    rows = out.numel() // V
+    h, hc, hs = hidden_states.contiguous(), _at(head_codes, 16), _at(head_scales, 4)
+    if workspace is None:
+        nbytes = int(_lib.load().dspark_markov_lm_head_fp4_workspace_bytes(rows, 1, d))
+        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+    else:
+        nbytes, buffer = workspace.nbytes, workspace.buffer
+    st = _call(dev, _lib.load().dspark_markov_lm_head_fp4, _ptr(h), tag, d, _ptr(hc), _ptr(hs), rows, 1, V, _ptr(out),
+               out_tag, _ptr(buffer), nbytes)
+    _lib.check(st, "lm_head_logits_fp4")
     return out
 
 

@@ -44,6 +44,10 @@ EXPORTS = (
     "dspark_markov_quantize_rows",
     "dspark_markov_lm_head_int8_workspace_bytes",
     "dspark_markov_lm_head_int8",
+    "dspark_markov_quantize_fp4",
+    "dspark_markov_dequantize_fp4",
+    "dspark_markov_lm_head_fp4_workspace_bytes",
+    "dspark_markov_lm_head_fp4",
     "dspark_markov_process_block",
     "dspark_markov_process_block_backward",
     "dspark_markov_processed_workspace_bytes",
@@ -137,6 +141,14 @@ def load():
     L.dspark_markov_lm_head_int8_workspace_bytes.restype = sz
     L.dspark_markov_lm_head_int8.argtypes = [p, i32, i64, p, p, i64, i64, i64, p, i32, p, sz, p]
     L.dspark_markov_lm_head_int8.restype = i32
+    L.dspark_markov_quantize_fp4.argtypes = [p, i32, i64, i64, p, p, p]
+    L.dspark_markov_quantize_fp4.restype = i32
+    L.dspark_markov_dequantize_fp4.argtypes = [p, p, i64, i64, p, i32, p]
+    L.dspark_markov_dequantize_fp4.restype = i32
+    L.dspark_markov_lm_head_fp4_workspace_bytes.argtypes = [i64, i64, i64]
+    L.dspark_markov_lm_head_fp4_workspace_bytes.restype = sz
+    L.dspark_markov_lm_head_fp4.argtypes = [p, i32, i64, p, p, i64, i64, i64, p, i32, p, sz, p]
+    L.dspark_markov_lm_head_fp4.restype = i32
     L.dspark_markov_process_block.argtypes = [p, i32, p, rules, i64, i64, i64, p, p]
     L.dspark_markov_process_block.restype = i32
     L.dspark_markov_process_block_backward.argtypes = [p, p, i32, p, rules, i64, i64, i64, p, p]

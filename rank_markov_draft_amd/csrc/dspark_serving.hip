@@ -16,8 +16,6 @@ namespace {
 
 using namespace dspark::host;
 
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
 // ---- 8-bit head: the quantised rows, then their scales and the floats past
 // them that the product reads in whole vectors
 size_t int8_rows_bytes(int64_t rows, int64_t d) {
@@ -28,22 +26,6 @@ size_t int8_scales_bytes(int64_t rows) {
 }
 
 // ---- logit rules
-// Byte ranges that a call's rules read, for the overlap checks.
-struct Ranges {
-  const void* at[16];
-  size_t bytes[16];
-  int n = 0;
-  void add(const void* p, size_t b) {
-    at[n] = p;
-    bytes[n++] = b;
-  }
-  bool meet(const void* p, size_t b) const {
-    for (int i = 0; i < n; ++i)
-      if (overlaps(p, b, at[i], bytes[i])) return true;
-    return false;
-  }
-};
-
 // Bytes from the first to the last element of `count` rows of `len` elements
 // `stride` apart; -1 when they cannot be represented.
 int64_t extent(int64_t count, int64_t stride, int64_t len, int64_t size) {

@@ -102,6 +102,24 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Byte ranges that a call reads, for the overlap checks.
+struct Ranges {
+  const void* at[16];
+  size_t bytes[16];
+  int n = 0;
+  void add(const void* p, size_t b) {
+    at[n] = p;
+    bytes[n++] = b;
+  }
+  bool meet(const void* p, size_t b) const {
+    for (int i = 0; i < n; ++i)
+      if (overlaps(p, b, at[i], bytes[i])) return true;
+    return false;
+  }
+};
+
 inline int64_t vocab_slices(int64_t V) { return (V + 127) / 128; }
 
 // Largest rank the row-tile kernels take (they walk the rank in chunks; the
