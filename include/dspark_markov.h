@@ -454,6 +454,46 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
                                                      int64_t* sampled_tokens, void* processed_logits, void* workspace,
                                                      size_t workspace_bytes, void* stream);
 
+/* Distillation of the drafter's logits from a teacher's top logits, for
+ * training.  For a row x of logits [B, M, V] and the teacher's K entries of that
+ * position, those with an id outside [0, V) (padding) or a logit of -inf left
+ * out, with q = softmax(teacher_logits / T) over the entries and
+ * p = softmax(x / T) over the vocabulary,
+ *     loss = T^2 sum_j q_j (log q_j - log p[id_j]).
+ * An id may stand in a list more than once (its weights add up in the
+ * gradient).  A row without entries has loss 0; one with entries and no logit
+ * above -inf has loss +inf, as one whose logit is -inf where q_j > 0; an entry
+ * whose weight underflows to zero counts nothing.  Infinities above and NaN
+ * make the loss NaN.  Streamed sums in fp32, the entries' terms in 64 bits.
+ *   teacher_ids    device, [B, M, K] int64; teacher_logits device, [B, M, K],
+ *                  teacher_dtype (F32 or BF16).  K from 0 to 1024.
+ *   temperature    T > 0 (log2(e) / T a normal fp32 number).
+ *   loss           device, [B, M] fp32 output.
+ *   stats          device, [B, M, 4] fp32 output for the backward pass.
+ * V from 1 to 2^30.  B*M == 0 is a successful no-op.  The workspace must hold
+ * dspark_markov_distill_workspace_bytes(...) bytes (no zero fill needed). */
+size_t dspark_markov_distill_workspace_bytes(int64_t B, int64_t M, int64_t V);
+
+dspark_status_t dspark_markov_distill_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* teacher_ids,
+                                            const void* teacher_logits, dspark_dtype_t teacher_dtype, int64_t B,
+                                            int64_t M, int64_t V, int64_t K, double temperature, float* loss,
+                                            float* stats, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradient with respect to the logits, for the loss rows' gradient:
+ *     grad_logits[v] = grad_loss T (p[v] - sum over id_j = v of q_j),
+ * in fp32, rounded once to the logits' dtype; zero for a row without entries
+ * or with no logit above -inf.  It is the grad_corrected of
+ * dspark_markov_apply_block_backward.  Arguments as in the forward call, with
+ * the stats it left.
+ *   grad_loss    device, [B, M] fp32.
+ *   grad_logits  device, [B, M, V] output, logits_dtype; may equal logits (in
+ *                place); any other overlap with an input is invalid. */
+dspark_status_t dspark_markov_distill_block_backward(const float* grad_loss, const void* logits,
+                                                     dspark_dtype_t logits_dtype, const int64_t* teacher_ids,
+                                                     const void* teacher_logits, dspark_dtype_t teacher_dtype,
+                                                     const float* stats, int64_t B, int64_t M, int64_t V, int64_t K,
+                                                     double temperature, void* grad_logits, void* stream);
+
 /* Synchronises `stream`, then returns in *bad_rows the number of rows whose
  * predecessor id was outside [0, V) in the calls made with this workspace
  * since the last read, and clears the count.  Returns DSPARK_ERR_DEVICE when

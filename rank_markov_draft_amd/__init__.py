@@ -45,7 +45,7 @@ __all__ = ["apply_block_logits", "sample_block_tokens", "apply_block_logits_gate
            "sample_block_tokens_gated", "apply_block_logits_backward", "apply_block_logits_lm_head",
            "quantize_rows", "lm_head_logits_int8", "quantize_blocks_fp4", "dequantize_blocks_fp4",
            "lm_head_logits_fp4", "process_block_logits", "process_block_logits_backward",
-           "sample_block_tokens_processed", "Workspace",
+           "sample_block_tokens_processed", "distill_block_loss", "distill_block_loss_backward", "Workspace",
            "read_device_error", "workspace_bytes"]
 
 
@@ -88,14 +88,14 @@ class Workspace:
     (``hidden``: the hidden size of gated calls; ``backward``: sized for the
     backward as well; ``int8_hidden``, ``fp4_hidden``: the hidden size of 8-bit
     and 4-bit head calls; ``processed``: sized for sampling under logit rules
-    as well).
+    as well, ``distill`` for distillation losses).
 
     Zero-filled once at creation; the library leaves it ready for the next
     call.  Calls sharing one workspace must be ordered on one stream."""
 
     def __init__(self, B: int, M: int, V: int, r: int, sample: bool, device=None,
                  hidden: int | None = None, backward: bool = False, int8_hidden: int | None = None,
-                 processed: bool = False, fp4_hidden: int | None = None):
+                 processed: bool = False, fp4_hidden: int | None = None, distill: bool = False):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.type != "cuda":
             raise ValueError(f"the head runs on a GPU; the workspace would be on {device}")
@@ -108,6 +108,8 @@ class Workspace:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(B, M, int8_hidden)))
         if fp4_hidden is not None:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_fp4_workspace_bytes(B, M, fp4_hidden)))
+        if distill:
+            self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_distill_workspace_bytes(B, M, V)))
         if processed:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_processed_workspace_bytes(B, M, V, r)))
         self.device = device
@@ -828,3 +830,73 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
     if check:
         read_device_error(workspace)
     return tokens_out, logits_out
+
+
+def _teacher(logits, teacher_ids, teacher_logits, temperature):
+    """(B, M, V, K, T) of a distillation call whose arguments fit together."""
+    B, M, V = _block(logits, None, "logits")
+    K = teacher_ids.shape[-1] if teacher_ids.dim() else 0
+    if tuple(teacher_ids.shape) != (B, M, K) or teacher_ids.is_floating_point():
+        raise ValueError(f"teacher_ids must be integer ids [{B}, {M}, K], got {teacher_ids.dtype} {tuple(teacher_ids.shape)}")
+    if tuple(teacher_logits.shape) != (B, M, K):
+        raise ValueError(f"teacher_logits must be {(B, M, K)}, got {tuple(teacher_logits.shape)}")
+    return B, M, V, K, float(temperature)
+
+
+def distill_block_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits: torch.Tensor, *,
+                       temperature: float = 1.0, workspace: Workspace | None = None):
+    """Distillation of the drafter's logits [B, M, V] from a teacher's top
+    logits: teacher_ids and teacher_logits [B, M, K] (K up to 1024) are its
+    list at each position; entries with an id outside the vocabulary (padding)
+    or a logit of -inf do not count.  With q the softmax of the list and p the
+    softmax of the row, both at ``temperature`` T, a position's loss is
+    T^2 sum_j q_j (log q_j - log p[id_j]).  Returns ``(loss [B, M], stats
+    [B, M, 4])``, both float32; distill_block_loss_backward takes the stats.
+    A row without entries has loss 0; one with entries and no logit above -inf
+    has +inf."""
+    B, M, V, K, T = _teacher(logits, teacher_ids, teacher_logits, temperature)
+    dev = logits.device
+    _check_device(dev, workspace, teacher_ids=teacher_ids, teacher_logits=teacher_logits)
+    tag, ttag = _dtype_tag(logits), _dtype_tag(teacher_logits)
+    loss = torch.empty((B, M), dtype=torch.float32, device=dev)
+    stats = torch.empty((B, M, 4), dtype=torch.float32, device=dev)
+    x, ids, t = logits.contiguous(), teacher_ids.to(torch.int64).contiguous(), teacher_logits.contiguous()
+    if workspace is None:
+        nbytes = int(_lib.load().dspark_markov_distill_workspace_bytes(B, M, V))
+        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+    else:
+        nbytes, buffer = workspace.nbytes, workspace.buffer
+    st = _call(dev, _lib.load().dspark_markov_distill_block, _ptr(x), tag, _ptr(ids), _ptr(t), ttag, B, M, V, K, T,
+               _ptr(loss), _ptr(stats), _ptr(buffer), nbytes)
+    _lib.check(st, "distill_block_loss")
+    return loss, stats
+
+
+def distill_block_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, teacher_ids: torch.Tensor,
+                                teacher_logits: torch.Tensor, stats: torch.Tensor, *, temperature: float = 1.0,
+                                out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the logits [B, M, V] for the gradient [B, M] of
+    distill_block_loss's rows: grad_loss T (p[v] - sum over id_j = v of q_j),
+    in the logits' dtype; zero for a row without entries or with no logit
+    above -inf.  It is the grad_corrected of apply_block_logits_backward.
+    ``stats`` as the forward call returned them, the other arguments as it
+    took them; ``out`` may be ``logits`` itself (in place)."""
+    B, M, V, K, T = _teacher(logits, teacher_ids, teacher_logits, temperature)
+    if tuple(grad_loss.shape) != (B, M) or not grad_loss.is_floating_point():
+        raise ValueError(f"grad_loss must be float {(B, M)}, got {grad_loss.dtype} {tuple(grad_loss.shape)}")
+    if tuple(stats.shape) != (B, M, 4) or stats.dtype != torch.float32:
+        raise ValueError(f"stats must be float32 {(B, M, 4)}, got {stats.dtype} {tuple(stats.shape)}")
+    dev = logits.device
+    _check_device(dev, None, grad_loss=grad_loss, teacher_ids=teacher_ids, teacher_logits=teacher_logits, stats=stats,
+                  out=out)
+    tag, ttag = _dtype_tag(logits), _dtype_tag(teacher_logits)
+    x, ids, t = logits.contiguous(), teacher_ids.to(torch.int64).contiguous(), teacher_logits.contiguous()
+    g, s = grad_loss.to(torch.float32).contiguous(), stats.contiguous()
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor shaped and typed like logits")
+    st = _call(dev, _lib.load().dspark_markov_distill_block_backward, _ptr(g), _ptr(x), tag, _ptr(ids), _ptr(t), ttag,
+               _ptr(s), B, M, V, K, T, _ptr(out))
+    _lib.check(st, "distill_block_loss_backward")
+    return out

@@ -52,6 +52,9 @@ EXPORTS = (
     "dspark_markov_process_block_backward",
     "dspark_markov_processed_workspace_bytes",
     "dspark_markov_sample_block_processed",
+    "dspark_markov_distill_workspace_bytes",
+    "dspark_markov_distill_block",
+    "dspark_markov_distill_block_backward",
     "dspark_markov_read_device_error",
     "dspark_status_string",
     "dspark_markov_last_error",
@@ -158,6 +161,12 @@ def load():
     L.dspark_markov_sample_block_processed.argtypes = [p, i32, p, p, p, i32, rules, i64, i64, i64, i64,
                                                        ctypes.c_double, u64, i64, i64, p, p, p, sz, p]
     L.dspark_markov_sample_block_processed.restype = i32
+    L.dspark_markov_distill_workspace_bytes.argtypes = [i64, i64, i64]
+    L.dspark_markov_distill_workspace_bytes.restype = sz
+    L.dspark_markov_distill_block.argtypes = [p, i32, p, p, i32, i64, i64, i64, i64, ctypes.c_double, p, p, p, sz, p]
+    L.dspark_markov_distill_block.restype = i32
+    L.dspark_markov_distill_block_backward.argtypes = [p, p, i32, p, p, i32, p, i64, i64, i64, i64, ctypes.c_double, p, p]
+    L.dspark_markov_distill_block_backward.restype = i32
     L.dspark_markov_read_device_error.argtypes = [p, p, ctypes.POINTER(i64)]
     L.dspark_markov_read_device_error.restype = i32
     L.dspark_status_string.argtypes = [i32]

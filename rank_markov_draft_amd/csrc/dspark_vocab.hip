@@ -1,8 +1,11 @@
-// dspark_vocab.hip -- host side of the 4-bit vocabulary head
-// (include/dspark_markov.h): argument validation, workspace layout and
-// launches.
+// dspark_vocab.hip -- host side of the 4-bit vocabulary head and of the
+// distillation loss (include/dspark_markov.h): argument validation, workspace
+// layout and launches.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+
+#include "distill.h"
 #include "dspark_markov.h"
 #include "fp4_head.h"
 #include "host_common.h"
@@ -30,6 +33,38 @@ dspark_status_t check_fp4(dspark_dtype_t dtype, int64_t rows, int64_t d, int64_t
   return DSPARK_OK;
 }
 bool fp4_aligned(const void* codes, const void* scales) { return aligned16(codes) && ((uintptr_t)scales & 3u) == 0; }
+
+// What both passes of the distillation loss check; nothing to do: *empty.
+dspark_status_t check_distill(const void* logits, dspark_dtype_t dtype, const int64_t* ids, const void* teacher,
+                              dspark_dtype_t teacher_dtype, int64_t B, int64_t M, int64_t V, int64_t K, double tau,
+                              dspark::DistillParams* p, Ranges* in, size_t* lbytes, bool* empty) {
+  if (!known_dtype(dtype) || !known_dtype(teacher_dtype) || B < 0 || M < 0 || V < 0 || K < 0)
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  int64_t rows = 0, elems = 0, t = 0;
+  if (!mul_ok(B, M, &rows) || !mul_ok(rows, V, &elems) || !mul_ok(elems, 4, &t) || !mul_ok(rows, K, &t) ||
+      !mul_ok(t, 8, &t) || !mul_ok(rows, 16, &t))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  // the kernels hold log2(e) / tau in fp32
+  const float kappa = (float)(1.4426950408889634 / tau);
+  if (!(tau > 0.0) || !std::isnormal(kappa)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (V > ((int64_t)1 << 30) || K > dspark::kDistillMaxEntries) return DSPARK_ERR_UNSUPPORTED;
+  *empty = rows == 0;
+  if (*empty) return DSPARK_OK;
+  if (V == 0 || !logits || (K > 0 && (!ids || !teacher))) return DSPARK_ERR_INVALID_ARGUMENT;
+  *lbytes = (size_t)elems * dtype_bytes(dtype);
+  in->add(ids, (size_t)(rows * K) * sizeof(int64_t));
+  in->add(teacher, (size_t)(rows * K) * dtype_bytes(teacher_dtype));
+  p->logits = logits;
+  p->teacher_ids = ids;
+  p->teacher_logits = teacher;
+  p->rows = rows;
+  p->V = V;
+  p->K = K;
+  p->tau = tau;
+  p->kappa = kappa;
+  p->teacher_bf16 = teacher_dtype == DSPARK_BF16;
+  return DSPARK_OK;
+}
 
 }  // namespace
 
@@ -111,6 +146,63 @@ dspark_status_t dspark_markov_lm_head_fp4(const void* hidden_states, dspark_dtyp
     return DSPARK_ERR_UNSUPPORTED;
   }
   if (e != hipSuccess) return device_failure(e, "fp4 head launch");
+  return DSPARK_OK;
+}
+
+size_t dspark_markov_distill_workspace_bytes(int64_t B, int64_t M, int64_t V) {
+  if (B < 0 || M < 0 || V < 0) return kDataOffset;
+  int64_t rows = 0;
+  if (!mul_ok(B, M, &rows)) return SIZE_MAX;
+  return add_sz(kDataOffset, align256(mul_sz(mul_sz((size_t)rows, (size_t)dspark::distill_slices(rows, V)), 2 * sizeof(float))));
+}
+
+dspark_status_t dspark_markov_distill_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* teacher_ids,
+                                            const void* teacher_logits, dspark_dtype_t teacher_dtype, int64_t B,
+                                            int64_t M, int64_t V, int64_t K, double temperature, float* loss,
+                                            float* stats, void* workspace, size_t workspace_bytes, void* stream) {
+  dspark::DistillParams p{};
+  Ranges in;
+  size_t lbytes = 0;
+  bool empty = false;
+  const dspark_status_t st = check_distill(logits, logits_dtype, teacher_ids, teacher_logits, teacher_dtype, B, M, V, K,
+                                           temperature, &p, &in, &lbytes, &empty);
+  if (st != DSPARK_OK || empty) return st;
+  if (!loss || !stats) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dspark_markov_distill_workspace_bytes(B, M, V)) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t rb = (size_t)p.rows * sizeof(float);
+  in.add(logits, lbytes);
+  if (in.meet(loss, rb) || in.meet(stats, 4 * rb) || overlaps(loss, rb, stats, 4 * rb)) return DSPARK_ERR_INVALID_ARGUMENT;
+  p.loss = loss;
+  p.stats = stats;
+  p.partials = (float*)((char*)workspace + kDataOffset);
+  const hipError_t e = dspark::launch_distill_loss(p, logits_dtype == DSPARK_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return device_failure(e, "distillation loss launch");
+  return DSPARK_OK;
+}
+
+dspark_status_t dspark_markov_distill_block_backward(const float* grad_loss, const void* logits,
+                                                     dspark_dtype_t logits_dtype, const int64_t* teacher_ids,
+                                                     const void* teacher_logits, dspark_dtype_t teacher_dtype,
+                                                     const float* stats, int64_t B, int64_t M, int64_t V, int64_t K,
+                                                     double temperature, void* grad_logits, void* stream) {
+  dspark::DistillParams p{};
+  Ranges in;
+  size_t lbytes = 0;
+  bool empty = false;
+  const dspark_status_t st = check_distill(logits, logits_dtype, teacher_ids, teacher_logits, teacher_dtype, B, M, V, K,
+                                           temperature, &p, &in, &lbytes, &empty);
+  if (st != DSPARK_OK || empty) return st;
+  if (!grad_loss || !stats || !grad_logits) return DSPARK_ERR_INVALID_ARGUMENT;
+  const size_t rb = (size_t)p.rows * sizeof(float);
+  in.add(grad_loss, rb);
+  in.add(stats, 4 * rb);
+  if (in.meet(grad_logits, lbytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (grad_logits != logits && overlaps(grad_logits, lbytes, logits, lbytes)) return DSPARK_ERR_INVALID_ARGUMENT;
+  p.grad_loss = grad_loss;
+  p.stats = const_cast<float*>(stats);
+  p.grad = grad_logits;
+  const hipError_t e = dspark::launch_distill_backward(p, logits_dtype == DSPARK_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return device_failure(e, "distillation gradient launch");
   return DSPARK_OK;
 }
 
