@@ -454,6 +454,50 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
                                                      int64_t* sampled_tokens, void* processed_logits, void* workspace,
                                                      size_t workspace_bytes, void* stream);
 
+/* Sampling from given logits under each request's limits, from given uniform
+ * numbers.  For a row x of logits [B, M, V] and its request's limits, with
+ * w_i = exp((x_i - max x) / temperature): of the tokens in the order of falling
+ * logits, equal ones by rising index,
+ *     the first top_k are kept (0 or less, or V or more: all),
+ *     of those the ones with w_i >= min_p (0 or less, or NaN: all; at most 1),
+ *     of those the shortest prefix whose sum of w reaches top_p of theirs
+ *     (1 or more, or NaN: all; 0 or less: the first),
+ * and the row's token is the first one, by index, at which the running sum of
+ * the kept tokens' w exceeds u times their whole sum, u the row's uniform
+ * number (clamped to [0, 1 - 2^-24]).  Weights and sums are held in 64 bits.
+ * A temperature below 1e-5 (or NaN) takes the first of the largest logits, and
+ * so does a row whose largest is +inf or NaN (which ranks above +inf, as in
+ * dspark_markov_sample_block).  Tokens with a logit of -inf are never drawn: a
+ * row of nothing else gets token -1 and probability 0.
+ * A pointer holds a number for each request; where it is null, the number in
+ * all_* is every request's. */
+typedef struct dspark_token_limits {
+  const float* temperature;  /* device, [B] */
+  const int64_t* top_k;      /* device, [B] */
+  const float* top_p;        /* device, [B] */
+  const float* min_p;        /* device, [B] */
+  int64_t all_top_k;
+  float all_temperature;
+  float all_top_p;
+  float all_min_p;
+} dspark_token_limits_t;
+
+/*   uniforms  device, [B, M] fp32, in [0, 1).
+ *   tokens    device, [B, M] int64 output.
+ *   probs     device, [B, M] fp32 output: the token's w over the kept ones' sum
+ *             (1 for the largest logit at a temperature below 1e-5 or +inf,
+ *             NaN where that is NaN).
+ * Outputs must not overlap an input or each other.  V from 1 to 2^30.  A row's
+ * result does not depend on the others.  B*M == 0 is a successful no-op.  The
+ * workspace must hold dspark_markov_sample_filtered_workspace_bytes(...) bytes
+ * (no zero fill needed). */
+size_t dspark_markov_sample_filtered_workspace_bytes(int64_t B, int64_t M, int64_t V);
+
+dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t logits_dtype, const float* uniforms,
+                                              const dspark_token_limits_t* limits, int64_t B, int64_t M, int64_t V,
+                                              int64_t* tokens, float* probs, void* workspace, size_t workspace_bytes,
+                                              void* stream);
+
 /* Distillation of the drafter's logits from a teacher's top logits, for
  * training.  For a row x of logits [B, M, V] and the teacher's K entries of that
  * position, those with an id outside [0, V) (padding) or a logit of -inf left

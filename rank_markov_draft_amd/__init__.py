@@ -45,7 +45,7 @@ __all__ = ["apply_block_logits", "sample_block_tokens", "apply_block_logits_gate
            "sample_block_tokens_gated", "apply_block_logits_backward", "apply_block_logits_lm_head",
            "quantize_rows", "lm_head_logits_int8", "quantize_blocks_fp4", "dequantize_blocks_fp4",
            "lm_head_logits_fp4", "process_block_logits", "process_block_logits_backward",
-           "sample_block_tokens_processed", "distill_block_loss", "distill_block_loss_backward", "Workspace",
+           "sample_block_tokens_processed", "sample_block_filtered", "distill_block_loss", "distill_block_loss_backward", "Workspace",
            "read_device_error", "workspace_bytes"]
 
 
@@ -88,14 +88,16 @@ class Workspace:
     (``hidden``: the hidden size of gated calls; ``backward``: sized for the
     backward as well; ``int8_hidden``, ``fp4_hidden``: the hidden size of 8-bit
     and 4-bit head calls; ``processed``: sized for sampling under logit rules
-    as well, ``distill`` for distillation losses).
+    as well, ``filtered`` for sampling under limits, ``distill`` for
+    distillation losses).
 
     Zero-filled once at creation; the library leaves it ready for the next
     call.  Calls sharing one workspace must be ordered on one stream."""
 
     def __init__(self, B: int, M: int, V: int, r: int, sample: bool, device=None,
                  hidden: int | None = None, backward: bool = False, int8_hidden: int | None = None,
-                 processed: bool = False, fp4_hidden: int | None = None, distill: bool = False):
+                 processed: bool = False, fp4_hidden: int | None = None, distill: bool = False,
+                 filtered: bool = False):
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.type != "cuda":
             raise ValueError(f"the head runs on a GPU; the workspace would be on {device}")
@@ -108,6 +110,8 @@ class Workspace:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_int8_workspace_bytes(B, M, int8_hidden)))
         if fp4_hidden is not None:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_lm_head_fp4_workspace_bytes(B, M, fp4_hidden)))
+        if filtered:
+            self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_sample_filtered_workspace_bytes(B, M, V)))
         if distill:
             self.nbytes = max(self.nbytes, int(_lib.load().dspark_markov_distill_workspace_bytes(B, M, V)))
         if processed:
@@ -830,6 +834,57 @@ def sample_block_tokens_processed(base_logits: torch.Tensor, first_prev_token_id
     if check:
         read_device_error(workspace)
     return tokens_out, logits_out
+
+
+def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperature: torch.Tensor | float = 1.0, *,
+                          top_k: torch.Tensor | int | None = None, top_p: torch.Tensor | float | None = None,
+                          min_p: torch.Tensor | float | None = None, workspace: Workspace | None = None):
+    """Tokens drawn from logits [B, M, V] under each request's limits, from
+    given uniform numbers [B, M] in [0, 1): ``(tokens [B, M] int64, probs [B, M]
+    float32)``.  With w = exp((x - max x) / temperature), the tokens in the
+    order of falling logits (equal ones by rising index) are cut to the first
+    ``top_k``, of those to the ones with w >= ``min_p``, of those to the shortest
+    prefix whose weight reaches ``top_p`` of theirs; the token is the first one,
+    by index, at which the kept tokens' running weight exceeds u of their sum,
+    its probability its share of it.  Each limit is a number for all requests
+    or a tensor [B]; None (and a top_k of 0, a top_p of 1, a min_p of 0) is off.
+    A temperature below 1e-5 takes the first of the largest logits (so does a
+    row whose largest is +inf or NaN).  A row with nothing above -inf gets token
+    -1 and probability 0.  Weights and their sums are held in 64 bits."""
+    B, M, V = _block(logits, None, "logits")
+    if tuple(uniforms.shape) != (B, M) or not uniforms.is_floating_point():
+        raise ValueError(f"uniforms must be float {(B, M)}, got {uniforms.dtype} {tuple(uniforms.shape)}")
+    dev = logits.device
+    lim, keep = _lib.TokenLimits(), []
+    for name, value, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int64),
+                                    ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
+        if isinstance(value, torch.Tensor):
+            if value.shape != (B,):
+                raise ValueError(f"{name} must be a number or [{B}], got {tuple(value.shape)}")
+            if value.is_floating_point() != dtype.is_floating_point:
+                raise TypeError(f"{name} must be {dtype}, got {value.dtype}")
+            if value.device != dev:
+                raise ValueError(f"{name} is on {value.device}, the logits on {dev}")
+            if value.dtype != dtype or not value.is_contiguous():
+                value = value.to(dtype).contiguous()
+            keep.append(value)
+            setattr(lim, name, value.data_ptr())
+        else:
+            setattr(lim, "all_" + name, off if value is None else int(value) if name == "top_k" else float(value))
+    _check_device(dev, workspace, uniforms=uniforms)
+    tag = _dtype_tag(logits)
+    tokens = torch.empty((B, M), dtype=torch.int64, device=dev)
+    probs = torch.empty((B, M), dtype=torch.float32, device=dev)
+    x, u = logits.contiguous(), uniforms.to(torch.float32).contiguous()
+    if workspace is None:
+        nbytes = int(_lib.load().dspark_markov_sample_filtered_workspace_bytes(B, M, V))
+        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+    else:
+        nbytes, buffer = workspace.nbytes, workspace.buffer
+    st = _call(dev, _lib.load().dspark_markov_sample_filtered, _ptr(x), tag, _ptr(u), lim, B, M, V, _ptr(tokens),
+               _ptr(probs), _ptr(buffer), nbytes)
+    _lib.check(st, "sample_block_filtered")
+    return tokens, probs
 
 
 def _teacher(logits, teacher_ids, teacher_logits, temperature):

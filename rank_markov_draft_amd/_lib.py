@@ -52,6 +52,8 @@ EXPORTS = (
     "dspark_markov_process_block_backward",
     "dspark_markov_processed_workspace_bytes",
     "dspark_markov_sample_block_processed",
+    "dspark_markov_sample_filtered_workspace_bytes",
+    "dspark_markov_sample_filtered",
     "dspark_markov_distill_workspace_bytes",
     "dspark_markov_distill_block",
     "dspark_markov_distill_block_backward",
@@ -81,6 +83,21 @@ class LogitRules(ctypes.Structure):
         ("token_mask", ctypes.c_void_p),
         ("mask_stride_b", ctypes.c_int64),
         ("mask_stride_m", ctypes.c_int64),
+    ]
+
+
+class TokenLimits(ctypes.Structure):
+    """dspark_token_limits_t: device pointers (None: the number for all requests holds)."""
+
+    _fields_ = [
+        ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p),
+        ("top_p", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+        ("all_top_k", ctypes.c_int64),
+        ("all_temperature", ctypes.c_float),
+        ("all_top_p", ctypes.c_float),
+        ("all_min_p", ctypes.c_float),
     ]
 
 
@@ -161,6 +178,10 @@ def load():
     L.dspark_markov_sample_block_processed.argtypes = [p, i32, p, p, p, i32, rules, i64, i64, i64, i64,
                                                        ctypes.c_double, u64, i64, i64, p, p, p, sz, p]
     L.dspark_markov_sample_block_processed.restype = i32
+    L.dspark_markov_sample_filtered_workspace_bytes.argtypes = [i64, i64, i64]
+    L.dspark_markov_sample_filtered_workspace_bytes.restype = sz
+    L.dspark_markov_sample_filtered.argtypes = [p, i32, p, ctypes.POINTER(TokenLimits), i64, i64, i64, p, p, p, sz, p]
+    L.dspark_markov_sample_filtered.restype = i32
     L.dspark_markov_distill_workspace_bytes.argtypes = [i64, i64, i64]
     L.dspark_markov_distill_workspace_bytes.restype = sz
     L.dspark_markov_distill_block.argtypes = [p, i32, p, p, i32, i64, i64, i64, i64, ctypes.c_double, p, p, p, sz, p]

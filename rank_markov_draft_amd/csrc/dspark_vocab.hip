@@ -1,6 +1,6 @@
-// dspark_vocab.hip -- host side of the 4-bit vocabulary head and of the
-// distillation loss (include/dspark_markov.h): argument validation, workspace
-// layout and launches.
+// dspark_vocab.hip -- host side of the 4-bit vocabulary head, of sampling under
+// a request's limits and of the distillation loss (include/dspark_markov.h):
+// argument validation, workspace layout and launches.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -10,6 +10,7 @@
 #include "fp4_head.h"
 #include "host_common.h"
 #include "markov_kernels.h"
+#include "token_filter.h"
 
 namespace {
 
@@ -146,6 +147,53 @@ dspark_status_t dspark_markov_lm_head_fp4(const void* hidden_states, dspark_dtyp
     return DSPARK_ERR_UNSUPPORTED;
   }
   if (e != hipSuccess) return device_failure(e, "fp4 head launch");
+  return DSPARK_OK;
+}
+
+size_t dspark_markov_sample_filtered_workspace_bytes(int64_t B, int64_t M, int64_t V) {
+  if (B < 0 || M < 0 || V < 0) return kDataOffset;
+  int64_t rows = 0;
+  if (!mul_ok(B, M, &rows)) return SIZE_MAX;
+  const size_t groups = mul_sz((size_t)rows, (size_t)(V / dspark::kFilterGroup + 1));
+  return add_sz(kDataOffset, add_sz(align256(mul_sz(groups, sizeof(double))), align256(mul_sz(groups, sizeof(uint32_t)))));
+}
+
+dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t logits_dtype, const float* uniforms,
+                                              const dspark_token_limits_t* limits, int64_t B, int64_t M, int64_t V,
+                                              int64_t* tokens, float* probs, void* workspace, size_t workspace_bytes,
+                                              void* stream) {
+  if (!known_dtype(logits_dtype) || B < 0 || M < 0 || V < 0 || !limits) return DSPARK_ERR_INVALID_ARGUMENT;
+  int64_t rows = 0, elems = 0, t = 0;
+  if (!mul_ok(B, M, &rows) || !mul_ok(rows, V, &elems) || !mul_ok(elems, 4, &t) || !mul_ok(rows, 8, &t))
+    return DSPARK_ERR_INVALID_ARGUMENT;
+  if (V > ((int64_t)1 << 30)) return DSPARK_ERR_UNSUPPORTED;
+  if (rows == 0) return DSPARK_OK;
+  if (V == 0 || !logits || !uniforms || !tokens || !probs) return DSPARK_ERR_INVALID_ARGUMENT;
+  if (!workspace || workspace_bytes < dspark_markov_sample_filtered_workspace_bytes(B, M, V))
+    return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t tb = (size_t)rows * sizeof(int64_t), pb = (size_t)rows * sizeof(float), vb = (size_t)B * sizeof(float);
+  Ranges in;
+  in.add(logits, (size_t)elems * dtype_bytes(logits_dtype));
+  in.add(uniforms, pb);
+  in.add(limits->temperature, vb);
+  in.add(limits->top_k, (size_t)B * sizeof(int64_t));
+  in.add(limits->top_p, vb);
+  in.add(limits->min_p, vb);
+  if (in.meet(tokens, tb) || in.meet(probs, pb) || overlaps(tokens, tb, probs, pb)) return DSPARK_ERR_INVALID_ARGUMENT;
+  dspark::FilterParams p{};
+  p.limits = dspark::TokenLimits{limits->temperature,   limits->top_k,           limits->top_p,     limits->min_p,
+                                 limits->all_top_k,     limits->all_temperature, limits->all_top_p, limits->all_min_p};
+  p.logits = logits;
+  p.uniforms = uniforms;
+  p.tokens = tokens;
+  p.probs = probs;
+  p.sums = (double*)((char*)workspace + kDataOffset);
+  p.tops = (uint32_t*)((char*)p.sums + align256((size_t)rows * (size_t)(V / dspark::kFilterGroup + 1) * sizeof(double)));
+  p.rows = rows;
+  p.M = M;
+  p.V = V;
+  const hipError_t e = dspark::launch_token_filter(p, logits_dtype == DSPARK_BF16, (hipStream_t)stream);
+  if (e != hipSuccess) return device_failure(e, "filtered sampling launch");
   return DSPARK_OK;
 }
 

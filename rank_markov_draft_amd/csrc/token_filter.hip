@@ -1,0 +1,730 @@
+// token_filter.hip -- sampling from given logits under a request's limits
+// (gfx950).
+//
+// Row x at temperature T, with w_i = 2^((x_i - max x) log2(e) / T): the tokens
+// in the order of falling logits, ties by rising index, are cut to the first
+// top_k, of those to the ones with w >= min_p, of those to the shortest
+// prefix whose weight reaches top_p of theirs; the token is the first one, by
+// index, at which the running weight of the kept ones exceeds u of their sum.
+//
+// The borders decide tokens, and a row has up to V of them, so weights are
+// computed in 64 bits and, wherever sums of them are compared, summed as
+// integers of at least 32 and usually 45 bits below the largest weight: a sum
+// does not depend on its order, and atomics may form it.
+//
+// Two launches.  The first reads the rows once, all of the device sharing
+// them, and leaves the largest logit of every group of 128 columns (and the
+// sum of its weights, for rows without top_k and min_p).  The second gives
+// each row a workgroup, which needs the groups that can hold a kept token
+// only: no token below the k-th largest of k groups' maxima is among the k
+// largest, none below max + T ln(min_p) passes min_p, and those below
+// (1 - top_p) / V of the sum together do not reach what top_p leaves out.  If
+// what is left fits its list (2048 tokens) it sorts them; else it finds each
+// border by counts and sums over bins of the row, narrowed until the border's
+// bin fits the list.
+#include "device_common.h"
+#include "token_filter.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kCap = 2048, kBins = 2048, kPer = kCap / kThreads;
+static_assert(kBins == kCap, "bins and masses share memory");
+constexpr int kVec = 8;
+constexpr uint32_t kNone = 0x007FFFFFu;     // code of -inf: what can be drawn lies above
+constexpr uint32_t kInfCode = 0xFF800000u;  // code of +inf
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // rows start at any element
+
+__device__ __forceinline__ float value_of(uint32_t code) {
+  return __uint_as_float((code & 0x80000000u) ? code & 0x7FFFFFFFu : ~code);
+}
+
+// The eight logits of a row from column v on; -inf past its end.
+template <bool BF>
+__device__ __forceinline__ void load8(const void* row, int64_t v, int64_t V, float (&x)[kVec]) {
+  if (v + kVec <= V) {
+    const u32x4_any_t* const src = (const u32x4_any_t*)((const char*)row + v * (BF ? 2 : 4));
+    const u32x4_t a = src[0];
+    if constexpr (BF) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[e] = (e & 1) ? bf16_hi(a[e >> 1]) : bf16_lo(a[e >> 1]);
+    } else {
+      const u32x4_t b = src[1];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) x[e] = __uint_as_float(e < 4 ? a[e] : b[e - 4]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      x[e] = v + e < V ? (BF ? bf16_lo(((const uint16_t*)row)[v + e]) : ((const float*)row)[v + e]) : -__builtin_inff();
+  }
+}
+template <bool BF>
+__device__ __forceinline__ float load1(const void* row, int64_t v) {
+  return BF ? bf16_lo(((const uint16_t*)row)[v]) : ((const float*)row)[v];
+}
+
+// 2^t for t <= 0, to 2^-50: 2^(t - n) by a polynomial through the Chebyshev
+// points of [-1/2, 1/2] (1 exactly at zero), times 2^n.
+__device__ __forceinline__ double exp2_64(double t) {
+  t = __builtin_fmax(t, -2000.0);  // -inf too: 2^-2000 is zero
+  const double n = __builtin_rint(t), f = t - n;
+  double y = 0x1.e5e9f548e5726p-28;
+  y = __builtin_fma(y, f, 0x1.b6571de2f2351p-24);
+  y = __builtin_fma(y, f, 0x1.62bfe46117445p-20);
+  y = __builtin_fma(y, f, 0x1.ffcb76789860fp-17);
+  y = __builtin_fma(y, f, 0x1.4309130378460p-13);
+  y = __builtin_fma(y, f, 0x1.5d87fe908f88ap-10);
+  y = __builtin_fma(y, f, 0x1.3b2ab6fba385fp-7);
+  y = __builtin_fma(y, f, 0x1.c6b08d7044119p-5);
+  y = __builtin_fma(y, f, 0x1.ebfbdff82c590p-3);
+  y = __builtin_fma(y, f, 0x1.62e42fefa39f7p-1);
+  return __builtin_ldexp(__builtin_fma(y, f, 1.0), (int)n);
+}
+// Weight of a logit relative to a number m that is not below it.
+__device__ __forceinline__ double weight64(float x, float m, double kappa) {
+  return exp2_64(((double)x - (double)m) * kappa);
+}
+
+// The limits of a row as its kernels use them.
+struct Limits {
+  double kappa;  // log2(e) / T
+  double min_p;  // 0: off, at most 1
+  float T;
+  float top_p;
+  int64_t k;     // V: off
+  bool greedy, nucleus;
+  bool full;     // every token can be kept: the sum over the row is needed
+};
+__device__ __forceinline__ Limits limits_of(const TokenLimits& l, int64_t b, int64_t V) {
+  Limits r;
+  r.T = l.temperature ? l.temperature[b] : l.all_temperature;
+  const int64_t k = l.top_k ? l.top_k[b] : l.all_top_k;
+  r.top_p = l.top_p ? l.top_p[b] : l.all_top_p;
+  const float m = l.min_p ? l.min_p[b] : l.all_min_p;
+  r.greedy = !(r.T >= 1e-5f);
+  r.kappa = 1.4426950408889634 / (double)(r.greedy ? 1.0f : r.T);
+  r.k = k > 0 && k < V ? k : V;
+  r.nucleus = r.top_p < 1.0f;
+  r.min_p = m > 0.0f ? __builtin_fmin((double)m, 1.0) : 0.0;
+  r.full = !r.greedy && r.k == V && r.min_p == 0.0;
+  return r;
+}
+
+// ---------------------------------------------------------------- sums of 64 bits
+__device__ __forceinline__ uint64_t shfl_u64(uint64_t v, int lane) {
+  return ((uint64_t)__shfl((uint32_t)(v >> 32), lane, 64) << 32) | __shfl((uint32_t)v, lane, 64);
+}
+template <typename T>
+__device__ __forceinline__ T shift_up(T v, int by) {  // lane l - by's value
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint64_t s = ((uint64_t)__shfl_up((uint32_t)(u >> 32), by, 64) << 32) | __shfl_up((uint32_t)u, by, 64);
+  return __builtin_bit_cast(T, s);
+}
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {  // inclusive
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) {
+    const T o = shift_up(v, by);
+    if (lane >= by) v += o;
+  }
+  return v;
+}
+__device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1)
+    v += ((uint64_t)__shfl_xor((uint32_t)(v >> 32), off, 64) << 32) | __shfl_xor((uint32_t)v, off, 64);
+  return v;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- groups
+// A wave takes 512 columns of a row at a time, 16 lanes a group.
+constexpr int kGroupThreads = 256, kTurns = 4;                          // turns of a wave
+constexpr int kGroupSlice = kGroupThreads / 64 * kTurns * 64 * kVec;   // columns of a workgroup
+
+template <bool BF>
+__global__ __launch_bounds__(kGroupThreads) void filter_groups_kernel(FilterParams p, int64_t r0, unsigned slices) {
+  const int64_t n = r0 + blockIdx.x / slices;
+  const int lane = threadIdx.x & 63;
+  const int64_t v0 = (int64_t)(blockIdx.x % slices) * kGroupSlice + (threadIdx.x >> 6) * (kTurns * 64 * kVec) + lane * kVec;
+  const char* const row = (const char*)p.logits + n * p.V * (BF ? 2 : 4);
+  const int64_t G = filter_groups(p.V);
+  const Limits lim = limits_of(p.limits, n / p.M, p.V);
+  float x[kTurns][kVec];
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j) load8<BF>(row, v0 + j * 64 * kVec, p.V, x[j]);
+#pragma unroll
+  for (int j = 0; j < kTurns; ++j) {
+    const int64_t v = v0 + j * 64 * kVec;
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) top = max(top, ordered_code(x[j][e]));
+#pragma unroll
+    for (int off = 1; off < 16; off *= 2) top = max(top, (uint32_t)__shfl_xor(top, off, 64));
+    if ((lane & 15) == 0 && v < p.V) p.tops[n * G + v / kFilterGroup] = top;
+    if (lim.full) {
+      double z = 0.0;
+      if (top > kNone && top < kInfCode) {
+        const float m = value_of(top);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) z += weight64(x[j][e], m, lim.kappa);
+      }
+#pragma unroll
+      for (int off = 1; off < 16; off *= 2) z += __shfl_xor(z, off, 64);
+      if ((lane & 15) == 0 && v < p.V) p.sums[n * G + v / kFilterGroup] = z;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- choice
+namespace {
+
+struct Shared {
+  uint64_t keys[kCap];
+  uint64_t mass[kCap];  // of the sorted keys, or bins
+  uint64_t wave[kWaves];
+  uint64_t lo, hi, found, before;
+  uint32_t count;
+  int at;
+};
+
+// Exclusive prefix of a value a thread, and the total.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* total, Shared& s) {
+  const T up = wave_scan(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) s.wave[threadIdx.x >> 6] = __builtin_bit_cast(uint64_t, up);
+  __syncthreads();
+  T base = T(0), all = T(0);
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const T x = __builtin_bit_cast(T, s.wave[w]);
+    if (w < (int)(threadIdx.x >> 6)) base += x;
+    all += x;
+  }
+  *total = all;
+  return base + (up - v);
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, Shared& s) {
+  v = wave_max_u32_to_lane63(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 63) s.wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint64_t m = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = max_u64(m, s.wave[w]);
+  return (uint32_t)m;
+}
+
+// Ascending sort of the list's n keys (a bitonic network).
+__device__ __forceinline__ void sort_keys(Shared& s, int n) {
+  int size = 2;
+  while (size < n) size *= 2;
+  __syncthreads();
+  for (int i = n + threadIdx.x; i < size; i += kThreads) s.keys[i] = ~0ull;
+  __syncthreads();
+  for (int k = 2; k <= size; k *= 2)
+    for (int j = k / 2; j > 0; j /= 2) {
+      for (int i = threadIdx.x; i < size; i += kThreads) {
+        const int o = i ^ j;
+        if (o > i) {
+          const uint64_t a = s.keys[i], b = s.keys[o];
+          if ((a > b) == ((i & k) == 0)) {
+            s.keys[i] = b;
+            s.keys[o] = a;
+          }
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// A token's place in the falling order: rising keys.
+__device__ __forceinline__ uint64_t order_key(uint32_t code, uint32_t i) { return ((uint64_t)~code << 32) | i; }
+__device__ __forceinline__ uint32_t key_code(uint64_t k) { return ~(uint32_t)(k >> 32); }
+
+// A row on its way to a token.
+template <bool BF>
+struct Choice {
+  const char* row;
+  int64_t V;
+  double kappa, min_p;
+  float m;         // the largest logit
+  uint32_t bound;  // code below which nothing is kept
+  int scale;       // weights are integers of 2^-scale
+  Shared* s;
+
+  __device__ __forceinline__ uint64_t mass(double w) const {
+    // w 2^scale <= 2^51: the sum's mantissa is the rounded integer
+    return __builtin_bit_cast(uint64_t, __builtin_ldexp(w, scale) + 0x1p52) & 0xFFFFFFFFFFFFFull;
+  }
+  // The mass of a token that passes min_p, else 0.
+  __device__ __forceinline__ uint64_t mass_of(uint32_t code) const {
+    const double w = weight64(value_of(code), m, kappa);
+    return w >= min_p ? mass(w) : 0;
+  }
+
+  // f(code, column) for the row's tokens that may be kept.
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+    for (int64_t v = threadIdx.x * kVec; v < V; v += kThreads * kVec) {
+      float x[kVec];
+      load8<BF>(row, v, V, x);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const uint32_t c = ordered_code(x[e]);
+        if (c >= bound) f(c, (uint32_t)(v + e));
+      }
+    }
+  }
+
+  // The list of the tokens for which keep(code, key); returns how many there
+  // are (more than kCap: the list is not whole), and their keys' range.
+  template <typename F>
+  __device__ __forceinline__ uint32_t gather(F keep, uint64_t* lo, uint64_t* hi) const {
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s->count = 0;
+      s->lo = ~0ull;
+      s->hi = 0;
+    }
+    __syncthreads();
+    uint64_t l = ~0ull, h = 0;
+    each([&](uint32_t c, uint32_t i) {
+      const uint64_t k = order_key(c, i);
+      if (!keep(c, k)) return;
+      l = k < l ? k : l;
+      h = k > h ? k : h;
+      const uint32_t at = atomicAdd(&s->count, 1u);
+      if (at < kCap) s->keys[at] = k;
+    });
+    if (l <= h) {
+      atomicMin((unsigned long long*)&s->lo, (unsigned long long)l);
+      atomicMax((unsigned long long*)&s->hi, (unsigned long long)h);
+    }
+    __syncthreads();
+    *lo = s->lo;
+    *hi = s->hi;
+    return s->count;
+  }
+
+  // The first of n amounts (in s->mass) whose running sum, begun at `before`,
+  // reaches the target: its place, and the sum before it.  One does.
+  __device__ __forceinline__ int reach(int n, uint64_t before, uint64_t target, uint64_t* sum) const {
+    uint64_t a[kPer], t = 0, all;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x * kPer + j;
+      a[j] = i < n ? s->mass[i] : 0;
+      t += a[j];
+    }
+    uint64_t up = before + block_scan(t, &all, *s);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (up < target && target <= up + a[j]) {
+        s->at = threadIdx.x * kPer + j;
+        s->found = up;
+      }
+      up += a[j];
+    }
+    __syncthreads();
+    *sum = s->found;
+    return s->at;
+  }
+  __device__ __forceinline__ uint64_t total(int n) const {
+    uint64_t t = 0, all;
+    __syncthreads();
+    for (int i = threadIdx.x * kPer; i < threadIdx.x * kPer + kPer; ++i) t += i < n ? s->mass[i] : 0;
+    block_scan(t, &all, *s);
+    return all;
+  }
+
+  // The key of the border among the tokens with keys up to `last`: the first at
+  // which their count reaches the target, or (MASS) their mass that share of
+  // `whole`, or of theirs where that is 0.
+  template <bool MASS>
+  __device__ uint64_t border(uint64_t last, uint64_t target, float share, uint64_t whole, float lowest) const {
+    // first by even bins of the logit's distance from the largest
+    const float width = m - lowest;
+    const float per = width > 0.0f && width < 3.0e38f ? (float)kBins / width : 0.0f;
+    auto line = [&](uint32_t c) __attribute__((always_inline)) {
+      const float d = (m - value_of(c)) * per;  // NaN (inf 0) falls into bin 0 with all others
+      return d < (float)(kBins - 1) ? (int)d : d >= (float)(kBins - 1) ? kBins - 1 : 0;
+    };
+    auto amount = [&](uint32_t c) __attribute__((always_inline)) -> uint64_t { return MASS ? mass_of(c) : 1; };
+    auto clear = [&]() __attribute__((always_inline)) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < kBins; i += kThreads) s->mass[i] = 0;
+      __syncthreads();
+    };
+    auto add = [&](int bin, uint64_t a) __attribute__((always_inline)) {
+      atomicAdd((unsigned long long*)&s->mass[bin], (unsigned long long)a);
+    };
+    clear();
+    each([&](uint32_t c, uint32_t i) {
+      if (order_key(c, i) <= last) add(line(c), amount(c));
+    });
+    const uint64_t all = total(kBins);
+    if (MASS) target = part_up(whole ? whole : all, share);
+    if (target > all) return last;
+    uint64_t before = 0, lo, hi;
+    const int b = reach(kBins, 0, target, &before);
+    uint32_t n = gather([&](uint32_t c, uint64_t k) { return k <= last && line(c) == b; }, &lo, &hi);
+    while (n > kCap) {
+      // then by bins of the key, of a power of two each
+      int shift = 0;
+      while (((hi - lo) >> shift) >= kBins) ++shift;
+      clear();
+      each([&](uint32_t c, uint32_t i) {
+        const uint64_t k = order_key(c, i);
+        if (k >= lo && k <= hi) add((int)((k - lo) >> shift), amount(c));
+      });
+      const uint64_t l = lo + ((uint64_t)reach(kBins, before, target, &before) << shift);
+      if (shift == 0) return l;
+      const uint64_t h = l + ((1ull << shift) - 1);
+      const uint64_t end = h < hi ? h : hi;
+      n = gather([&](uint32_t, uint64_t k) { return k >= l && k <= end; }, &lo, &hi);
+    }
+    sort_keys(*s, (int)n);
+    for (int i = threadIdx.x; i < (int)n; i += kThreads) s->mass[i] = amount(key_code(s->keys[i]));
+    uint64_t sum;
+    const int at = reach((int)n, before, target, &sum);
+    return s->keys[at];
+  }
+
+  // ceil(share total), at least 1; floor(u total).
+  static __device__ __forceinline__ uint64_t part_up(uint64_t total, float share) {
+    const uint64_t f = share > 0.0f ? (uint64_t)((double)share * 0x1p40) : 0;
+    const uint64_t up = __umul64hi(total, f << 24) + (total * (f << 24) != 0);
+    return up > 0 ? up : 1;
+  }
+  static __device__ __forceinline__ uint64_t part_down(uint64_t total, float u) {
+    const double c = fmin(fmax((double)u, 0.0), 1.0 - 0x1p-24);  // NaN: 0
+    return __umul64hi(total, (uint64_t)(c * 0x1p40) << 24);
+  }
+
+  // The column at which the running mass, by index, of the tokens with keys up
+  // to `last` exceeds u of their sum, which is left in *z.
+  __device__ int64_t draw(uint64_t last, float u, uint64_t* z) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    constexpr int64_t kStep = 64 * kVec;
+    int64_t a = 0, b = V;
+    uint64_t target = 0;  // of what is left of it in [a, b)
+    bool first = true;
+    auto kept = [&](float x, int64_t i) __attribute__((always_inline)) -> uint64_t {
+      const uint32_t c = ordered_code(x);
+      return c >= bound && order_key(c, (uint32_t)i) <= last ? mass_of(c) : 0;
+    };
+    while (first || b - a > kStep) {
+      const int64_t part = ((b - a + kWaves - 1) / kWaves + kStep - 1) / kStep * kStep;
+      const int64_t w0 = a + wave * part, w1 = w0 + part < b ? w0 + part : b;
+      uint64_t t = 0;
+      for (int64_t v = w0 + lane * kVec; v < w1; v += kStep) {
+        float x[kVec];
+        load8<BF>(row, v, V, x);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) t += kept(x[e], v + e);
+      }
+      t = wave_sum_u64(t);
+      __syncthreads();
+      if (lane == 0) s->wave[wave] = t;
+      __syncthreads();
+      if (first) {
+        uint64_t all = 0;
+        for (int w = 0; w < kWaves; ++w) all += s->wave[w];
+        *z = all;
+        target = part_down(all, u);
+        first = false;
+      }
+      uint64_t up = 0;
+      int w = 0;
+      while (w < kWaves - 1 && up + s->wave[w] <= target) up += s->wave[w++];
+      target -= up;
+      a += w * part;
+      b = a + part < b ? a + part : b;
+    }
+    // at most 512 columns, eight a lane: every wave finds the same
+    float x[kVec];
+    uint64_t k[kVec], t = 0;
+    const int64_t v = a + lane * kVec;
+    load8<BF>(row, v < b ? v : V, V, x);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      k[e] = kept(x[e], v + e);
+      t += k[e];
+    }
+    const uint64_t up = wave_scan(t) - t;
+    int64_t at = -1;
+    uint64_t run = up;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if (at < 0 && run <= target && target < run + k[e]) at = v + e;
+      run += k[e];
+    }
+    const uint64_t hit = __ballot(at >= 0);
+    return (int64_t)shfl_u64((uint64_t)at, hit ? __builtin_ctzll(hit) : 0);
+  }
+};
+
+}  // namespace
+
+template <bool BF>
+__global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p, int64_t r0) {
+  __shared__ Shared s;
+  const int64_t n = r0 + blockIdx.x, V = p.V, G = filter_groups(V);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const uint32_t* const tops = p.tops + n * G;
+  const double* const sums = p.sums + n * G;
+  const Limits lim = limits_of(p.limits, n / p.M, V);
+  const float u = p.uniforms[n];
+  Choice<BF> c;
+  c.row = (const char*)p.logits + n * V * (BF ? 2 : 4);
+  c.V = V;
+  c.kappa = lim.kappa;
+  c.min_p = lim.min_p;
+  c.s = &s;
+  {
+    int bits = 0;
+    while (((int64_t)1 << bits) < V) ++bits;
+    c.scale = 62 - bits < 51 ? 62 - bits : 51;
+  }
+  // a thread's groups are consecutive
+  const int64_t per = (G + kThreads - 1) / kThreads, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
+  uint32_t own = 0, low = 0xFFFFFFFFu;
+  for (int64_t g = g0; g < g1; ++g) {
+    const uint32_t t = tops[g];
+    own = max(own, t);
+    if (t > kNone) low = min(low, t);
+  }
+  const uint32_t top = block_max(own, s);
+  int64_t token = -1;
+  float prob = 0.0f;
+  auto finish = [&]() __attribute__((always_inline)) {
+    if (tid == 0) {
+      p.tokens[n] = token;
+      p.probs[n] = prob;
+    }
+  };
+  if (top <= kNone) return finish();  // nothing to draw from
+  if (lim.greedy || top >= kInfCode) {
+    // the first of the largest, in the first group that has it
+    int64_t g = g0;
+    while (g < g1 && tops[g] != top) ++g;
+    const uint32_t not_mine = g < g1 ? 0xFFFFFFFFu - (uint32_t)g : 0u;
+    g = 0xFFFFFFFFu - block_max(not_mine, s);
+    uint32_t best = 0;
+    for (int j = 0; j < kFilterGroup / 64; ++j) {
+      const int64_t v = g * kFilterGroup + j * 64 + lane;
+      if (v < V && ordered_code(load1<BF>(c.row, v)) == top) best = max(best, 0xFFFFFFFFu - (uint32_t)v);
+    }
+    best = (uint32_t)__builtin_amdgcn_readlane((int)wave_max_u32_to_lane63(best), 63);
+    token = 0xFFFFFFFFu - best;
+    prob = top == 0xFFFFFFFFu ? __builtin_nanf("") : 1.0f;
+    return finish();
+  }
+  const float m = value_of(top);
+  c.m = m;
+
+  if (lim.full && !lim.nucleus) {
+    // every token is kept: to the group by the groups' sums, then within it
+    double t = 0.0, z;
+    for (int64_t g = g0; g < g1; ++g)
+      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa);
+    const double up = block_scan(t, &z, s), target = fmin(fmax((double)u, 0.0), 1.0 - 0x1p-24) * z;
+    __syncthreads();
+    if (tid == 0) s.found = 0;
+    __syncthreads();
+    // the last thread that begins at or below the target and holds anything
+    if (t > 0.0 && up <= target) atomicMax((unsigned long long*)&s.found, (unsigned long long)tid + 1);
+    __syncthreads();
+    if (s.found == (uint64_t)tid + 1) {
+      double run = up, begin = up;
+      int64_t at = g0;
+      for (int64_t g = g0; g < g1 && run <= target; ++g) {
+        const double z = tops[g] > kNone ? sums[g] * weight64(value_of(tops[g]), m, c.kappa) : 0.0;
+        if (z == 0.0) continue;
+        at = g;
+        begin = run;
+        run += z;
+      }
+      s.lo = (uint64_t)at;
+      s.hi = __builtin_bit_cast(uint64_t, begin);
+    }
+    __syncthreads();
+    const int64_t v = (int64_t)s.lo * kFilterGroup + 2 * lane;
+    double w[2];
+    for (int e = 0; e < 2; ++e) {
+      const float x = v + e < V ? load1<BF>(c.row, v + e) : -__builtin_inff();
+      w[e] = weight64(x, m, c.kappa);
+    }
+    // the last token that begins at or below the target and weighs anything
+    const double b0 = __builtin_bit_cast(double, s.hi) + (wave_scan(w[0] + w[1]) - (w[0] + w[1])), b1 = b0 + w[0];
+    uint32_t best = 0;
+    if (w[0] > 0.0 && b0 <= target) best = 2 * lane + 1;
+    if (w[1] > 0.0 && b1 <= target) best = 2 * lane + 2;
+    best = (uint32_t)__builtin_amdgcn_readlane((int)wave_max_u32_to_lane63(best), 63);
+    token = (int64_t)s.lo * kFilterGroup + (best > 0 ? best - 1 : 0);
+    if (best == 0) {  // rounding of the group's sum put the target before its first token
+      const uint64_t some = __ballot(w[0] > 0.0 || w[1] > 0.0);
+      const int l = some ? __builtin_ctzll(some) : 0;
+      token = (int64_t)s.lo * kFilterGroup + 2 * l + (__shfl(w[0] > 0.0 ? 1 : 0, l, 64) ? 0 : 1);
+    }
+    prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa) / z);
+    return finish();
+  }
+
+  // ---- a bound below which nothing is kept
+  uint32_t bound = kNone + 1;
+  if (lim.k <= kThreads) {
+    // the k-th largest of the threads' maxima, to its upper 16 bits
+    __syncthreads();
+    s.keys[tid] = own;
+    __syncthreads();
+    uint32_t v[kWaves], kth = 0;
+    for (int j = 0; j < kWaves; ++j) v[j] = (uint32_t)s.keys[j * 64 + lane];
+    for (int bit = 31; bit >= 16; --bit) {
+      const uint32_t t = kth | (1u << bit);
+      int64_t cnt = 0;
+      for (int j = 0; j < kWaves; ++j) cnt += __popcll(__ballot(v[j] >= t));
+      if (cnt >= lim.k) kth = t;
+    }
+    bound = max(bound, kth);
+  }
+  if (lim.min_p > 0.0) {
+    // a little below the border: the tokens next to it are looked at one by one
+    const double x = (double)m + log(lim.min_p) * (double)lim.T;
+    const float f = (float)(x - 1e-5 * (fabs(x) + fabs((double)m)));
+    if (f > -3.0e38f) bound = max(bound, ordered_code(f));
+  }
+  uint64_t whole = 0;  // mass of the row where groups below the bound count too
+  if (lim.full) {
+    double t = 0.0, z;
+    for (int64_t g = g0; g < g1; ++g)
+      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa);
+    block_scan(t, &z, s);
+    whole = (uint64_t)__builtin_rint(__builtin_ldexp(z, c.scale));
+    // what weighs less than (1 - top_p) z / V reaches no more than 1 - top_p of
+    // z with all its like (and a little less, for the roundings)
+    const double share = (1.0 - fmax((double)lim.top_p, 0.0)) * 0.999, x = (double)m + log(share * z / (double)V) * (double)lim.T;
+    const float f = (float)(x - 1e-5 * (fabs(x) + fabs((double)m)));
+    if (f > -3.0e38f) bound = max(bound, min(ordered_code(f), top));
+  }
+  c.bound = min(bound, top);
+
+  // ---- the groups that reach it, and their tokens, while they fit the list
+  uint32_t mine = 0;
+  for (int64_t g = g0; g < g1; ++g) mine += tops[g] >= c.bound;
+  uint64_t groups;
+  const uint64_t before = block_scan((uint64_t)mine, &groups, s);
+  uint32_t count = kCap + 1;
+  if (groups <= kCap) {
+    uint32_t* const list = (uint32_t*)s.mass;
+    uint32_t at = (uint32_t)before;
+    __syncthreads();
+    for (int64_t g = g0; g < g1; ++g)
+      if (tops[g] >= c.bound) list[at++] = (uint32_t)g;
+    if (tid == 0) s.count = 0;
+    __syncthreads();
+    for (uint32_t i = tid >> 4; i < (uint32_t)groups; i += kThreads / 16) {
+      float x[kVec];
+      const int64_t v = (int64_t)list[i] * kFilterGroup + (tid & 15) * kVec;
+      load8<BF>(c.row, v, V, x);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const uint32_t code = ordered_code(x[e]);
+        if (code >= c.bound) {
+          const uint32_t slot = atomicAdd(&s.count, 1u);
+          if (slot < kCap) s.keys[slot] = order_key(code, (uint32_t)(v + e));
+        }
+      }
+    }
+    __syncthreads();
+    count = s.count;
+  }
+  uint64_t z;
+  if (count <= kCap) {
+    sort_keys(s, (int)count);
+    int kept = lim.k < (int64_t)count ? (int)lim.k : (int)count;
+    for (int i = tid; i < kept; i += kThreads) s.mass[i] = c.mass_of(key_code(s.keys[i]));
+    if (lim.nucleus) {
+      uint64_t sum;
+      const uint64_t all = c.total(kept), target = Choice<BF>::part_up(whole ? whole : all, lim.top_p);
+      if (target <= all) kept = c.reach(kept, 0, target, &sum) + 1;
+    }
+    z = c.total(kept);
+    const uint64_t target = Choice<BF>::part_down(z, u);
+    // by index: the key's halves change places, the lower one now the place in the list
+    __syncthreads();
+    uint64_t k[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * kThreads;
+      k[j] = i < kept ? (s.keys[i] << 32) | (uint32_t)i : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (tid + j * kThreads < kept) s.keys[tid + j * kThreads] = k[j];
+    sort_keys(s, kept);
+    uint64_t a[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid + j * kThreads;
+      a[j] = i < kept ? s.mass[(uint32_t)s.keys[i]] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      if (tid + j * kThreads < kept) s.mass[tid + j * kThreads] = a[j];
+    uint64_t sum;
+    token = (int64_t)(s.keys[c.reach(kept, 0, target + 1, &sum)] >> 32);
+  } else {
+    // lowest of the groups' maxima: most of what is above the bins' end counts
+    const float lowest = value_of(max(c.bound, 0xFFFFFFFFu - block_max(0xFFFFFFFFu - low, s)));
+    uint64_t last = ~0ull;
+    if (lim.k < V) last = c.template border<false>(last, (uint64_t)lim.k, 0.0f, 0, lowest);
+    if (lim.nucleus) last = c.template border<true>(last, 0, lim.top_p, whole, lowest);
+    token = c.draw(last, u, &z);
+  }
+  prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa) / __builtin_ldexp((double)z, -c.scale));
+  finish();
+}
+
+namespace {
+// launch(r0, rows) for parts of the rows whose workgroups of `threads` fit one launch.
+template <typename F>
+hipError_t by_rows(int64_t rows, int64_t groups, int threads, F launch) {
+  const int64_t step = kLaunchGroups / (threads / 256) / groups;
+  if (step < 1) return hipErrorNotSupported;
+  for (int64_t r = 0; r < rows; r += step) {
+    launch(r, rows - r < step ? rows - r : step);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+template <bool BF>
+hipError_t filter_go(const FilterParams& p, hipStream_t s) {
+  const int64_t slices = (p.V + kGroupSlice - 1) / kGroupSlice;
+  const hipError_t e = by_rows(p.rows, slices, kGroupThreads, [&](int64_t r, int64_t rows) {
+    hipLaunchKernelGGL(filter_groups_kernel<BF>, dim3((unsigned)(rows * slices)), dim3(kGroupThreads), 0, s, p, r,
+                       (unsigned)slices);
+  });
+  if (e != hipSuccess) return e;
+  return by_rows(p.rows, 1, kThreads, [&](int64_t r, int64_t rows) {
+    hipLaunchKernelGGL(filter_choose_kernel<BF>, dim3((unsigned)rows), dim3(kThreads), 0, s, p, r);
+  });
+}
+}  // namespace
+
+hipError_t launch_token_filter(const FilterParams& p, bool bf16, hipStream_t s) {
+  return bf16 ? filter_go<true>(p, s) : filter_go<false>(p, s);
+}
+
+}  // namespace dspark
