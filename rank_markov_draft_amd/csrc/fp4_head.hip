@@ -234,14 +234,31 @@ __device__ __forceinline__ f32x16_t mfma_fp4(i32x4_t a, i32x4_t b, f32x16_t c, u
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
+// Loads to LDS as load_lds16 and load_lds4, with a scalar offset besides the
+// lanes' (which need no addition for each load then): past the buffer's end
+// where their sum is.  soff is at most the buffer's size.
+__device__ __forceinline__ void load_lds16_at(const BufferWords& r, uint32_t off, uint32_t soff, uint32_t lds) {
+  uint32_t saved;
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %4\n\ts_nop 2\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds\n\ts_mov_b32 m0, %0"
+                   : "=&s"(saved) : "v"(off), "s"(r.w), "s"(soff), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+}
+__device__ __forceinline__ void load_lds4_at(const BufferWords& r, uint32_t off, uint32_t soff, uint32_t lds) {
+  uint32_t saved;
+  __asm__ volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %4\n\ts_nop 2\n\tbuffer_load_dword %1, %2, %3 offen lds\n\ts_mov_b32 m0, %0"
+                   : "=&s"(saved) : "v"(off), "s"(r.w), "s"(soff), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory");
+}
+
 // A workgroup of WM x WN waves owns tiles of 32 MI WM rows x 32 NJ WN
 // vocabulary columns and walks them in a persistent loop; a wave holds MI x
 // NJ blocks of 32 x 32 sums.  The inner dimension is cut into chunks of 128
-// bytes of codes (256 numbers) and their 8 scale bytes; a chunk's rows of
-// codes (16 bytes a lane) and of scales (4 bytes a lane) are loaded straight
-// into LDS, up to STAGES chunks at a time.  A row's eight 16-byte pieces sit at
-// positions piece ^ (row % 8), so that the fragment reads of eight consecutive
-// rows fall on different banks.  The chunk stream runs on across tiles.
+// bytes of codes (256 numbers; half of that reads L2 at half its rate) and
+// their 8 scale bytes; a chunk's rows of codes (16 bytes a lane) and of scales
+// (4 bytes a lane) are loaded straight into LDS, up to STAGES chunks at a time.
+// A row's eight 16-byte pieces sit at positions piece ^ (row / 2 % 8): a
+// fragment read takes sixteen consecutive rows at a time, over LDS's 64 banks,
+// and these fall on all of them once (216 bytes a clock and CU, against 117 at
+// piece ^ (row % 8), where rows eight apart meet).  The chunk stream runs on
+// across tiles.
 //
 // The rows of codes of x are padded with zeros to whole chunks, and scales past
 // a row's blocks are read as zeros (2^-127), so that what of the head's next
@@ -249,7 +266,10 @@ __device__ __forceinline__ f32x16_t mfma_fp4(i32x4_t a, i32x4_t b, f32x16_t c, u
 //
 // AHEAD (tiles bound by the matrix cores): the fragments of a product are
 // read while the product before it runs, and the hand-over from chunk to
-// chunk (wait, barrier, first reads) runs behind the chunk's last products.
+// chunk (wait, barrier, first reads, the next loads one by one between
+// products) runs behind the chunk's last products.  The sums are pinned after
+// each step, or the compiler would move all of a chunk's products past the wait
+// for the next one's loads (at 2560 rows 9% of the time).
 // Otherwise (tiles bound by the head's stream) all of a chunk's fragments are
 // read at once, so that their latency is paid once a chunk.
 template <int MI, int NJ, int WM, int WN, int STAGES, bool AHEAD, bool OBF>
@@ -278,7 +298,6 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
   const int G = (int)gridDim.x;
   const int first = G % 8 == 0 ? ((int)blockIdx.x % 8) * (G / 8) + (int)blockIdx.x / 8 : (int)blockIdx.x;
   const int my = first < tiles ? (tiles - 1 - first) / G + 1 : 0;
-  const int total = my * C;
 
   // ---- the load stream
   int lt = 0, lc = 0;  // tile (of mine) and chunk
@@ -293,35 +312,50 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     sb = buffer_words(p.ws + v0 * lws, nv * lws);
   };
   // load instruction j of this wave fills rows 8 (wave + j NW) .. + 7, lane l
-  // the position l % 8 of row l / 8 (which holds piece l % 8 ^ row % 8)
+  // the position l % 8 of row l / 8 (which holds piece l % 8 ^ row / 2 % 8); the
+  // scales' fill rows 32 i .. + 31 of x, then of the head, lane l word l % 2 of
+  // row l / 2 (every wave issues PS of them, the last one over again)
   const uint32_t row8 = 8u * (uint32_t)wave + (uint32_t)(lane >> 3);
-  const uint32_t q16 = 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
-  const uint32_t offa = row8 * ldx + q16, offb = row8 * ldw + q16;
-  auto issue = [&](int g) __attribute__((always_inline)) {  // chunk g of the stream, in order
-    const bool live = g < total;
-    const uint32_t k0 = (uint32_t)lc * BK;
-    const uint32_t stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]);
+  const uint32_t q16 = 16u * ((uint32_t)(lane & 7) ^ (row8 >> 1 & 7));
+  static_assert(NW % 2 == 0, "a lane's swizzle is the same for all its rows");
+  uint32_t offa[PA], offb[PB], offs[PS];
 #pragma unroll
-    for (int j = 0; j < PA; ++j)
-      load_lds16(ba, live ? offa + (uint32_t)(8 * NW * j) * ldx + k0 : kBufferOob, stage + 1024u * (uint32_t)(wave + NW * j));
+  for (int j = 0; j < PA; ++j) offa[j] = (row8 + (uint32_t)(8 * NW * j)) * ldx + q16;
 #pragma unroll
-    for (int j = 0; j < PB; ++j)
-      load_lds16(bb, live ? offb + (uint32_t)(8 * NW * j) * ldw + k0 : kBufferOob,
-                 stage + BM * BK + 1024u * (uint32_t)(wave + NW * j));
-    // scales: instruction i fills rows 32 i .. + 31 of x, then of the head, lane
-    // l word l % 2 of row l / 2.  Every wave issues PS, the last one over again.
+  for (int j = 0; j < PB; ++j) offb[j] = (row8 + (uint32_t)(8 * NW * j)) * ldw + q16;
+  auto scale_rows = [&](int j) __attribute__((always_inline)) { return wave + NW * j < SI ? wave + NW * j : SI - 1; };
 #pragma unroll
-    for (int j = 0; j < PS; ++j) {
-      const int i = wave + NW * j < SI ? wave + NW * j : SI - 1;
+  for (int j = 0; j < PS; ++j) {
+    const int i = scale_rows(j);
+    const bool x = i < BM / 32;
+    offs[j] = (32u * (uint32_t)(x ? i : i - BM / 32) + (uint32_t)(lane >> 1)) * (x ? lxs : lws) + 4u * (uint32_t)(lane & 1);
+  }
+  auto load = [&](int g, int q) __attribute__((always_inline)) {  // load q of chunk g of the stream
+    const uint32_t k0 = (uint32_t)lc * BK, stage = lds_address(&lds[(uint32_t)(g % STAGES) * STAGE]);
+    if (q < PA) {
+      load_lds16_at(ba, offa[q < PA ? q : 0], k0, stage + 1024u * (uint32_t)(wave + NW * q));
+    } else if (q < PA + PB) {
+      const int j = q - PA;
+      load_lds16_at(bb, offb[j < PB ? j : 0], k0, stage + BM * BK + 1024u * (uint32_t)(wave + NW * j));
+    } else {
+      const int j = q - PA - PB, i = scale_rows(j);
       const bool x = i < BM / 32;
-      const uint32_t ld = x ? lxs : lws, k = (uint32_t)lc * SB + 4u * (uint32_t)(lane & 1);
-      const uint32_t row = 32u * (uint32_t)(x ? i : i - BM / 32) + (uint32_t)(lane >> 1);
-      load_lds4(x ? sa : sb, live && k < ld ? row * ld + k : kBufferOob, stage + CODES + 256u * (uint32_t)i);
+      const uint32_t k = (uint32_t)lc * SB;
+      load_lds4_at(x ? sa : sb, k + 4u * (uint32_t)(lane & 1) < (x ? lxs : lws) ? offs[j < PS ? j : 0] : kBufferOob, k,
+                   stage + CODES + 256u * (uint32_t)i);
     }
+  };
+  auto next = [&]() __attribute__((always_inline)) {  // on to the stream's next chunk
     if (++lc == C) {
       lc = 0;
       if (++lt < my) bind(lt);
+      else ba = bb = sa = sb = buffer_words(p.xc, 0);  // the loads past the last chunk bring zeros
     }
+  };
+  auto issue = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) load(g, q);
+    next();
   };
 
   // ---- the products: fragments of the wave's MI x NJ blocks for one matrix
@@ -335,7 +369,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     uint32_t a[MI], b[NJ];
   };
   auto read = [&](int g, int s, Frags& f) __attribute__((always_inline)) {  // step s of chunk g
-    const unsigned char* const st = &lds[(g % STAGES) * STAGE + 16 * ((2 * s + (lane >> 5)) ^ (lane & 7))];
+    const unsigned char* const st = &lds[(g % STAGES) * STAGE + 16 * ((2 * s + (lane >> 5)) ^ (lane >> 1 & 7))];
 #pragma unroll
     for (int i = 0; i < MI; ++i) f.a[i] = *(const i32x4_t*)(st + (32 * (MI * wm + i) + (lane & 31)) * BK);
 #pragma unroll
@@ -356,11 +390,16 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     }
   };
   f32x16_t acc[MI][NJ];
-  auto multiply = [&](auto step, const Frags& f, const Scales& sc) __attribute__((always_inline)) {
+  // product q of step s
+  auto product = [&](auto s, int q, const Frags& f, const Scales& sc) __attribute__((always_inline)) {
+    const int i = q / NJ, j = q % NJ;
+    acc[i][j] = mfma_fp4<decltype(s)::value>(f.a[i], f.b[j], acc[i][j], sc.a[i], sc.b[j]);
+    if constexpr (AHEAD) __asm__ volatile("" : "+a"(acc[i][j]));  // no instruction: the sum stays in its place
+  };
+  auto multiply = [&](auto s, const Frags& f, const Scales& sc) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) acc[i][j] = mfma_fp4<decltype(step)::value>(f.a[i], f.b[j], acc[i][j], sc.a[i], sc.b[j]);
+    for (int q = 0; q < MI * NJ; ++q) product(s, q, f, sc);
+    if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
   };
   using std::integral_constant;
   constexpr integral_constant<int, 0> s0{};
@@ -407,8 +446,16 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
         lds_barrier();
         read(g + 1, 0, f[0]);  // before the loads, which would hold up LDS
         read_scales(g + 1, sn);
-        issue(g + STAGES);
-        multiply(s3, f[1], sc);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < MI * NJ; ++q) {
+          product(s3, q, f[1], sc);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int l = q * PER / (MI * NJ); l < (q + 1) * PER / (MI * NJ); ++l) load(g + STAGES, l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        next();
         sc = sn;
       } else {
         // chunk g has landed for every wave, and every wave has read chunk g - 1
@@ -440,6 +487,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     unsigned char* const mine = &lds[STAGES * STAGE + wave * EBYTES];
     constexpr int PIECES = EROW / 16, HALF = PIECES / 2;  // of a row
     constexpr int SETS = ER / 8;                          // groups of 8 rows in an exchange
+    auto turned = [](int q, int half) __attribute__((always_inline)) {
+      const int r = q + HALF * half;
+      return r < PIECES ? r : r - PIECES;
+    };
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
@@ -455,7 +506,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
             for (int j = 0; j < NJ; ++j) {
               const float y = acc[i][j][4 * (SETS * x + u) + e];
               const int byte = (32 * j + (lane & 31)) * OS;
-              unsigned char* const at = mine + (lr + e) * EROW + 16 * ((byte >> 4) ^ (HALF * (lane >> 5))) + (byte & 15);
+              unsigned char* const at = mine + (lr + e) * EROW + 16 * turned(byte >> 4, lane >> 5) + (byte & 15);
               if constexpr (OBF) *(uint16_t*)at = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
               else *(float*)at = y;
             }
@@ -463,7 +514,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
 #pragma unroll
         for (int h = 0; h < ER * PIECES / 64; ++h) {
           const int pc = lane + 64 * h, lr = pc / PIECES, q = pc % PIECES;
-          const u32x4_t w = *(const u32x4_t*)(mine + lr * EROW + 16 * (q ^ (HALF * (lr >> 2 & 1))));
+          const u32x4_t w = *(const u32x4_t*)(mine + lr * EROW + 16 * turned(q, lr >> 2 & 1));
           const int64_t n = rb + lr, v = v0 + q * (16 / OS);
           if (n < p.rows && v < p.V) {
             unsigned char* const dst = (unsigned char*)p.out + (n * p.V + v) * OS;
@@ -499,11 +550,50 @@ hipError_t head_go(const Fp4HeadParams& p, bool obf, int groups, hipStream_t s) 
 }
 }  // namespace
 
+// The forms of the kernel, and what a round of their tiles over the CUs takes
+// (us at d = 5120, the one hidden size at which they were timed against each
+// other).  The form with the shortest sum of rounds is taken.  At V = 129280, in
+// us: 1 row 70 (32x128), 68 (32x256); 64 rows 134, 117 (32 rows), 95 (64x128), 81
+// (64x256); 128 rows 137 (64x256), 99 (128x256), 104 (192x256); 320 rows 239
+// (128x256), 195 (192x256), 170 (320x128), 163 (320x192), 219 (256x256); 2560
+// rows 1378, 1100, 1210, 1171, 1110.  37 rows of 2056 at V = 32003: 13.5
+// (32x128), 9.1 (64x128), 12.8 (64x256).
+namespace {
+struct Form {
+  int bm, bn;
+  float round;
+};
+constexpr Form kForms[] = {{32, 128, 17.5f},  {64, 128, 24.0f},  {64, 256, 40.0f}, {128, 256, 45.0f},
+                           {192, 256, 46.0f}, {256, 256, 56.0f}, {320, 128, 42.0f}, {320, 192, 54.0f}};
+int pick_form(int64_t rows, int64_t V, int num_cus) {
+  int best = 0;
+  double least = 0.0;
+  for (int i = 0; i < (int)(sizeof(kForms) / sizeof(kForms[0])); ++i) {
+    const Form& f = kForms[i];
+    const int64_t tiles = ((rows + f.bm - 1) / f.bm) * ((V + f.bn - 1) / f.bn);
+    const double cost = (double)((tiles + num_cus - 1) / num_cus) * f.round;
+    if (i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  return best;
+}
+}  // namespace
+
 hipError_t launch_fp4_head(const Fp4HeadParams& p, bool out_bf16, int num_cus, hipStream_t s) {
-  if (num_cus < 1 || p.ldx % kFp4K != 0 || p.ldx < 16 * p.blocks || p.blocks % 4 != 0 || 32 * p.blocks > kFp4MaxInner + 128)
+  if (num_cus < 1 || p.ldx % kFp4K != 0 || p.ldx < 16 * p.blocks || p.blocks % 4 != 0 || 32 * p.blocks > kFp4MaxInner)
     return hipErrorNotSupported;
-  if (p.rows <= 32) return head_go<1, 1, 1, 4, 4, false>(p, out_bf16, num_cus, s);
-  return head_go<2, 2, 2, 4, 2, true>(p, out_bf16, num_cus, s);
+  switch (pick_form(p.rows, p.V, num_cus)) {
+    case 0: return head_go<1, 1, 1, 4, 4, false>(p, out_bf16, num_cus, s);
+    case 1: return head_go<1, 1, 2, 4, 3, false>(p, out_bf16, num_cus, s);
+    case 2: return head_go<1, 2, 2, 4, 3, false>(p, out_bf16, num_cus, s);
+    case 3: return head_go<2, 4, 2, 2, 2, true>(p, out_bf16, num_cus, s);
+    case 4: return head_go<3, 4, 2, 2, 2, true>(p, out_bf16, num_cus, s);
+    case 5: return head_go<4, 4, 2, 2, 2, true>(p, out_bf16, num_cus, s);
+    case 6: return head_go<5, 2, 2, 2, 2, true>(p, out_bf16, num_cus, s);
+    default: return head_go<5, 3, 2, 2, 2, true>(p, out_bf16, num_cus, s);
+  }
 }
 
 }  // namespace dspark
