@@ -31,8 +31,10 @@ namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kCap = 2048, kBins = 2048, kPer = kCap / kThreads;
-static_assert(kBins == kCap, "bins and masses share memory");
+constexpr int kParts = 1024;  // parts of a row whose masses are kept
+static_assert(kBins == kCap && kParts <= kCap, "bins and masses share memory, and a scan's steps");
 constexpr int kVec = 8;
+constexpr int64_t kStep = 64 * kVec;  // columns a wave takes at once
 constexpr uint32_t kNone = 0x007FFFFFu;     // code of -inf: what can be drawn lies above
 constexpr uint32_t kInfCode = 0xFF800000u;  // code of +inf
 typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // rows start at any element
@@ -187,6 +189,7 @@ namespace {
 struct Shared {
   uint64_t keys[kCap];
   uint64_t mass[kCap];  // of the sorted keys, or bins
+  uint64_t part[kParts];
   uint64_t wave[kWaves];
   uint64_t lo, hi, found, before;
   uint32_t count;
@@ -257,6 +260,8 @@ struct Choice {
   float m;         // the largest logit
   uint32_t bound;  // code below which nothing is kept
   int scale;       // weights are integers of 2^-scale
+  int64_t part;    // columns of a part: at most kParts of them, whole steps of a wave
+  const uint32_t* tops;
   Shared* s;
 
   __device__ __forceinline__ uint64_t mass(double w) const {
@@ -269,18 +274,50 @@ struct Choice {
     return w >= min_p ? mass(w) : 0;
   }
 
+  // f(codes, first column) for eight columns a lane, 512 a wave, wherever one of
+  // the wave's groups reaches the bound; the waves take turns.  `columns` are
+  // loaded while the ones before them are worked on.
+  template <typename F>
+  __device__ __forceinline__ void steps(F f) const {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t n = (V + kStep - 1) / kStep, G = filter_groups(V);
+    // 64 of the wave's steps at a time, a lane each, to see which of them count
+    for (int64_t i0 = wave; i0 < n; i0 += 64 * kWaves) {
+      const int64_t i = i0 + (int64_t)lane * kWaves;
+      uint32_t t = 0;
+#pragma unroll
+      for (int j = 0; j < kStep / kFilterGroup; ++j)
+        if (i * (kStep / kFilterGroup) + j < G) t = max(t, tops[i * (kStep / kFilterGroup) + j]);
+      uint64_t live = __ballot(t >= bound);
+      if (live == 0) continue;
+      auto first = [&](uint64_t m) __attribute__((always_inline)) {
+        return (i0 + (int64_t)__builtin_ctzll(m) * kWaves) * kStep + lane * kVec;
+      };
+      int64_t v = first(live);
+      float x[kVec];
+      load8<BF>(row, v, V, x);
+      while (live) {
+        live &= live - 1;
+        uint32_t c[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) c[e] = ordered_code(x[e]);
+        const int64_t at = v;
+        if (live) {
+          v = first(live);
+          load8<BF>(row, v, V, x);
+        }
+        f(c, at);
+      }
+    }
+  }
   // f(code, column) for the row's tokens that may be kept.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    for (int64_t v = threadIdx.x * kVec; v < V; v += kThreads * kVec) {
-      float x[kVec];
-      load8<BF>(row, v, V, x);
+    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const uint32_t c = ordered_code(x[e]);
-        if (c >= bound) f(c, (uint32_t)(v + e));
-      }
-    }
+      for (int e = 0; e < kVec; ++e)
+        if (c[e] >= bound) f(c[e], (uint32_t)(v + e));
+    });
   }
 
   // The list of the tokens for which keep(code, key); returns how many there
@@ -313,15 +350,15 @@ struct Choice {
     return s->count;
   }
 
-  // The first of n amounts (in s->mass) whose running sum, begun at `before`,
+  // The first of n amounts whose running sum, begun at `before`,
   // reaches the target: its place, and the sum before it.  One does.
-  __device__ __forceinline__ int reach(int n, uint64_t before, uint64_t target, uint64_t* sum) const {
+  __device__ __forceinline__ int reach(const uint64_t* from, int n, uint64_t before, uint64_t target, uint64_t* sum) const {
     uint64_t a[kPer], t = 0, all;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = threadIdx.x * kPer + j;
-      a[j] = i < n ? s->mass[i] : 0;
+      a[j] = i < n ? from[i] : 0;
       t += a[j];
     }
     uint64_t up = before + block_scan(t, &all, *s);
@@ -337,65 +374,199 @@ struct Choice {
     *sum = s->found;
     return s->at;
   }
-  __device__ __forceinline__ uint64_t total(int n) const {
+  __device__ __forceinline__ uint64_t total(const uint64_t* from, int n) const {
     uint64_t t = 0, all;
     __syncthreads();
-    for (int i = threadIdx.x * kPer; i < threadIdx.x * kPer + kPer; ++i) t += i < n ? s->mass[i] : 0;
+    for (int i = threadIdx.x * kPer; i < threadIdx.x * kPer + kPer; ++i) t += i < n ? from[i] : 0;
     block_scan(t, &all, *s);
     return all;
   }
 
-  // The key of the border among the tokens with keys up to `last`: the first at
-  // which their count reaches the target, or (MASS) their mass that share of
-  // `whole`, or of theirs where that is 0.
-  template <bool MASS>
-  __device__ uint64_t border(uint64_t last, uint64_t target, float share, uint64_t whole, float lowest) const {
-    // first by even bins of the logit's distance from the largest
+  // Even bins of a logit's distance from the largest, the last one for all
+  // that lie further away.
+  __device__ __forceinline__ float bins_of(float lowest) const {
     const float width = m - lowest;
-    const float per = width > 0.0f && width < 3.0e38f ? (float)kBins / width : 0.0f;
-    auto line = [&](uint32_t c) __attribute__((always_inline)) {
-      const float d = (m - value_of(c)) * per;  // NaN (inf 0) falls into bin 0 with all others
-      return d < (float)(kBins - 1) ? (int)d : d >= (float)(kBins - 1) ? kBins - 1 : 0;
-    };
-    auto amount = [&](uint32_t c) __attribute__((always_inline)) -> uint64_t { return MASS ? mass_of(c) : 1; };
-    auto clear = [&]() __attribute__((always_inline)) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kBins; i += kThreads) s->mass[i] = 0;
-      __syncthreads();
-    };
-    auto add = [&](int bin, uint64_t a) __attribute__((always_inline)) {
-      atomicAdd((unsigned long long*)&s->mass[bin], (unsigned long long)a);
-    };
-    clear();
-    each([&](uint32_t c, uint32_t i) {
-      if (order_key(c, i) <= last) add(line(c), amount(c));
-    });
-    const uint64_t all = total(kBins);
-    if (MASS) target = part_up(whole ? whole : all, share);
-    if (target > all) return last;
-    uint64_t before = 0, lo, hi;
-    const int b = reach(kBins, 0, target, &before);
-    uint32_t n = gather([&](uint32_t c, uint64_t k) { return k <= last && line(c) == b; }, &lo, &hi);
+    return width > 0.0f && width < 3.0e38f ? (float)kBins / width : 0.0f;
+  }
+  __device__ __forceinline__ int bin(uint32_t c, float per) const {
+    const float d = (m - value_of(c)) * per;  // NaN (inf 0) falls into bin 0 with all others
+    return d < (float)(kBins - 1) ? (int)d : d >= (float)(kBins - 1) ? kBins - 1 : 0;
+  }
+  __device__ __forceinline__ void clear(uint64_t* p, int n) const {
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) p[i] = 0;
+    __syncthreads();
+  }
+  template <bool MASS>
+  __device__ __forceinline__ uint64_t amount(uint32_t c) const {
+    if constexpr (MASS) return mass_of(c);
+    else return 1;
+  }
+
+  // The key at which the running count (MASS: mass) of the n tokens with keys
+  // in [lo, hi] reaches the target, begun at `before`: by bins of the key, of
+  // a power of two each, until the border's bin fits the list.  The list may
+  // hold them already.
+  template <bool MASS>
+  __device__ __forceinline__ uint64_t narrow(uint32_t n, uint64_t lo, uint64_t hi, uint64_t before, uint64_t target) const {
     while (n > kCap) {
-      // then by bins of the key, of a power of two each
       int shift = 0;
       while (((hi - lo) >> shift) >= kBins) ++shift;
-      clear();
+      clear(s->mass, kBins);
       each([&](uint32_t c, uint32_t i) {
         const uint64_t k = order_key(c, i);
-        if (k >= lo && k <= hi) add((int)((k - lo) >> shift), amount(c));
+        if (k >= lo && k <= hi)
+          atomicAdd((unsigned long long*)&s->mass[(k - lo) >> shift], (unsigned long long)amount<MASS>(c));
       });
-      const uint64_t l = lo + ((uint64_t)reach(kBins, before, target, &before) << shift);
+      const uint64_t l = lo + ((uint64_t)reach(s->mass, kBins, before, target, &before) << shift);
       if (shift == 0) return l;
       const uint64_t h = l + ((1ull << shift) - 1);
       const uint64_t end = h < hi ? h : hi;
       n = gather([&](uint32_t, uint64_t k) { return k >= l && k <= end; }, &lo, &hi);
     }
     sort_keys(*s, (int)n);
-    for (int i = threadIdx.x; i < (int)n; i += kThreads) s->mass[i] = amount(key_code(s->keys[i]));
+    for (int i = threadIdx.x; i < (int)n; i += kThreads) s->mass[i] = amount<MASS>(key_code(s->keys[i]));
     uint64_t sum;
-    const int at = reach((int)n, before, target, &sum);
-    return s->keys[at];
+    return s->keys[reach(s->mass, (int)n, before, target, &sum)];
+  }
+
+  // The key of the k-th token; all of them if there are no more than k.
+  __device__ __forceinline__ uint64_t border_count(uint64_t k, float lowest) const {
+    const float per = bins_of(lowest);
+    clear(s->mass, kBins);
+    each([&](uint32_t c, uint32_t) { atomicAdd((uint32_t*)&s->mass[bin(c, per)], 1u); });
+    if (k >= total(s->mass, kBins)) return ~0ull;
+    uint64_t before, lo, hi;
+    const int b = reach(s->mass, kBins, 0, k, &before);
+    const uint32_t n = gather([&](uint32_t c, uint64_t) { return bin(c, per) == b; }, &lo, &hi);
+    return narrow<false>(n, lo, hi, before, k);
+  }
+
+  // The key at which the mass of the tokens with keys up to `last` reaches that
+  // share of `whole`, or of theirs where that is 0, the masses of the parts up
+  // to there left in s->part.  Two passes: sums in fp32 over even bins say which
+  // bin the border lies in, then exact sums are formed of what lies above that
+  // bin and its neighbours, whose tokens are sorted.  Should the border not lie
+  // among them after all, or they not fit the list, it is searched for by exact
+  // sums over bins.
+  __device__ __forceinline__ uint64_t border_mass(uint64_t last, float share, uint64_t whole, float lowest) const {
+    const float per = bins_of(lowest), kf = (float)kappa, mf = (float)min_p;
+    float* const bins = (float*)s->mass;
+    clear(s->mass, kBins / 2);
+    each([&](uint32_t c, uint32_t i) {
+      const float w = __builtin_amdgcn_exp2f((value_of(c) - m) * kf);
+      if (w >= mf && order_key(c, i) <= last) unsafeAtomicAdd(&bins[bin(c, per)], w);
+    });
+    __syncthreads();
+    double a[kPer], t = 0.0, all;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      a[j] = (double)bins[threadIdx.x * kPer + j];
+      t += a[j];
+    }
+    double up = block_scan(t, &all, *s);
+    const double goal = (double)share * (whole ? __builtin_ldexp((double)whole, -scale) : all);
+    if (threadIdx.x == 0) s->at = kBins - 1;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (up < goal && goal <= up + a[j]) s->at = threadIdx.x * kPer + j;
+      up += a[j];
+    }
+    __syncthreads();
+    const int b0 = s->at - 1, b1 = s->at + 1;
+
+    clear(s->part, kParts);
+    if (threadIdx.x == 0) {
+      s->count = 0;
+      s->before = 0;
+    }
+    __syncthreads();
+    uint64_t below = 0;
+    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
+      uint64_t above = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        const uint64_t k = order_key(c[e], (uint32_t)(v + e));
+        if (c[e] < bound || k > last) continue;
+        const int b = bin(c[e], per);
+        if (b < b0) {
+          above += mass_of(c[e]);
+        } else if (b <= b1) {
+          const uint32_t at = atomicAdd(&s->count, 1u);
+          if (at < kCap) s->keys[at] = k;
+        } else if (!whole) {
+          below += mass_of(c[e]);
+        }
+      }
+      if (__ballot(above != 0)) add_part(v, above);
+    });
+    below = wave_sum_u64(below);
+    if ((threadIdx.x & 63) == 0) atomicAdd((unsigned long long*)&s->before, (unsigned long long)below);
+    __syncthreads();
+    below = s->before;
+    const uint32_t n = s->count;
+    const uint64_t above = total(s->part, kParts);
+    if (n <= kCap) {
+      sort_keys(*s, (int)n);
+      for (int i = threadIdx.x; i < (int)n; i += kThreads) s->mass[i] = mass_of(key_code(s->keys[i]));
+      const uint64_t near = total(s->mass, (int)n), target = part_up(whole ? whole : above + near + below, share);
+      if (above < target && target <= above + near) {
+        uint64_t sum;
+        const int at = reach(s->mass, (int)n, above, target, &sum);
+        for (int i = threadIdx.x; i <= at; i += kThreads) {
+          const int64_t v = (uint32_t)s->keys[i];
+          atomicAdd((unsigned long long*)&s->part[(uint32_t)v / (uint32_t)part], (unsigned long long)s->mass[i]);
+        }
+        const uint64_t key = s->keys[at];
+        __syncthreads();
+        return key;
+      }
+    }
+    // by exact sums, from all that can be kept
+    uint64_t l = ~0ull, h = 0, exact = 0;
+    each([&](uint32_t c, uint32_t i) {
+      const uint64_t k = order_key(c, i);
+      if (k > last) return;
+      l = k < l ? k : l;
+      h = k > h ? k : h;
+      exact += mass_of(c);
+    });
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      s->lo = ~0ull;
+      s->hi = 0;
+      s->before = 0;
+    }
+    __syncthreads();
+    atomicMin((unsigned long long*)&s->lo, (unsigned long long)l);
+    atomicMax((unsigned long long*)&s->hi, (unsigned long long)h);
+    atomicAdd((unsigned long long*)&s->before, (unsigned long long)exact);
+    __syncthreads();
+    l = s->lo;
+    h = s->hi;
+    exact = s->before;
+    const uint64_t target = part_up(whole ? whole : exact, share);
+    const uint64_t key = target > exact ? last : narrow<true>(kCap + 1, l, h, 0, target);
+    parts_upto(key);
+    return key;
+  }
+
+  // The masses of the parts, of the tokens with keys up to `last`.
+  __device__ __forceinline__ void parts_upto(uint64_t last) const {
+    clear(s->part, kParts);
+    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
+      uint64_t t = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (c[e] >= bound && order_key(c[e], (uint32_t)(v + e)) <= last) t += mass_of(c[e]);
+      if (__ballot(t != 0)) add_part(v, t);
+    });
+    __syncthreads();
+  }
+  __device__ __forceinline__ void add_part(int64_t v, uint64_t t) const {
+    t = wave_sum_u64(t);
+    if ((threadIdx.x & 63) == 0) atomicAdd((unsigned long long*)&s->part[(uint32_t)v / (uint32_t)part], (unsigned long long)t);
   }
 
   // ceil(share total), at least 1; floor(u total).
@@ -410,20 +581,21 @@ struct Choice {
   }
 
   // The column at which the running mass, by index, of the tokens with keys up
-  // to `last` exceeds u of their sum, which is left in *z.
-  __device__ int64_t draw(uint64_t last, float u, uint64_t* z) const {
+  // to `last`, whose parts' masses stand in s->part, exceeds u of their sum,
+  // which is left in *z.
+  __device__ __forceinline__ int64_t draw(uint64_t last, float u, uint64_t* z) const {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    constexpr int64_t kStep = 64 * kVec;
-    int64_t a = 0, b = V;
-    uint64_t target = 0;  // of what is left of it in [a, b)
-    bool first = true;
+    *z = total(s->part, kParts);
+    uint64_t before, target = part_down(*z, u);
+    int64_t a = (int64_t)reach(s->part, kParts, 0, target + 1, &before) * part, b = a + part < V ? a + part : V;
+    target -= before;  // of what is left of it in [a, b)
     auto kept = [&](float x, int64_t i) __attribute__((always_inline)) -> uint64_t {
       const uint32_t c = ordered_code(x);
       return c >= bound && order_key(c, (uint32_t)i) <= last ? mass_of(c) : 0;
     };
-    while (first || b - a > kStep) {
-      const int64_t part = ((b - a + kWaves - 1) / kWaves + kStep - 1) / kStep * kStep;
-      const int64_t w0 = a + wave * part, w1 = w0 + part < b ? w0 + part : b;
+    while (b - a > kStep) {
+      const int64_t piece = ((b - a + kWaves - 1) / kWaves + kStep - 1) / kStep * kStep;
+      const int64_t w0 = a + wave * piece, w1 = w0 + piece < b ? w0 + piece : b;
       uint64_t t = 0;
       for (int64_t v = w0 + lane * kVec; v < w1; v += kStep) {
         float x[kVec];
@@ -435,19 +607,12 @@ struct Choice {
       __syncthreads();
       if (lane == 0) s->wave[wave] = t;
       __syncthreads();
-      if (first) {
-        uint64_t all = 0;
-        for (int w = 0; w < kWaves; ++w) all += s->wave[w];
-        *z = all;
-        target = part_down(all, u);
-        first = false;
-      }
       uint64_t up = 0;
       int w = 0;
       while (w < kWaves - 1 && up + s->wave[w] <= target) up += s->wave[w++];
       target -= up;
-      a += w * part;
-      b = a + part < b ? a + part : b;
+      a += w * piece;
+      b = a + piece < b ? a + piece : b;
     }
     // at most 512 columns, eight a lane: every wave finds the same
     float x[kVec];
@@ -459,9 +624,8 @@ struct Choice {
       k[e] = kept(x[e], v + e);
       t += k[e];
     }
-    const uint64_t up = wave_scan(t) - t;
+    uint64_t run = wave_scan(t) - t;
     int64_t at = -1;
-    uint64_t run = up;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       if (at < 0 && run <= target && target < run + k[e]) at = v + e;
@@ -494,6 +658,8 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     while (((int64_t)1 << bits) < V) ++bits;
     c.scale = 62 - bits < 51 ? 62 - bits : 51;
   }
+  c.part = (V + kParts * kStep - 1) / (kParts * kStep) * kStep;
+  c.tops = tops;
   // a thread's groups are consecutive
   const int64_t per = (G + kThreads - 1) / kThreads, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
   uint32_t own = 0, low = 0xFFFFFFFFu;
@@ -654,10 +820,10 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     for (int i = tid; i < kept; i += kThreads) s.mass[i] = c.mass_of(key_code(s.keys[i]));
     if (lim.nucleus) {
       uint64_t sum;
-      const uint64_t all = c.total(kept), target = Choice<BF>::part_up(whole ? whole : all, lim.top_p);
-      if (target <= all) kept = c.reach(kept, 0, target, &sum) + 1;
+      const uint64_t all = c.total(s.mass, kept), target = Choice<BF>::part_up(whole ? whole : all, lim.top_p);
+      if (target <= all) kept = c.reach(s.mass, kept, 0, target, &sum) + 1;
     }
-    z = c.total(kept);
+    z = c.total(s.mass, kept);
     const uint64_t target = Choice<BF>::part_down(z, u);
     // by index: the key's halves change places, the lower one now the place in the list
     __syncthreads();
@@ -683,13 +849,15 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     for (int j = 0; j < kPer; ++j)
       if (tid + j * kThreads < kept) s.mass[tid + j * kThreads] = a[j];
     uint64_t sum;
-    token = (int64_t)(s.keys[c.reach(kept, 0, target + 1, &sum)] >> 32);
+    token = (int64_t)(s.keys[c.reach(s.mass, kept, 0, target + 1, &sum)] >> 32);
   } else {
-    // lowest of the groups' maxima: most of what is above the bins' end counts
-    const float lowest = value_of(max(c.bound, 0xFFFFFFFFu - block_max(0xFFFFFFFFu - low, s)));
+    // where the bins end: at the bound, or well below the groups' least maximum
+    const float least = value_of(0xFFFFFFFFu - block_max(0xFFFFFFFFu - low, s));
+    const float lowest = c.bound > kNone + 1 ? value_of(c.bound) : m - 4.0f * (m - least);
     uint64_t last = ~0ull;
-    if (lim.k < V) last = c.template border<false>(last, (uint64_t)lim.k, 0.0f, 0, lowest);
-    if (lim.nucleus) last = c.template border<true>(last, 0, lim.top_p, whole, lowest);
+    if (lim.k < V) last = c.border_count((uint64_t)lim.k, lowest);
+    if (lim.nucleus) last = c.border_mass(last, lim.top_p, whole, lowest);
+    else c.parts_upto(last);
     token = c.draw(last, u, &z);
   }
   prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa) / __builtin_ldexp((double)z, -c.scale));
