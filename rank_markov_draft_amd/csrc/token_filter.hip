@@ -31,10 +31,12 @@ namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kCap = 2048, kBins = 2048, kPer = kCap / kThreads;
-constexpr int kParts = 1024;  // parts of a row whose masses are kept
+constexpr int kParts = 1024, kPartBits = 11;  // parts of a row whose masses are kept, of at least 2^kPartBits columns
 static_assert(kBins == kCap && kParts <= kCap, "bins and masses share memory, and a scan's steps");
 constexpr int kVec = 8;
-constexpr int64_t kStep = 64 * kVec;  // columns a wave takes at once
+constexpr int kStepBits = 9;          // log2 of
+constexpr int64_t kStep = 64 * kVec;  // the columns a wave takes at once
+static_assert(kStep == 1 << kStepBits, "columns of a step");
 constexpr uint32_t kNone = 0x007FFFFFu;     // code of -inf: what can be drawn lies above
 constexpr uint32_t kInfCode = 0xFF800000u;  // code of +inf
 typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));  // rows start at any element
@@ -43,56 +45,86 @@ __device__ __forceinline__ float value_of(uint32_t code) {
   return __uint_as_float((code & 0x80000000u) ? code & 0x7FFFFFFFu : ~code);
 }
 
-// The eight logits of a row from column v on; -inf past its end.
+// Eight logits of a row from column v on, as loaded; -inf past its end.
 template <bool BF>
-__device__ __forceinline__ void load8(const void* row, int64_t v, int64_t V, float (&x)[kVec]) {
+struct Raw {
+  u32x4_t w[BF ? 1 : 2];
+  __device__ __forceinline__ float operator[](int e) const {
+    if constexpr (BF) return (e & 1) ? bf16_hi(w[0][e >> 1]) : bf16_lo(w[0][e >> 1]);
+    else return __uint_as_float(w[e >> 2][e & 3]);
+  }
+};
+template <bool BF>
+__device__ __forceinline__ Raw<BF> load8(const void* row, int64_t v, int64_t V) {
+  Raw<BF> r;
   if (v + kVec <= V) {
     const u32x4_any_t* const src = (const u32x4_any_t*)((const char*)row + v * (BF ? 2 : 4));
-    const u32x4_t a = src[0];
-    if constexpr (BF) {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[e] = (e & 1) ? bf16_hi(a[e >> 1]) : bf16_lo(a[e >> 1]);
-    } else {
-      const u32x4_t b = src[1];
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[e] = __uint_as_float(e < 4 ? a[e] : b[e - 4]);
-    }
+    r.w[0] = src[0];
+    if constexpr (!BF) r.w[1] = src[1];
   } else {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      x[e] = v + e < V ? (BF ? bf16_lo(((const uint16_t*)row)[v + e]) : ((const float*)row)[v + e]) : -__builtin_inff();
+    for (int e = 0; e < kVec; ++e) {
+      const bool in = v + e < V;
+      if constexpr (BF) {
+        const uint32_t b = in ? ((const uint16_t*)row)[v + e] : 0xFF80u;
+        if (e & 1) r.w[0][e >> 1] |= b << 16;
+        else r.w[0][e >> 1] = b;
+      } else {
+        r.w[e >> 2][e & 3] = in ? ((const uint32_t*)row)[v + e] : 0xFF800000u;
+      }
+    }
   }
+  return r;
 }
 template <bool BF>
 __device__ __forceinline__ float load1(const void* row, int64_t v) {
   return BF ? bf16_lo(((const uint16_t*)row)[v]) : ((const float*)row)[v];
 }
 
-// 2^t for t <= 0, to 2^-50: 2^(t - n) by a polynomial through the Chebyshev
-// points of [-1/2, 1/2] (1 exactly at zero), times 2^n.
-__device__ __forceinline__ double exp2_64(double t) {
-  t = __builtin_fmax(t, -2000.0);  // -inf too: 2^-2000 is zero
-  const double n = __builtin_rint(t), f = t - n;
-  double y = 0x1.e5e9f548e5726p-28;
-  y = __builtin_fma(y, f, 0x1.b6571de2f2351p-24);
-  y = __builtin_fma(y, f, 0x1.62bfe46117445p-20);
-  y = __builtin_fma(y, f, 0x1.ffcb76789860fp-17);
-  y = __builtin_fma(y, f, 0x1.4309130378460p-13);
-  y = __builtin_fma(y, f, 0x1.5d87fe908f88ap-10);
-  y = __builtin_fma(y, f, 0x1.3b2ab6fba385fp-7);
-  y = __builtin_fma(y, f, 0x1.c6b08d7044119p-5);
-  y = __builtin_fma(y, f, 0x1.ebfbdff82c590p-3);
-  y = __builtin_fma(y, f, 0x1.62e42fefa39f7p-1);
-  return __builtin_ldexp(__builtin_fma(y, f, 1.0), (int)n);
+// 2^(j / 32), j = 0 .. 31, in LDS: 64 banks hold one table, so that lanes that
+// read different entries never meet in a bank.
+constexpr int kTable = 32;
+__device__ __forceinline__ void fill_table(double* table) {  // a barrier is the caller's
+  if (threadIdx.x < kTable) {
+    // a polynomial through the Chebyshev points of [-1/2, 1/2], 1 exactly at zero, good to 2^-50
+    const double t = threadIdx.x * (1.0 / kTable), n = t > 0.5 ? 1.0 : 0.0, f = t - n;
+    double y = 0x1.e5e9f548e5726p-28;
+    y = __builtin_fma(y, f, 0x1.b6571de2f2351p-24);
+    y = __builtin_fma(y, f, 0x1.62bfe46117445p-20);
+    y = __builtin_fma(y, f, 0x1.ffcb76789860fp-17);
+    y = __builtin_fma(y, f, 0x1.4309130378460p-13);
+    y = __builtin_fma(y, f, 0x1.5d87fe908f88ap-10);
+    y = __builtin_fma(y, f, 0x1.3b2ab6fba385fp-7);
+    y = __builtin_fma(y, f, 0x1.c6b08d7044119p-5);
+    y = __builtin_fma(y, f, 0x1.ebfbdff82c590p-3);
+    y = __builtin_fma(y, f, 0x1.62e42fefa39f7p-1);
+    table[threadIdx.x] = __builtin_fma(y, f, 1.0) * (1.0 + n);
+  }
 }
-// Weight of a logit relative to a number m that is not below it.
-__device__ __forceinline__ double weight64(float x, float m, double kappa) {
-  return exp2_64(((double)x - (double)m) * kappa);
+// 2^(scale + t / 32) for t <= 0, to 2^-50 (1 at zero exactly): the table at t's
+// integer, and a polynomial through the Chebyshev points of [-1/2, 1/2] for what
+// is left of it.  Half the 64-bit operations of a polynomial over a whole
+// octave, and these bound the kernels.
+__device__ __forceinline__ double exp2_32nds(double t, int scale, const double* table) {
+  t = __builtin_fmax(t, -64000.0);  // -inf too: 2^-2000 is zero
+  const double k = t + 0x1.8p52;    // t's integer in the low bits
+  const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, k);
+  const double f = t - (k - 0x1.8p52);
+  double y = 0x1.5d884e708e6aap-35;
+  y = __builtin_fma(y, f, 0x1.3b2b1bee88b09p-27);
+  y = __builtin_fma(y, f, 0x1.c6b08d70400d0p-20);
+  y = __builtin_fma(y, f, 0x1.ebfbdff8131c3p-13);
+  y = __builtin_fma(y, f, 0x1.62e42fefa39efp-6);
+  return __builtin_ldexp(table[n & (kTable - 1)] * __builtin_fma(y, f, 1.0), (n >> 5) + scale);
+}
+// Weight of a logit relative to a number m that is not below it; kappa: 32 log2(e) / T.
+__device__ __forceinline__ double weight64(float x, float m, double kappa, const double* table) {
+  return exp2_32nds(((double)x - (double)m) * kappa, 0, table);
 }
 
 // The limits of a row as its kernels use them.
 struct Limits {
-  double kappa;  // log2(e) / T
+  double kappa;  // 32 log2(e) / T
   double min_p;  // 0: off, at most 1
   float T;
   float top_p;
@@ -107,7 +139,7 @@ __device__ __forceinline__ Limits limits_of(const TokenLimits& l, int64_t b, int
   r.top_p = l.top_p ? l.top_p[b] : l.all_top_p;
   const float m = l.min_p ? l.min_p[b] : l.all_min_p;
   r.greedy = !(r.T >= 1e-5f);
-  r.kappa = 1.4426950408889634 / (double)(r.greedy ? 1.0f : r.T);
+  r.kappa = kTable * 1.4426950408889634 / (double)(r.greedy ? 1.0f : r.T);
   r.k = k > 0 && k < V ? k : V;
   r.nucleus = r.top_p < 1.0f;
   r.min_p = m > 0.0f ? __builtin_fmin((double)m, 1.0) : 0.0;
@@ -157,9 +189,12 @@ __global__ __launch_bounds__(kGroupThreads) void filter_groups_kernel(FilterPara
   const char* const row = (const char*)p.logits + n * p.V * (BF ? 2 : 4);
   const int64_t G = filter_groups(p.V);
   const Limits lim = limits_of(p.limits, n / p.M, p.V);
-  float x[kTurns][kVec];
+  __shared__ double table[kTable];
+  Raw<BF> x[kTurns];
 #pragma unroll
-  for (int j = 0; j < kTurns; ++j) load8<BF>(row, v0 + j * 64 * kVec, p.V, x[j]);
+  for (int j = 0; j < kTurns; ++j) x[j] = load8<BF>(row, v0 + j * 64 * kVec, p.V);
+  fill_table(table);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kTurns; ++j) {
     const int64_t v = v0 + j * 64 * kVec;
@@ -174,7 +209,7 @@ __global__ __launch_bounds__(kGroupThreads) void filter_groups_kernel(FilterPara
       if (top > kNone && top < kInfCode) {
         const float m = value_of(top);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) z += weight64(x[j][e], m, lim.kappa);
+        for (int e = 0; e < kVec; ++e) z += weight64(x[j][e], m, lim.kappa, table);
       }
 #pragma unroll
       for (int off = 1; off < 16; off *= 2) z += __shfl_xor(z, off, 64);
@@ -190,6 +225,8 @@ struct Shared {
   uint64_t keys[kCap];
   uint64_t mass[kCap];  // of the sorted keys, or bins
   uint64_t part[kParts];
+  double table[kTable];
+  float stack[kWaves][63 + kStep];
   uint64_t wave[kWaves];
   uint64_t lo, hi, found, before;
   uint32_t count;
@@ -256,70 +293,144 @@ template <bool BF>
 struct Choice {
   const char* row;
   int64_t V;
-  double kappa, min_p;
+  double kappa, min_p;  // min_p in units of masses
   float m;         // the largest logit
   uint32_t bound;  // code below which nothing is kept
   int scale;       // weights are integers of 2^-scale
-  int64_t part;    // columns of a part: at most kParts of them, whole steps of a wave
+  int part;        // a part's columns are 2^part, so that there are at most kParts
   const uint32_t* tops;
   Shared* s;
 
-  __device__ __forceinline__ uint64_t mass(double w) const {
-    // w 2^scale <= 2^51: the sum's mantissa is the rounded integer
-    return __builtin_bit_cast(uint64_t, __builtin_ldexp(w, scale) + 0x1p52) & 0xFFFFFFFFFFFFFull;
-  }
   // The mass of a token that passes min_p, else 0.
-  __device__ __forceinline__ uint64_t mass_of(uint32_t code) const {
-    const double w = weight64(value_of(code), m, kappa);
-    return w >= min_p ? mass(w) : 0;
+  __device__ __forceinline__ uint64_t mass(float x) const {
+    const double w = exp2_32nds(((double)x - (double)m) * kappa, scale, s->table);
+    // at most 2^51: the sum's mantissa is the rounded integer
+    return w >= min_p ? __builtin_bit_cast(uint64_t, w + 0x1p52) & 0xFFFFFFFFFFFFFull : 0;
   }
+  __device__ __forceinline__ uint64_t mass_of(uint32_t code) const { return mass(value_of(code)); }
 
-  // f(codes, first column) for eight columns a lane, 512 a wave, wherever one of
-  // the wave's groups reaches the bound; the waves take turns.  `columns` are
-  // loaded while the ones before them are worked on.
-  template <typename F>
-  __device__ __forceinline__ void steps(F f) const {
+  // f(logits, first column) for eight columns a lane, 512 a wave, wherever one
+  // of the wave's groups reaches the bound, and done(part) after the last of a
+  // part.  The waves take turns by parts.  A few such steps are loaded before
+  // the first is worked on: a row has few waves to hide its loads behind.
+  template <typename F, typename D>
+  __device__ __forceinline__ void steps(F f, D done) const {
+    constexpr int kLoads = BF ? 4 : 2;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t n = (V + kStep - 1) / kStep, G = filter_groups(V);
+    const int shift = part - kStepBits;  // steps of a part
+    const uint32_t n = (uint32_t)((V + kStep - 1) / kStep), parts = ((n - 1) >> shift) + 1;
+    const uint32_t mine = wave < (int)parts ? ((parts - 1 - wave) / kWaves + 1) << shift : 0;
+    const int64_t G = filter_groups(V);
+    auto step = [&](uint32_t q) __attribute__((always_inline)) {
+      return ((wave + (q >> shift) * kWaves) << shift) + (q & ((1u << shift) - 1));
+    };
+    uint32_t open = 0xFFFFFFFFu;  // the part that has been begun
     // 64 of the wave's steps at a time, a lane each, to see which of them count
-    for (int64_t i0 = wave; i0 < n; i0 += 64 * kWaves) {
-      const int64_t i = i0 + (int64_t)lane * kWaves;
+    for (uint32_t q0 = 0; q0 < mine; q0 += 64) {
+      const int64_t i = step(q0 + lane);
       uint32_t t = 0;
 #pragma unroll
       for (int j = 0; j < kStep / kFilterGroup; ++j)
-        if (i * (kStep / kFilterGroup) + j < G) t = max(t, tops[i * (kStep / kFilterGroup) + j]);
+        if (q0 + lane < mine && i * (kStep / kFilterGroup) + j < G) t = max(t, tops[i * (kStep / kFilterGroup) + j]);
       uint64_t live = __ballot(t >= bound);
-      if (live == 0) continue;
-      auto first = [&](uint64_t m) __attribute__((always_inline)) {
-        return (i0 + (int64_t)__builtin_ctzll(m) * kWaves) * kStep + lane * kVec;
-      };
-      int64_t v = first(live);
-      float x[kVec];
-      load8<BF>(row, v, V, x);
       while (live) {
-        live &= live - 1;
-        uint32_t c[kVec];
+        Raw<BF> x[kLoads];
+        uint32_t at[kLoads];
+        int have = 0;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) c[e] = ordered_code(x[e]);
-        const int64_t at = v;
-        if (live) {
-          v = first(live);
-          load8<BF>(row, v, V, x);
+        for (int j = 0; j < kLoads; ++j) {
+          if (!live) continue;
+          at[j] = step(q0 + (uint32_t)__builtin_ctzll(live));
+          x[j] = load8<BF>(row, (int64_t)at[j] * kStep + lane * kVec, V);
+          live &= live - 1;
+          have = j + 1;
         }
-        f(c, at);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+          if (j >= have) continue;
+          if (open != at[j] >> shift) {
+            if (open != 0xFFFFFFFFu) done(open);
+            open = at[j] >> shift;
+          }
+          f(x[j], (int64_t)at[j] * kStep + lane * kVec);
+        }
       }
     }
+    if (open != 0xFFFFFFFFu) done(open);
   }
   // f(code, column) for the row's tokens that may be kept.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
+    const float least = value_of(bound);
+    steps(
+        [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        if (c[e] >= bound) f(c[e], (uint32_t)(v + e));
-    });
+          for (int e = 0; e < kVec; ++e)
+            if (x[e] >= least) f(ordered_code(x[e]), (uint32_t)(v + e));
+        },
+        [](uint32_t) {});
   }
 
+  // The mass of a wave's tokens that belong to one part.  Those to be counted
+  // are moved together first, so that no lane is idle while masses are computed:
+  // a border usually keeps a few in a hundred of a row.
+  struct Part {
+    uint64_t sum = 0;
+    uint32_t held = 0;  // on the wave's stack
+  };
+  template <typename F>
+  __device__ __forceinline__ void count(Part& q, const Raw<BF>& x, F take) const {
+    float* const stack = s->stack[threadIdx.x >> 6];
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) n += take(e) ? 1u : 0u;
+    if (__ballot(n != 0) == 0) return;
+    const uint32_t upto = wave_inclusive_sum_u32(n);
+    float* to = stack + q.held + (upto - n);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      if (take(e)) *to++ = x[e];
+    q.held += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    __builtin_amdgcn_wave_barrier();
+    while (q.held >= 128) {
+      q.held -= 128;
+      const float y = stack[q.held + lane], z = stack[q.held + 64 + lane];
+      q.sum += mass(y) + mass(z);
+    }
+    if (q.held >= 64) {
+      q.held -= 64;
+      q.sum += mass(stack[q.held + lane]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __device__ __forceinline__ void close(Part& q, uint32_t at) const {
+    const uint32_t lane = threadIdx.x & 63;
+    if (lane < q.held) q.sum += mass(s->stack[threadIdx.x >> 6][lane]);
+    const uint64_t t = wave_sum_u64(q.sum);
+    if (lane == 0) s->part[at] = t;
+    q = Part{};
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // Appends those of eight logits that take(e) names to the list.
+  template <typename F>
+  __device__ __forceinline__ void append(const Raw<BF>& x, int64_t v, F take) const {
+    uint32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) n += take(e) ? 1u : 0u;
+    if (__ballot(n != 0) == 0) return;
+    const uint32_t upto = wave_inclusive_sum_u32(n);
+    uint32_t slot = 0;
+    if ((threadIdx.x & 63) == 63) slot = atomicAdd(&s->count, upto);
+    slot = (uint32_t)__builtin_amdgcn_readlane((int)slot, 63) + upto - n;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e)
+      if (take(e)) {
+        if (slot < kCap) s->keys[slot] = order_key(ordered_code(x[e]), (uint32_t)(v + e));
+        ++slot;
+      }
+  }
   // The list of the tokens for which keep(code, key); returns how many there
   // are (more than kCap: the list is not whole), and their keys' range.
   template <typename F>
@@ -389,8 +500,7 @@ struct Choice {
     return width > 0.0f && width < 3.0e38f ? (float)kBins / width : 0.0f;
   }
   __device__ __forceinline__ int bin(uint32_t c, float per) const {
-    const float d = (m - value_of(c)) * per;  // NaN (inf 0) falls into bin 0 with all others
-    return d < (float)(kBins - 1) ? (int)d : d >= (float)(kBins - 1) ? kBins - 1 : 0;
+    return (int)fminf((m - value_of(c)) * per, (float)(kBins - 1));  // NaN (inf 0) falls into the last one
   }
   __device__ __forceinline__ void clear(uint64_t* p, int n) const {
     __syncthreads();
@@ -444,19 +554,37 @@ struct Choice {
 
   // The key at which the mass of the tokens with keys up to `last` reaches that
   // share of `whole`, or of theirs where that is 0, the masses of the parts up
-  // to there left in s->part.  Two passes: sums in fp32 over even bins say which
+  // to there left in s->part.  Two passes: rough sums over even bins say which
   // bin the border lies in, then exact sums are formed of what lies above that
   // bin and its neighbours, whose tokens are sorted.  Should the border not lie
   // among them after all, or they not fit the list, it is searched for by exact
   // sums over bins.
+  // CUT: not all tokens have keys up to `last`.
+  template <bool CUT>
   __device__ __forceinline__ uint64_t border_mass(uint64_t last, float share, uint64_t whole, float lowest) const {
-    const float per = bins_of(lowest), kf = (float)kappa, mf = (float)min_p;
-    float* const bins = (float*)s->mass;
+    const float per = bins_of(lowest), kf = (float)(kappa / kTable);
+    const float mf = (float)__builtin_ldexp(min_p, -scale), least = value_of(bound);
+    auto within = [&](float x, int64_t i) __attribute__((always_inline)) {
+      if constexpr (CUT) return order_key(ordered_code(x), (uint32_t)i) <= last;
+      else return true;
+    };
+    // weights as integers of 2^-31 of a bound on their sum (float atomics on LDS
+    // take twenty times as long as these)
+    uint32_t* const bins = (uint32_t*)s->mass;
+    int bits = 31;
+    for (uint64_t z = whole ? (whole >> scale) + 1 : (uint64_t)V; z > 1; z = (z + 1) / 2) --bits;
+    const float fb = (float)bits, mb = mf > 0.0f ? mf * __builtin_ldexpf(1.0f, bits) : 0.0f;
     clear(s->mass, kBins / 2);
-    each([&](uint32_t c, uint32_t i) {
-      const float w = __builtin_amdgcn_exp2f((value_of(c) - m) * kf);
-      if (w >= mf && order_key(c, i) <= last) unsafeAtomicAdd(&bins[bin(c, per)], w);
-    });
+    steps(
+        [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            const float d = m - x[e], w = __builtin_amdgcn_exp2f(__builtin_fmaf(-d, kf, fb));
+            if (x[e] >= least && w >= mb && within(x[e], v + e))
+              atomicAdd(&bins[(int)fminf(d * per, (float)(kBins - 1))], (uint32_t)(w + 0.5f));
+          }
+        },
+        [](uint32_t) {});
     __syncthreads();
     double a[kPer], t = 0.0, all;
 #pragma unroll
@@ -465,7 +593,7 @@ struct Choice {
       t += a[j];
     }
     double up = block_scan(t, &all, *s);
-    const double goal = (double)share * (whole ? __builtin_ldexp((double)whole, -scale) : all);
+    const double goal = (double)share * (whole ? __builtin_ldexp((double)whole, bits - scale) : all);
     if (threadIdx.x == 0) s->at = kBins - 1;
     __syncthreads();
 #pragma unroll
@@ -483,24 +611,22 @@ struct Choice {
     }
     __syncthreads();
     uint64_t below = 0;
-    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
-      uint64_t above = 0;
+    Part over;
+    const float high = b0 > 0 ? m - (float)b0 / per : __builtin_inff();
+    const float low = b1 + 1 < kBins ? fmaxf(m - (float)(b1 + 1) / per, least) : least;
+    steps(
+        [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
+          count(over, x, [&](int e) __attribute__((always_inline)) { return x[e] > high && within(x[e], v + e); });
+          append(x, v, [&](int e) __attribute__((always_inline)) {
+            return x[e] >= low && !(x[e] > high) && within(x[e], v + e);
+          });
+          if (!whole) {
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const uint64_t k = order_key(c[e], (uint32_t)(v + e));
-        if (c[e] < bound || k > last) continue;
-        const int b = bin(c[e], per);
-        if (b < b0) {
-          above += mass_of(c[e]);
-        } else if (b <= b1) {
-          const uint32_t at = atomicAdd(&s->count, 1u);
-          if (at < kCap) s->keys[at] = k;
-        } else if (!whole) {
-          below += mass_of(c[e]);
-        }
-      }
-      if (__ballot(above != 0)) add_part(v, above);
-    });
+            for (int e = 0; e < kVec; ++e)
+              if (x[e] >= least && x[e] < low && within(x[e], v + e)) below += mass(x[e]);
+          }
+        },
+        [&](uint32_t at) __attribute__((always_inline)) { close(over, at); });
     below = wave_sum_u64(below);
     if ((threadIdx.x & 63) == 0) atomicAdd((unsigned long long*)&s->before, (unsigned long long)below);
     __syncthreads();
@@ -516,7 +642,7 @@ struct Choice {
         const int at = reach(s->mass, (int)n, above, target, &sum);
         for (int i = threadIdx.x; i <= at; i += kThreads) {
           const int64_t v = (uint32_t)s->keys[i];
-          atomicAdd((unsigned long long*)&s->part[(uint32_t)v / (uint32_t)part], (unsigned long long)s->mass[i]);
+          atomicAdd((unsigned long long*)&s->part[v >> part], (unsigned long long)s->mass[i]);
         }
         const uint64_t key = s->keys[at];
         __syncthreads();
@@ -554,19 +680,17 @@ struct Choice {
 
   // The masses of the parts, of the tokens with keys up to `last`.
   __device__ __forceinline__ void parts_upto(uint64_t last) const {
+    const float least = value_of(bound);
+    Part q;
     clear(s->part, kParts);
-    steps([&](const uint32_t (&c)[kVec], int64_t v) __attribute__((always_inline)) {
-      uint64_t t = 0;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e)
-        if (c[e] >= bound && order_key(c[e], (uint32_t)(v + e)) <= last) t += mass_of(c[e]);
-      if (__ballot(t != 0)) add_part(v, t);
-    });
+    steps(
+        [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
+          count(q, x, [&](int e) __attribute__((always_inline)) {
+            return x[e] >= least && order_key(ordered_code(x[e]), (uint32_t)(v + e)) <= last;
+          });
+        },
+        [&](uint32_t at) __attribute__((always_inline)) { close(q, at); });
     __syncthreads();
-  }
-  __device__ __forceinline__ void add_part(int64_t v, uint64_t t) const {
-    t = wave_sum_u64(t);
-    if ((threadIdx.x & 63) == 0) atomicAdd((unsigned long long*)&s->part[(uint32_t)v / (uint32_t)part], (unsigned long long)t);
   }
 
   // ceil(share total), at least 1; floor(u total).
@@ -587,19 +711,19 @@ struct Choice {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     *z = total(s->part, kParts);
     uint64_t before, target = part_down(*z, u);
-    int64_t a = (int64_t)reach(s->part, kParts, 0, target + 1, &before) * part, b = a + part < V ? a + part : V;
+    int64_t a = (int64_t)reach(s->part, kParts, 0, target + 1, &before) << part;
+    int64_t b = a + ((int64_t)1 << part) < V ? a + ((int64_t)1 << part) : V;
     target -= before;  // of what is left of it in [a, b)
     auto kept = [&](float x, int64_t i) __attribute__((always_inline)) -> uint64_t {
       const uint32_t c = ordered_code(x);
-      return c >= bound && order_key(c, (uint32_t)i) <= last ? mass_of(c) : 0;
+      return c >= bound && order_key(c, (uint32_t)i) <= last ? mass(x) : 0;
     };
     while (b - a > kStep) {
       const int64_t piece = ((b - a + kWaves - 1) / kWaves + kStep - 1) / kStep * kStep;
       const int64_t w0 = a + wave * piece, w1 = w0 + piece < b ? w0 + piece : b;
       uint64_t t = 0;
       for (int64_t v = w0 + lane * kVec; v < w1; v += kStep) {
-        float x[kVec];
-        load8<BF>(row, v, V, x);
+        const Raw<BF> x = load8<BF>(row, v, V);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) t += kept(x[e], v + e);
       }
@@ -615,10 +739,9 @@ struct Choice {
       b = a + piece < b ? a + piece : b;
     }
     // at most 512 columns, eight a lane: every wave finds the same
-    float x[kVec];
     uint64_t k[kVec], t = 0;
     const int64_t v = a + lane * kVec;
-    load8<BF>(row, v < b ? v : V, V, x);
+    const Raw<BF> x = load8<BF>(row, v < b ? v : V, V);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
       k[e] = kept(x[e], v + e);
@@ -639,8 +762,9 @@ struct Choice {
 }  // namespace
 
 template <bool BF>
-__global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p, int64_t r0) {
+__global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams p, int64_t r0) {
   __shared__ Shared s;
+  fill_table(s.table);
   const int64_t n = r0 + blockIdx.x, V = p.V, G = filter_groups(V);
   const int tid = threadIdx.x, lane = tid & 63;
   const uint32_t* const tops = p.tops + n * G;
@@ -651,14 +775,15 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
   c.row = (const char*)p.logits + n * V * (BF ? 2 : 4);
   c.V = V;
   c.kappa = lim.kappa;
-  c.min_p = lim.min_p;
   c.s = &s;
   {
     int bits = 0;
     while (((int64_t)1 << bits) < V) ++bits;
     c.scale = 62 - bits < 51 ? 62 - bits : 51;
   }
-  c.part = (V + kParts * kStep - 1) / (kParts * kStep) * kStep;
+  c.min_p = __builtin_ldexp(lim.min_p, c.scale);
+  c.part = kPartBits;
+  while (((V - 1) >> c.part) >= kParts) ++c.part;
   c.tops = tops;
   // a thread's groups are consecutive
   const int64_t per = (G + kThreads - 1) / kThreads, g0 = tid * per, g1 = g0 + per < G ? g0 + per : G;
@@ -701,7 +826,7 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     // every token is kept: to the group by the groups' sums, then within it
     double t = 0.0, z;
     for (int64_t g = g0; g < g1; ++g)
-      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa);
+      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa, s.table);
     const double up = block_scan(t, &z, s), target = fmin(fmax((double)u, 0.0), 1.0 - 0x1p-24) * z;
     __syncthreads();
     if (tid == 0) s.found = 0;
@@ -713,7 +838,7 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
       double run = up, begin = up;
       int64_t at = g0;
       for (int64_t g = g0; g < g1 && run <= target; ++g) {
-        const double z = tops[g] > kNone ? sums[g] * weight64(value_of(tops[g]), m, c.kappa) : 0.0;
+        const double z = tops[g] > kNone ? sums[g] * weight64(value_of(tops[g]), m, c.kappa, s.table) : 0.0;
         if (z == 0.0) continue;
         at = g;
         begin = run;
@@ -727,7 +852,7 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     double w[2];
     for (int e = 0; e < 2; ++e) {
       const float x = v + e < V ? load1<BF>(c.row, v + e) : -__builtin_inff();
-      w[e] = weight64(x, m, c.kappa);
+      w[e] = weight64(x, m, c.kappa, s.table);
     }
     // the last token that begins at or below the target and weighs anything
     const double b0 = __builtin_bit_cast(double, s.hi) + (wave_scan(w[0] + w[1]) - (w[0] + w[1])), b1 = b0 + w[0];
@@ -741,7 +866,7 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
       const int l = some ? __builtin_ctzll(some) : 0;
       token = (int64_t)s.lo * kFilterGroup + 2 * l + (__shfl(w[0] > 0.0 ? 1 : 0, l, 64) ? 0 : 1);
     }
-    prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa) / z);
+    prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa, s.table) / z);
     return finish();
   }
 
@@ -772,7 +897,7 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
   if (lim.full) {
     double t = 0.0, z;
     for (int64_t g = g0; g < g1; ++g)
-      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa);
+      if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa, s.table);
     block_scan(t, &z, s);
     whole = (uint64_t)__builtin_rint(__builtin_ldexp(z, c.scale));
     // what weighs less than (1 - top_p) z / V reaches no more than 1 - top_p of
@@ -797,18 +922,21 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
       if (tops[g] >= c.bound) list[at++] = (uint32_t)g;
     if (tid == 0) s.count = 0;
     __syncthreads();
-    for (uint32_t i = tid >> 4; i < (uint32_t)groups; i += kThreads / 16) {
-      float x[kVec];
-      const int64_t v = (int64_t)list[i] * kFilterGroup + (tid & 15) * kVec;
-      load8<BF>(c.row, v, V, x);
+    constexpr uint32_t kTurn = kThreads / 16;  // 16 lanes a group
+    const float least = value_of(c.bound);
+    for (uint32_t i = (tid >> 6) * 4 + (lane >> 4), i0 = (tid >> 6) * 4; i0 < (uint32_t)groups; i += 4 * kTurn, i0 += 4 * kTurn) {
+      if (__builtin_amdgcn_readfirstlane((int)__atomic_load_n(&s.count, __ATOMIC_RELAXED)) > kCap) break;  // it does not
+      Raw<BF> x[4];
+      int64_t v[4];
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        const uint32_t code = ordered_code(x[e]);
-        if (code >= c.bound) {
-          const uint32_t slot = atomicAdd(&s.count, 1u);
-          if (slot < kCap) s.keys[slot] = order_key(code, (uint32_t)(v + e));
-        }
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t g = i + j * kTurn;
+        v[j] = g < (uint32_t)groups ? (int64_t)list[g] * kFilterGroup + (tid & 15) * kVec : V;
+        x[j] = load8<BF>(c.row, v[j], V);
       }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        c.append(x[j], v[j], [&](int e) __attribute__((always_inline)) { return x[j][e] >= least; });
     }
     __syncthreads();
     count = s.count;
@@ -856,11 +984,12 @@ __global__ __launch_bounds__(kThreads) void filter_choose_kernel(FilterParams p,
     const float lowest = c.bound > kNone + 1 ? value_of(c.bound) : m - 4.0f * (m - least);
     uint64_t last = ~0ull;
     if (lim.k < V) last = c.border_count((uint64_t)lim.k, lowest);
-    if (lim.nucleus) last = c.border_mass(last, lim.top_p, whole, lowest);
+    if (lim.nucleus && last != ~0ull) last = c.template border_mass<true>(last, lim.top_p, whole, lowest);
+    else if (lim.nucleus) last = c.template border_mass<false>(last, lim.top_p, whole, lowest);
     else c.parts_upto(last);
     token = c.draw(last, u, &z);
   }
-  prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa) / __builtin_ldexp((double)z, -c.scale));
+  prob = (float)(weight64(load1<BF>(c.row, token), m, c.kappa, s.table) / __builtin_ldexp((double)z, -c.scale));
   finish();
 }
 
