@@ -325,8 +325,8 @@ __global__ __launch_bounds__(kThreads) void distill_backward_kernel(DistillParam
 
 int64_t distill_slices(int64_t rows, int64_t V) {
   // enough workgroups to fill the device, of whole turns of their loop
-  const int64_t turn = kAhead * kGroup, most = (V + turn - 1) / turn;
-  const int64_t want = rows > 0 ? (2048 + rows - 1) / rows : 1;
+  const int64_t turn = kAhead * kGroup, most = V / turn + (V % turn != 0);
+  const int64_t want = rows > 0 && rows < 2048 ? (2048 + rows - 1) / rows : 1;
   const int64_t n = want < most ? want : most;
   return n < 1 ? 1 : n;
 }

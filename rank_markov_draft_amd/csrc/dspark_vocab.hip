@@ -201,7 +201,10 @@ size_t dspark_markov_distill_workspace_bytes(int64_t B, int64_t M, int64_t V) {
   if (B < 0 || M < 0 || V < 0) return kDataOffset;
   int64_t rows = 0;
   if (!mul_ok(B, M, &rows)) return SIZE_MAX;
-  return add_sz(kDataOffset, align256(mul_sz(mul_sz((size_t)rows, (size_t)dspark::distill_slices(rows, V)), 2 * sizeof(float))));
+  // a slice's two numbers: rows * distill_slices(rows, V) of them at most, in a
+  // form that no smaller call exceeds
+  const size_t all = mul_sz((size_t)rows, (size_t)dspark::distill_slices(1, V)), some = add_sz((size_t)rows, 2048);
+  return add_sz(kDataOffset, align256(mul_sz(all < some ? all : some, 2 * sizeof(float))));
 }
 
 dspark_status_t dspark_markov_distill_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* teacher_ids,
