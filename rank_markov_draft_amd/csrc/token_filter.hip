@@ -101,20 +101,21 @@ __device__ __forceinline__ void fill_table(double* table) {  // a barrier is the
     table[threadIdx.x] = __builtin_fma(y, f, 1.0) * (1.0 + n);
   }
 }
-// 2^(scale + t / 32) for t <= 0, to 2^-50 (1 at zero exactly): the table at t's
+// 2^(scale + t / 32) for t <= 0, to 2^-42 (1 at zero exactly): the table at t's
 // integer, and a polynomial through the Chebyshev points of [-1/2, 1/2] for what
 // is left of it.  Half the 64-bit operations of a polynomial over a whole
-// octave, and these bound the kernels.
+// octave, and these bound the kernels.  A row has up to V borders between
+// tokens, each moved by at most 2^-42 of the sum: its token is another one than
+// the exact weights' once in 10^7 rows.
 __device__ __forceinline__ double exp2_32nds(double t, int scale, const double* table) {
   t = __builtin_fmax(t, -64000.0);  // -inf too: 2^-2000 is zero
   const double k = t + 0x1.8p52;    // t's integer in the low bits
   const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, k);
   const double f = t - (k - 0x1.8p52);
-  double y = 0x1.5d884e708e6aap-35;
-  y = __builtin_fma(y, f, 0x1.3b2b1bee88b09p-27);
-  y = __builtin_fma(y, f, 0x1.c6b08d70400d0p-20);
-  y = __builtin_fma(y, f, 0x1.ebfbdff8131c3p-13);
-  y = __builtin_fma(y, f, 0x1.62e42fefa39efp-6);
+  double y = 0x1.3b2b07bdf358dp-27;
+  y = __builtin_fma(y, f, 0x1.c6b13c3465457p-20);
+  y = __builtin_fma(y, f, 0x1.ebfbdff82240ap-13);
+  y = __builtin_fma(y, f, 0x1.62e42fef8dc67p-6);
   return __builtin_ldexp(table[n & (kTable - 1)] * __builtin_fma(y, f, 1.0), (n >> 5) + scale);
 }
 // Weight of a logit relative to a number m that is not below it; kappa: 32 log2(e) / T.
@@ -198,18 +199,23 @@ __global__ __launch_bounds__(kGroupThreads) void filter_groups_kernel(FilterPara
 #pragma unroll
   for (int j = 0; j < kTurns; ++j) {
     const int64_t v = v0 + j * 64 * kVec;
-    uint32_t top = 0;
+    float m = x[j][0];
+    bool nan = false;  // which a maximum passes over
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) top = max(top, ordered_code(x[j][e]));
+    for (int e = 0; e < kVec; ++e) {
+      nan = nan || x[j][e] != x[j][e];
+      m = __builtin_fmaxf(m, x[j][e]);
+    }
+    uint32_t top = nan ? 0xFFFFFFFFu : ordered_code(m);
 #pragma unroll
     for (int off = 1; off < 16; off *= 2) top = max(top, (uint32_t)__shfl_xor(top, off, 64));
     if ((lane & 15) == 0 && v < p.V) p.tops[n * G + v / kFilterGroup] = top;
     if (lim.full) {
       double z = 0.0;
       if (top > kNone && top < kInfCode) {
-        const float m = value_of(top);
+        const float all = value_of(top);
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) z += weight64(x[j][e], m, lim.kappa, table);
+        for (int e = 0; e < kVec; ++e) z += weight64(x[j][e], all, lim.kappa, table);
       }
 #pragma unroll
       for (int off = 1; off < 16; off *= 2) z += __shfl_xor(z, off, 64);
@@ -563,7 +569,7 @@ struct Choice {
   template <bool CUT>
   __device__ __forceinline__ uint64_t border_mass(uint64_t last, float share, uint64_t whole, float lowest) const {
     const float per = bins_of(lowest), kf = (float)(kappa / kTable);
-    const float mf = (float)__builtin_ldexp(min_p, -scale), least = value_of(bound);
+    const float least = value_of(bound);  // next to where min_p cuts, if it does
     auto within = [&](float x, int64_t i) __attribute__((always_inline)) {
       if constexpr (CUT) return order_key(ordered_code(x), (uint32_t)i) <= last;
       else return true;
@@ -573,14 +579,14 @@ struct Choice {
     uint32_t* const bins = (uint32_t*)s->mass;
     int bits = 31;
     for (uint64_t z = whole ? (whole >> scale) + 1 : (uint64_t)V; z > 1; z = (z + 1) / 2) --bits;
-    const float fb = (float)bits, mb = mf > 0.0f ? mf * __builtin_ldexpf(1.0f, bits) : 0.0f;
+    const float fb = (float)bits;
     clear(s->mass, kBins / 2);
     steps(
         [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
 #pragma unroll
           for (int e = 0; e < kVec; ++e) {
             const float d = m - x[e], w = __builtin_amdgcn_exp2f(__builtin_fmaf(-d, kf, fb));
-            if (x[e] >= least && w >= mb && within(x[e], v + e))
+            if (x[e] >= least && within(x[e], v + e))
               atomicAdd(&bins[(int)fminf(d * per, (float)(kBins - 1))], (uint32_t)(w + 0.5f));
           }
         },
