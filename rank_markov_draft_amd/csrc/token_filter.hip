@@ -229,10 +229,12 @@ namespace {
 
 struct Shared {
   uint64_t keys[kCap];
-  uint64_t mass[kCap];  // of the sorted keys, or bins
+  union {
+    uint64_t mass[kCap];                // of the sorted keys, or bins
+    float stack[kWaves][63 + kStep];    // logits on their way to masses
+  };
   uint64_t part[kParts];
   double table[kTable];
-  float stack[kWaves][63 + kStep];
   uint64_t wave[kWaves];
   uint64_t lo, hi, found, before;
   uint32_t count;
