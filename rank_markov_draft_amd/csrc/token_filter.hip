@@ -319,11 +319,11 @@ struct Choice {
 
   // f(logits, first column) for eight columns a lane, 512 a wave, wherever one
   // of the wave's groups reaches the bound, and done(part) after the last of a
-  // part.  The waves take turns by parts.  A few such steps are loaded before
-  // the first is worked on: a row has few waves to hide its loads behind.
-  template <typename F, typename D>
+  // part.  The waves take turns by parts.  LOADS such steps are loaded before
+  // the first is worked on: a row has few waves to hide its loads behind.  (What
+  // rarely runs takes one at a time: f stands in the code LOADS times.)
+  template <int LOADS, typename F, typename D>
   __device__ __forceinline__ void steps(F f, D done) const {
-    constexpr int kLoads = BF ? 4 : 2;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int shift = part - kStepBits;  // steps of a part
     const uint32_t n = (uint32_t)((V + kStep - 1) / kStep), parts = ((n - 1) >> shift) + 1;
@@ -342,11 +342,11 @@ struct Choice {
         if (q0 + lane < mine && i * (kStep / kFilterGroup) + j < G) t = max(t, tops[i * (kStep / kFilterGroup) + j]);
       uint64_t live = __ballot(t >= bound);
       while (live) {
-        Raw<BF> x[kLoads];
-        uint32_t at[kLoads];
+        Raw<BF> x[LOADS];
+        uint32_t at[LOADS];
         int have = 0;
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < LOADS; ++j) {
           if (!live) continue;
           at[j] = step(q0 + (uint32_t)__builtin_ctzll(live));
           x[j] = load8<BF>(row, (int64_t)at[j] * kStep + lane * kVec, V);
@@ -354,7 +354,7 @@ struct Choice {
           have = j + 1;
         }
 #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
+        for (int j = 0; j < LOADS; ++j) {
           if (j >= have) continue;
           if (open != at[j] >> shift) {
             if (open != 0xFFFFFFFFu) done(open);
@@ -370,7 +370,7 @@ struct Choice {
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
     const float least = value_of(bound);
-    steps(
+    steps<1>(
         [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
 #pragma unroll
           for (int e = 0; e < kVec; ++e)
@@ -570,6 +570,7 @@ struct Choice {
   // CUT: not all tokens have keys up to `last`.
   template <bool CUT>
   __device__ __forceinline__ uint64_t border_mass(uint64_t last, float share, uint64_t whole, float lowest) const {
+    constexpr int kLoads = CUT ? 1 : BF ? 4 : 2;
     const float per = bins_of(lowest), kf = (float)(kappa / kTable);
     const float least = value_of(bound);  // next to where min_p cuts, if it does
     auto within = [&](float x, int64_t i) __attribute__((always_inline)) {
@@ -583,14 +584,19 @@ struct Choice {
     for (uint64_t z = whole ? (whole >> scale) + 1 : (uint64_t)V; z > 1; z = (z + 1) / 2) --bits;
     const float fb = (float)bits;
     clear(s->mass, kBins / 2);
-    steps(
+    steps<kLoads>(
         [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
+          uint32_t w[kVec];
+          int at[kVec];
 #pragma unroll
           for (int e = 0; e < kVec; ++e) {
-            const float d = m - x[e], w = __builtin_amdgcn_exp2f(__builtin_fmaf(-d, kf, fb));
-            if (x[e] >= least && within(x[e], v + e))
-              atomicAdd(&bins[(int)fminf(d * per, (float)(kBins - 1))], (uint32_t)(w + 0.5f));
+            const float d = m - x[e];
+            w[e] = (uint32_t)(__builtin_amdgcn_exp2f(__builtin_fmaf(-d, kf, fb)) + 0.5f);
+            at[e] = (int)fminf(d * per, (float)(kBins - 1));
           }
+#pragma unroll
+          for (int e = 0; e < kVec; ++e)
+            if (x[e] >= least && within(x[e], v + e)) atomicAdd(&bins[at[e]], w[e]);
         },
         [](uint32_t) {});
     __syncthreads();
@@ -622,7 +628,7 @@ struct Choice {
     Part over;
     const float high = b0 > 0 ? m - (float)b0 / per : __builtin_inff();
     const float low = b1 + 1 < kBins ? fmaxf(m - (float)(b1 + 1) / per, least) : least;
-    steps(
+    steps<kLoads>(
         [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
           count(over, x, [&](int e) __attribute__((always_inline)) { return x[e] > high && within(x[e], v + e); });
           append(x, v, [&](int e) __attribute__((always_inline)) {
@@ -691,7 +697,7 @@ struct Choice {
     const float least = value_of(bound);
     Part q;
     clear(s->part, kParts);
-    steps(
+    steps<1>(
         [&](const Raw<BF>& x, int64_t v) __attribute__((always_inline)) {
           count(q, x, [&](int e) __attribute__((always_inline)) {
             return x[e] >= least && order_key(ordered_code(x[e]), (uint32_t)(v + e)) <= last;
