@@ -557,7 +557,7 @@ def quantize_blocks_fp4(x: torch.Tensor, *, out: torch.Tensor | None = None, sca
         scale_out = torch.empty(lead + (n,), dtype=torch.uint8, device=x.device)
     xc = x.contiguous()
     rows = math.prod(lead)
-    st = _call(x.device, _lib.load().dspark_markov_quantize_fp4, _ptr(xc), tag, rows, d, _ptr(out), _ptr(scale_out))
+    st = _call(x.device, _lib.load().dspark_markov_quantize_fp4, xc.data_ptr(), tag, rows, d, out.data_ptr(), scale_out.data_ptr())
     _lib.check(st, "quantize_blocks_fp4")
     return out, scale_out
 
@@ -579,7 +579,7 @@ def dequantize_blocks_fp4(codes: torch.Tensor, scales: torch.Tensor, size: int, 
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {lead + (size,)}")
     tag = _dtype_tag(out)
     c, s = _at(codes, 16), _at(scales, 4)
-    st = _call(codes.device, _lib.load().dspark_markov_dequantize_fp4, _ptr(c), _ptr(s), math.prod(lead), size, _ptr(out),
+    st = _call(codes.device, _lib.load().dspark_markov_dequantize_fp4, c.data_ptr(), s.data_ptr(), math.prod(lead), size, out.data_ptr(),
                tag)
     _lib.check(st, "dequantize_blocks_fp4")
     return out
@@ -622,8 +622,8 @@ def lm_head_logits_fp4(hidden_states: torch.Tensor, head_codes: torch.Tensor, he
         buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
-    st = _call(dev, _lib.load().dspark_markov_lm_head_fp4, _ptr(h), tag, d, _ptr(hc), _ptr(hs), rows, 1, V, _ptr(out),
-               out_tag, _ptr(buffer), nbytes)
+    st = _call(dev, _lib.load().dspark_markov_lm_head_fp4, h.data_ptr(), tag, d, hc.data_ptr(), hs.data_ptr(), rows, 1, V, out.data_ptr(),
+               out_tag, buffer.data_ptr(), nbytes)
     _lib.check(st, "lm_head_logits_fp4")
     return out
 
@@ -855,22 +855,26 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
     if tuple(uniforms.shape) != (B, M) or not uniforms.is_floating_point():
         raise ValueError(f"uniforms must be float {(B, M)}, got {uniforms.dtype} {tuple(uniforms.shape)}")
     dev = logits.device
-    lim, keep = _lib.TokenLimits(), []
+    keep, at, num = [], [], []
     for name, value, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int64),
                                     ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
         if isinstance(value, torch.Tensor):
             if value.shape != (B,):
                 raise ValueError(f"{name} must be a number or [{B}], got {tuple(value.shape)}")
-            if value.is_floating_point() != dtype.is_floating_point:
-                raise TypeError(f"{name} must be {dtype}, got {value.dtype}")
+            if value.dtype != dtype:
+                if value.is_floating_point() != dtype.is_floating_point:
+                    raise TypeError(f"{name} must be {dtype}, got {value.dtype}")
             if value.device != dev:
                 raise ValueError(f"{name} is on {value.device}, the logits on {dev}")
             if value.dtype != dtype or not value.is_contiguous():
                 value = value.to(dtype).contiguous()
             keep.append(value)
-            setattr(lim, name, value.data_ptr())
+            at.append(value.data_ptr())
+            num.append(off)
         else:
-            setattr(lim, "all_" + name, off if value is None else int(value) if name == "top_k" else float(value))
+            at.append(None)
+            num.append(off if value is None else int(value) if dtype == torch.int64 else float(value))
+    lim = _lib.TokenLimits(*at, num[1], num[0], num[2], num[3])
     _check_device(dev, workspace, uniforms=uniforms)
     tag = _dtype_tag(logits)
     tokens = torch.empty((B, M), dtype=torch.int64, device=dev)
@@ -881,8 +885,8 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
         buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
-    st = _call(dev, _lib.load().dspark_markov_sample_filtered, _ptr(x), tag, _ptr(u), lim, B, M, V, _ptr(tokens),
-               _ptr(probs), _ptr(buffer), nbytes)
+    st = _call(dev, _lib.load().dspark_markov_sample_filtered, x.data_ptr(), tag, u.data_ptr(), lim, B, M, V, tokens.data_ptr(),
+               probs.data_ptr(), buffer.data_ptr(), nbytes)
     _lib.check(st, "sample_block_filtered")
     return tokens, probs
 
@@ -921,8 +925,8 @@ def distill_block_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_
         buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
-    st = _call(dev, _lib.load().dspark_markov_distill_block, _ptr(x), tag, _ptr(ids), _ptr(t), ttag, B, M, V, K, T,
-               _ptr(loss), _ptr(stats), _ptr(buffer), nbytes)
+    st = _call(dev, _lib.load().dspark_markov_distill_block, x.data_ptr(), tag, ids.data_ptr(), t.data_ptr(), ttag, B, M, V, K, T,
+               loss.data_ptr(), stats.data_ptr(), buffer.data_ptr(), nbytes)
     _lib.check(st, "distill_block_loss")
     return loss, stats
 
@@ -951,7 +955,7 @@ def distill_block_loss_backward(grad_loss: torch.Tensor, logits: torch.Tensor, t
         out = torch.empty_like(x)
     elif out.shape != logits.shape or out.dtype != logits.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped and typed like logits")
-    st = _call(dev, _lib.load().dspark_markov_distill_block_backward, _ptr(g), _ptr(x), tag, _ptr(ids), _ptr(t), ttag,
-               _ptr(s), B, M, V, K, T, _ptr(out))
+    st = _call(dev, _lib.load().dspark_markov_distill_block_backward, g.data_ptr(), x.data_ptr(), tag, ids.data_ptr(), t.data_ptr(), ttag,
+               s.data_ptr(), B, M, V, K, T, out.data_ptr())
     _lib.check(st, "distill_block_loss_backward")
     return out
