@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kCap = 2048, kBins = 2048, kPer = kCap / kThreads;
+constexpr int kFew = 128;      // keys that a workgroup places without sorting
 constexpr int kParts = 1024, kPartBits = 11;  // parts of a row whose masses are kept, of at least 2^kPartBits columns
 static_assert(kBins == kCap && kParts <= kCap, "bins and masses share memory, and a scan's steps");
 constexpr int kVec = 8;
@@ -956,7 +957,78 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
     count = s.count;
   }
   uint64_t z;
-  if (count <= kCap) {
+  if (count <= kFew) {
+    // Few tokens, as a top_k leaves: every wave holds all of them, two a lane, and
+    // compares each with sixteen; the waves' counts and sums meet in LDS.  Four
+    // barriers in place of two sorts and five scans.
+    const int wave = tid >> 6;
+    uint64_t* const places = s.mass;
+    uint64_t* const befores = s.mass + kFew;
+    uint64_t* const uptos = s.mass + 2 * kFew;
+    uint64_t* const sums2 = s.mass + 3 * kFew;
+    uint64_t key[2], w[2], n1[2] = {0, 0}, n2[2] = {0, 0}, n3[2] = {0, 0}, all = 0;
+    if (tid < 3 * kFew + 2) s.mass[tid] = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      key[h] = lane + 64 * h < (int)count ? s.keys[lane + 64 * h] : ~0ull;
+      w[h] = lane + 64 * h < (int)count ? c.mass_of(key_code(key[h])) : 0;
+    }
+    auto of = [&](const uint64_t (&v)[2], int j) __attribute__((always_inline)) {  // token 16 wave + j's
+      const uint64_t x = wave < 4 ? v[0] : v[1];
+      const int l = 16 * (wave & 3) + j;
+      return ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(x >> 32), l) << 32) |
+             (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, l);
+    };
+    auto meet = [&](uint64_t* to, uint64_t x) __attribute__((always_inline)) {
+      atomicAdd((unsigned long long*)to, (unsigned long long)x);
+    };
+    __syncthreads();
+    for (int j = 0; j < kFew / kWaves; ++j) {
+      const uint64_t o = of(key, j);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) n1[h] += o < key[h] ? 1 : 0;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) meet(&places[lane + 64 * h], n1[h]);
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) w[h] = places[lane + 64 * h] < (uint64_t)lim.k ? w[h] : 0;
+    if (lim.nucleus) {
+      for (int j = 0; j < kFew / kWaves; ++j) {
+        const uint64_t o = of(key, j), x = of(w, j);
+        all += x;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) n2[h] += o < key[h] ? x : 0;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) meet(&befores[lane + 64 * h], n2[h]);
+      if (lane == 0) meet(&sums2[0], all);
+      __syncthreads();
+      const uint64_t target = Choice<BF>::part_up(whole ? whole : sums2[0], lim.top_p);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) w[h] = befores[lane + 64 * h] < target ? w[h] : 0;
+    }
+    all = 0;
+    for (int j = 0; j < kFew / kWaves; ++j) {
+      const uint64_t o = of(key, j), x = of(w, j);
+      all += x;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) n3[h] += (uint32_t)o <= (uint32_t)key[h] ? x : 0;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) meet(&uptos[lane + 64 * h], n3[h]);
+    if (lane == 0) meet(&sums2[1], all);
+    __syncthreads();
+    z = sums2[1];
+    const uint64_t target = Choice<BF>::part_down(z, u);
+    token = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint64_t upto = uptos[lane + 64 * h];
+      const uint64_t hit = __ballot(upto > target && upto - w[h] <= target);  // w is not zero then
+      if (hit) token = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key[h], __builtin_ctzll(hit));
+    }
+  } else if (count <= kCap) {
     sort_keys(s, (int)count);
     int kept = lim.k < (int64_t)count ? (int)lim.k : (int)count;
     for (int i = tid; i < kept; i += kThreads) s.mass[i] = c.mass_of(key_code(s.keys[i]));
