@@ -327,7 +327,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
 #pragma unroll
   for (int j = 0; j < PS; ++j) {
     const int i = scale_rows(j);
-    const bool x = i < BM / 32;
+    const bool x = NW * (j + 1) <= BM / 32 || (NW * j < BM / 32 && i < BM / 32);
     offs[j] = (32u * (uint32_t)(x ? i : i - BM / 32) + (uint32_t)(lane >> 1)) * (x ? lxs : lws) + 4u * (uint32_t)(lane & 1);
   }
   auto load = [&](int g, int q) __attribute__((always_inline)) {  // load q of chunk g of the stream
@@ -339,14 +339,14 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
       load_lds16_at(bb, offb[j < PB ? j : 0], k0, stage + BM * BK + 1024u * (uint32_t)(wave + NW * j));
     } else {
       const int j = q - PA - PB, i = scale_rows(j);
-      const bool x = i < BM / 32;
+      const bool x = NW * (j + 1) <= BM / 32 || (NW * j < BM / 32 && i < BM / 32);  // the compiler knows it for most j
       const uint32_t k = (uint32_t)lc * SB;
       load_lds4_at(x ? sa : sb, k + 4u * (uint32_t)(lane & 1) < (x ? lxs : lws) ? offs[j < PS ? j : 0] : kBufferOob, k,
                    stage + CODES + 256u * (uint32_t)i);
     }
   };
   auto next = [&]() __attribute__((always_inline)) {  // on to the stream's next chunk
-    if (++lc == C) {
+    if (lt < my && ++lc == C) {
       lc = 0;
       if (++lt < my) bind(lt);
       else ba = bb = sa = sb = buffer_words(p.xc, 0);  // the loads past the last chunk bring zeros
@@ -369,23 +369,26 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     uint32_t a[MI], b[NJ];
   };
   auto read = [&](int g, int s, Frags& f) __attribute__((always_inline)) {  // step s of chunk g
-    const unsigned char* const st = &lds[(g % STAGES) * STAGE + 16 * ((2 * s + (lane >> 5)) ^ (lane >> 1 & 7))];
+    const int piece = 16 * ((2 * s + (lane >> 5)) ^ (lane >> 1 & 7)) + (lane & 31) * BK;
+    const unsigned char* const x = &lds[(g % STAGES) * STAGE + piece];
+    const unsigned char* const h = x + BM * BK;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) f.a[i] = *(const i32x4_t*)(st + (32 * (MI * wm + i) + (lane & 31)) * BK);
+    for (int i = 0; i < MI; ++i) f.a[i] = *(const i32x4_t*)(x + 32 * (MI * wm + i) * BK);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) f.b[j] = *(const i32x4_t*)(st + (BM + 32 * (NJ * wn + j) + (lane & 31)) * BK);
+    for (int j = 0; j < NJ; ++j) f.b[j] = *(const i32x4_t*)(h + 32 * (NJ * wn + j) * BK);
   };
   const uint32_t pick = lane >> 5 ? 0x07050301u : 0x06040200u;
   auto read_scales = [&](int g, Scales& f) __attribute__((always_inline)) {
-    const unsigned char* const st = &lds[(g % STAGES) * STAGE + CODES];
+    const unsigned char* const x = &lds[(g % STAGES) * STAGE + CODES + (lane & 31) * SB];
+    const unsigned char* const h = x + BM * SB;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-      const uint64_t w = *(const uint64_t*)(st + (32 * (MI * wm + i) + (lane & 31)) * SB);
+      const uint64_t w = *(const uint64_t*)(x + 32 * (MI * wm + i) * SB);
       f.a[i] = __builtin_amdgcn_perm((uint32_t)(w >> 32), (uint32_t)w, pick);
     }
 #pragma unroll
     for (int j = 0; j < NJ; ++j) {
-      const uint64_t w = *(const uint64_t*)(st + (BM + 32 * (NJ * wn + j) + (lane & 31)) * SB);
+      const uint64_t w = *(const uint64_t*)(h + 32 * (NJ * wn + j) * SB);
       f.b[j] = __builtin_amdgcn_perm((uint32_t)(w >> 32), (uint32_t)w, pick);
     }
   };
@@ -555,8 +558,8 @@ hipError_t head_go(const Fp4HeadParams& p, bool obf, int groups, hipStream_t s) 
 // other).  The form with the shortest sum of rounds is taken.  At V = 129280, in
 // us: 1 row 70 (32x128), 68 (32x256); 64 rows 134, 117 (32 rows), 95 (64x128), 81
 // (64x256); 128 rows 137 (64x256), 99 (128x256), 104 (192x256); 320 rows 239
-// (128x256), 195 (192x256), 170 (320x128), 163 (320x192), 219 (256x256); 2560
-// rows 1378, 1100, 1210, 1171, 1110.  37 rows of 2056 at V = 32003: 13.5
+// (128x256), 195 (192x256), 170 (320x128), 163 (320x192), 200 (256x256); 2560
+// rows 1378, 1100, 1210, 1171, 1040.  37 rows of 2056 at V = 32003: 13.5
 // (32x128), 9.1 (64x128), 12.8 (64x256).
 namespace {
 struct Form {
@@ -564,7 +567,7 @@ struct Form {
   float round;
 };
 constexpr Form kForms[] = {{32, 128, 17.5f},  {64, 128, 24.0f},  {64, 256, 40.0f}, {128, 256, 45.0f},
-                           {192, 256, 46.0f}, {256, 256, 56.0f}, {320, 128, 42.0f}, {320, 192, 54.0f}};
+                           {192, 256, 46.0f}, {256, 256, 52.0f}, {320, 128, 42.0f}, {320, 192, 54.0f}};
 int pick_form(int64_t rows, int64_t V, int num_cus) {
   int best = 0;
   double least = 0.0;
