@@ -24,9 +24,9 @@ def _check(x, u, T, k, p, m, tokens, probs, what):
             args = (u[b, j].item(), T[b], k[b], p[b], m[b])
             want, prob, near = ref.row(X[b, j], *args)
             got = tokens[b, j].item()
-            # A border closer than this may fall to either side: weights good to
-            # 2^-45 of the largest, their sums in the reference and in the kernel
-            # to 2^-50 of what is summed
+            # A border closer than this (2^-39.8 of the sum) may fall to either
+            # side: each weight is good to 2^-42 of itself, a sum of them and its
+            # part by top_p or u with it, a sum's roundings to 2^-45
             if near > 1e-12:
                 assert got == want, f"{what} row {b},{j} {args}: {got}, want {want}"
                 if math.isnan(prob):
@@ -128,6 +128,30 @@ def test_many_ties(native, dtype):
     lim = tuple([np.float32(v).item() if isinstance(v, float) else v for v in part] for part in lim)
     tokens, probs = _call(x, u, *lim)
     _check(x, u, *lim, tokens, probs, "ties")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_numbers_of_candidates(native, dtype):
+    """As many kept tokens as the ways of placing them hold, and one more or
+    less; with top_p and min_p inside them, and -inf above the k-th."""
+    g = torch.Generator().manual_seed(21)
+    ks = [1, 2, 63, 64, 65, 127, 128, 129, 130, 500, 2047, 2048, 2049, 2050]
+    V = 33001
+    x = torch.randn(len(ks), 3, V, generator=g)
+    x[:, 1] = torch.round(4 * x[:, 1]) / 4                       # ties at every border
+    x[:, 2, torch.randperm(V, generator=g)[100:]] = -INF         # never more than 100
+    x = x.to(dtype)
+    u = torch.rand(len(ks), 3, generator=g)
+    ones, zeros = [1.0] * len(ks), [0.0] * len(ks)
+    for T, p, m in ((1.0, 1.0, 0.0), (0.5, 0.75, 0.0), (2.0, 1.0, 0.125), (1.0, 0.9375, 0.0625)):
+        lim = ([T] * len(ks), ks, [p] * len(ks), [m] * len(ks))
+        tokens, probs = _call(x, u, *lim)
+        _check(x, u, *lim, tokens, probs, f"candidates T {T} p {p} m {m}")
+    # the same number of tokens left by a mask of -inf, no limit on
+    for b, k in enumerate(ks):
+        x[b, 0, torch.randperm(V, generator=g)[k:]] = -INF
+    tokens, probs = _call(x, u, ones, [0] * len(ks), ones, zeros)
+    _check(x, u, ones, [0] * len(ks), ones, zeros, tokens, probs, "candidates masked")
 
 
 def test_masks_and_special_rows(native):
