@@ -781,8 +781,8 @@ struct Choice {
 // A workgroup a row, two a CU (at 1024 threads 256 x 8 rows took 873 us instead of
 // 740).  Nucleus rows of 151936 fp32 logits with tens of thousands of kept tokens
 // take two more passes over themselves: 2048 of them 500 us, 2.37 GB at 4.7 TB/s;
-// a row alone 62 us, all barriers and loads that wait for each other.  With at
-// most 128 candidates a row takes 12 us, with a sorted list 20.
+// a row alone 69 us (62 at 1024 threads), all barriers and loads that wait for
+// each other.  With at most 128 candidates a row takes 12 us.
 template <bool BF>
 __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams p, int64_t r0) {
   __shared__ Shared s;
