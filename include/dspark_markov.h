@@ -349,7 +349,8 @@ dspark_status_t dspark_markov_dequantize_fp4(const uint8_t* codes, const uint8_t
  *   logits         device, [B, M, V] output, logits_dtype; must not overlap
  *                  an input.
  * B*M*V == 0 is a successful no-op.  The workspace must hold
- * dspark_markov_lm_head_fp4_workspace_bytes(...) bytes (no zero fill needed). */
+ * dspark_markov_lm_head_fp4_workspace_bytes(...) bytes (no zero fill needed),
+ * 16-byte aligned, apart from inputs and outputs. */
 size_t dspark_markov_lm_head_fp4_workspace_bytes(int64_t B, int64_t M, int64_t d);
 
 dspark_status_t dspark_markov_lm_head_fp4(const void* hidden_states, dspark_dtype_t hidden_dtype, int64_t d,
@@ -490,7 +491,7 @@ typedef struct dspark_token_limits {
  * Outputs must not overlap an input or each other.  V from 1 to 2^30.  A row's
  * result does not depend on the others.  B*M == 0 is a successful no-op.  The
  * workspace must hold dspark_markov_sample_filtered_workspace_bytes(...) bytes
- * (no zero fill needed). */
+ * (no zero fill needed), 16-byte aligned, apart from inputs and outputs. */
 size_t dspark_markov_sample_filtered_workspace_bytes(int64_t B, int64_t M, int64_t V);
 
 dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t logits_dtype, const float* uniforms,
@@ -515,7 +516,8 @@ dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t
  *   loss           device, [B, M] fp32 output.
  *   stats          device, [B, M, 4] fp32 output for the backward pass.
  * V from 1 to 2^30.  B*M == 0 is a successful no-op.  The workspace must hold
- * dspark_markov_distill_workspace_bytes(...) bytes (no zero fill needed). */
+ * dspark_markov_distill_workspace_bytes(...) bytes (no zero fill needed),
+ * 16-byte aligned, apart from inputs and outputs. */
 size_t dspark_markov_distill_workspace_bytes(int64_t B, int64_t M, int64_t V);
 
 dspark_status_t dspark_markov_distill_block(const void* logits, dspark_dtype_t logits_dtype, const int64_t* teacher_ids,

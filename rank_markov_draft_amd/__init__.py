@@ -43,6 +43,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+from operator import index
 
 import torch
 
@@ -855,15 +856,15 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
     by index, at which the kept tokens' running weight exceeds u of their sum,
     its probability its share of it.  Each limit is a number for all requests
     or a tensor [B]; None (and a top_k of 0, a top_p of 1, a min_p of 0) is off.
-    A temperature below 1e-5 takes the first of the largest logits (so does a
-    row whose largest is +inf or NaN).  A row with nothing above -inf gets token
+    A temperature below 1e-5, or None, takes the first of the largest logits (so
+    does a row whose largest is +inf or NaN).  A row with nothing above -inf gets token
     -1 and probability 0.  Weights and their sums are held in 64 bits."""
     B, M, V = _block(logits, None, "logits")
     if tuple(uniforms.shape) != (B, M) or not uniforms.is_floating_point():
         raise ValueError(f"uniforms must be float {(B, M)}, got {uniforms.dtype} {tuple(uniforms.shape)}")
     dev = logits.device
     keep, at, num = [], [], []
-    for name, value, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int64),
+    for name, value, off, dtype in (("temperature", temperature, 0.0, torch.float32), ("top_k", top_k, 0, torch.int64),
                                     ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
         if isinstance(value, torch.Tensor):
             if value.shape != (B,):
@@ -880,7 +881,10 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
             num.append(off)
         else:
             at.append(None)
-            num.append(off if value is None else int(value) if dtype == torch.int64 else float(value))
+            value = off if value is None else index(value) if dtype == torch.int64 else float(value)
+            if name == "top_k" and not -2 ** 63 <= value < 2 ** 63:
+                raise ValueError(f"top_k must fit 64 bits, got {value}")
+            num.append(value)
     lim = _lib.TokenLimits(*at, num[1], num[0], num[2], num[3])
     _check_device(dev, workspace, uniforms=uniforms)
     tag = _dtype_tag(logits)

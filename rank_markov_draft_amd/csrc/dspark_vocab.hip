@@ -35,6 +35,12 @@ dspark_status_t check_fp4(dspark_dtype_t dtype, int64_t rows, int64_t d, int64_t
 }
 bool fp4_aligned(const void* codes, const void* scales) { return aligned16(codes) && ((uintptr_t)scales & 3u) == 0; }
 
+// Whether a call's scratch, the workspace from kDataOffset to its `need` bytes,
+// can be used: aligned, and apart from what the call reads (and writes).
+bool scratch_ok(const void* workspace, size_t need, const Ranges& others) {
+  return aligned16(workspace) && !others.meet((const char*)workspace + kDataOffset, need - kDataOffset);
+}
+
 // What both passes of the distillation loss check; nothing to do: *empty.
 dspark_status_t check_distill(const void* logits, dspark_dtype_t dtype, const int64_t* ids, const void* teacher,
                               dspark_dtype_t teacher_dtype, int64_t B, int64_t M, int64_t V, int64_t K, double tau,
@@ -126,14 +132,16 @@ dspark_status_t dspark_markov_lm_head_fp4(const void* hidden_states, dspark_dtyp
   if (elems == 0) return DSPARK_OK;
   if (!hidden_states || !head_codes || !head_scales || !logits || !fp4_aligned(head_codes, head_scales))
     return DSPARK_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < dspark_markov_lm_head_fp4_workspace_bytes(B, M, d))
-    return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = dspark_markov_lm_head_fp4_workspace_bytes(B, M, d);
+  if (!workspace || workspace_bytes < need) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
   const int64_t blocks = dspark::fp4_blocks(d);
   Ranges in;
   in.add(hidden_states, (size_t)(rows * d) * dtype_bytes(hidden_dtype));
   in.add(head_codes, (size_t)(V * blocks * 16));
   in.add(head_scales, (size_t)(V * blocks));
   if (in.meet(logits, (size_t)elems * dtype_bytes(logits_dtype))) return DSPARK_ERR_INVALID_ARGUMENT;
+  in.add(logits, (size_t)elems * dtype_bytes(logits_dtype));
+  if (!scratch_ok(workspace, need, in)) return DSPARK_ERR_INVALID_ARGUMENT;
   const hipStream_t s = (hipStream_t)stream;
   uint8_t* const xc = (uint8_t*)workspace + kDataOffset;
   uint8_t* const xs = xc + fp4_codes_bytes(rows, d);
@@ -169,8 +177,8 @@ dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t
   if (V > ((int64_t)1 << 30)) return DSPARK_ERR_UNSUPPORTED;
   if (rows == 0) return DSPARK_OK;
   if (V == 0 || !logits || !uniforms || !tokens || !probs) return DSPARK_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < dspark_markov_sample_filtered_workspace_bytes(B, M, V))
-    return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = dspark_markov_sample_filtered_workspace_bytes(B, M, V);
+  if (!workspace || workspace_bytes < need) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
   const size_t tb = (size_t)rows * sizeof(int64_t), pb = (size_t)rows * sizeof(float), vb = (size_t)B * sizeof(float);
   Ranges in;
   in.add(logits, (size_t)elems * dtype_bytes(logits_dtype));
@@ -180,6 +188,9 @@ dspark_status_t dspark_markov_sample_filtered(const void* logits, dspark_dtype_t
   in.add(limits->top_p, vb);
   in.add(limits->min_p, vb);
   if (in.meet(tokens, tb) || in.meet(probs, pb) || overlaps(tokens, tb, probs, pb)) return DSPARK_ERR_INVALID_ARGUMENT;
+  in.add(tokens, tb);
+  in.add(probs, pb);
+  if (!scratch_ok(workspace, need, in)) return DSPARK_ERR_INVALID_ARGUMENT;
   dspark::FilterParams p{};
   p.limits = dspark::TokenLimits{limits->temperature,   limits->top_k,           limits->top_p,     limits->min_p,
                                  limits->all_top_k,     limits->all_temperature, limits->all_top_p, limits->all_min_p};
@@ -219,10 +230,14 @@ dspark_status_t dspark_markov_distill_block(const void* logits, dspark_dtype_t l
                                            temperature, &p, &in, &lbytes, &empty);
   if (st != DSPARK_OK || empty) return st;
   if (!loss || !stats) return DSPARK_ERR_INVALID_ARGUMENT;
-  if (!workspace || workspace_bytes < dspark_markov_distill_workspace_bytes(B, M, V)) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = dspark_markov_distill_workspace_bytes(B, M, V);
+  if (!workspace || workspace_bytes < need) return DSPARK_ERR_WORKSPACE_TOO_SMALL;
   const size_t rb = (size_t)p.rows * sizeof(float);
   in.add(logits, lbytes);
   if (in.meet(loss, rb) || in.meet(stats, 4 * rb) || overlaps(loss, rb, stats, 4 * rb)) return DSPARK_ERR_INVALID_ARGUMENT;
+  in.add(loss, rb);
+  in.add(stats, 4 * rb);
+  if (!scratch_ok(workspace, need, in)) return DSPARK_ERR_INVALID_ARGUMENT;
   p.loss = loss;
   p.stats = stats;
   p.partials = (float*)((char*)workspace + kDataOffset);

@@ -221,6 +221,9 @@ def test_numbers_for_all_requests_views_workspace(native):
              for b in range(B) for j in range(M)]
     assert torch.equal(torch.cat([t for t, _ in parts]).view(B, M), want[0])
     assert rmd.sample_block_filtered(x[:0], u[:0], 0.7)[0].shape == (0, M)
+    # no temperature, as elsewhere: the largest logit
+    got = rmd.sample_block_filtered(x, u, None, top_k=torch.tensor([3] * B).cuda())
+    assert torch.equal(got[0], x.argmax(-1)) and bool((got[1] == 1).all())
 
 
 def test_streams_and_graph(native):

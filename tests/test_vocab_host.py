@@ -62,7 +62,8 @@ def test_head_workspace_and_refusals(L):
     for kw in (dict(hdt=9), dict(odt=2), dict(d=0), dict(d=-3), dict(B=-1), dict(M=-1), dict(V=-1), dict(hid=None),
                dict(c=None), dict(s=None), dict(out=None), dict(B=2 ** 40, M=2 ** 40), dict(V=2 ** 58, B=1, M=1),
                dict(out=at(A[0], 8)), dict(out=at(A[1], 100)), dict(out=at(A[2], 4)), dict(c=at(A[1], 8)),
-               dict(s=at(A[2], 2))):
+               dict(s=at(A[2], 2)), dict(ws=at(A[4], 8)), dict(ws=at(A[0], -data)), dict(ws=at(A[3], -data)),
+               dict(ws=at(A[1], 16 - data))):
         assert h(**kw) == INVALID, kw
     assert h(d=2 ** 20 + 1) == UNSUPPORTED and b"1048576" in L.dspark_markov_last_error()
     assert h(V=2 ** 31, B=1, M=1) == UNSUPPORTED
@@ -90,7 +91,8 @@ def test_sample_workspace_and_refusals(L):
                dict(t=None), dict(p=None), dict(B=2 ** 40, M=2 ** 40), dict(B=2 ** 60, V=1, M=1), dict(t=at(A[0], 8)),
                dict(p=at(A[0], 8)), dict(t=at(A[1], 8)), dict(p=at(A[1], 20)), dict(p=at(A[2], 40)),
                dict(l=lim(temperature=A[2])), dict(l=lim(top_k=A[3])), dict(l=lim(top_p=at(A[2], 44))),
-               dict(l=lim(min_p=A[3]))):
+               dict(l=lim(min_p=A[3])), dict(ws=at(A[4], 8)), dict(ws=at(A[0], -data)), dict(ws=at(A[2], -data)),
+               dict(ws=at(A[3], 16 - data))):
         assert f(**kw) == INVALID, kw
     assert f(V=2 ** 30 + 1) == UNSUPPORTED
     assert f(ws=None) == SMALL and f(n=data) == SMALL
@@ -117,7 +119,8 @@ def test_distill_workspace_and_refusals(L):
            dict(t=None), dict(T=0.0), dict(T=-1.0), dict(T=float("nan")), dict(T=float("inf")), dict(T=1e-40), dict(T=1e40),
            dict(B=2 ** 40, M=2 ** 40), dict(B=2 ** 40, M=2 ** 20, V=8)]
     for kw in bad + [dict(loss=None), dict(st=None), dict(loss=at(A[0], 4)), dict(loss=at(A[1], 8)), dict(st=at(A[2], 4)),
-                     dict(st=at(A[0], 4)), dict(st=at(A[3], 16))]:
+                     dict(st=at(A[0], 4)), dict(st=at(A[3], 16)), dict(ws=at(A[5], 8)), dict(ws=at(A[0], -data)),
+                     dict(ws=at(A[3], -data)), dict(ws=at(A[4], 16 - data))]:
         assert f(**kw) == INVALID, kw
     assert f(V=2 ** 30 + 1) == UNSUPPORTED and f(K=1025) == UNSUPPORTED
     assert f(ws=None) == SMALL and f(n=data) == SMALL
@@ -166,6 +169,7 @@ def test_binding_refuses_shapes_and_types():
             (lambda: rmd.sample_block_filtered(x, _cpu(2, 3, dtype=i64)), "uniforms must be"),
             (lambda: rmd.sample_block_filtered(x, _cpu(2, 3), _cpu(3)), r"temperature must be a number or \[2\]"),
             (lambda: rmd.sample_block_filtered(x, _cpu(2, 3), top_p=_cpu(2, 3)), r"top_p must be a number or \[2\]"),
+            (lambda: rmd.sample_block_filtered(x, _cpu(2, 3), top_k=2 ** 64 + 5), "64 bits"),
             (lambda: rmd.distill_block_loss(x, ids[:1], t), "teacher_ids must be"),
             (lambda: rmd.distill_block_loss(x, t, t), "teacher_ids must be"),
             (lambda: rmd.distill_block_loss(x, ids, t[..., :3]), "teacher_logits must be"),
@@ -176,6 +180,7 @@ def test_binding_refuses_shapes_and_types():
             call()
     for call in (lambda: rmd.sample_block_filtered(x, _cpu(2, 3), top_k=_cpu(2)),
                  lambda: rmd.sample_block_filtered(x, _cpu(2, 3), _cpu(2, dtype=i64)),
-                 lambda: rmd.sample_block_filtered(x, _cpu(2, 3), min_p=_cpu(2, dtype=i64))):
+                 lambda: rmd.sample_block_filtered(x, _cpu(2, 3), min_p=_cpu(2, dtype=i64)),
+                 lambda: rmd.sample_block_filtered(x, _cpu(2, 3), top_k=3.5)):
         with pytest.raises(TypeError):
             call()
