@@ -283,6 +283,8 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
   static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "whole load instructions per wave");
   static_assert((STAGES - 1) * PER < 64, "wait count");
   // a wave's part of the output on its way to memory: ER rows x 32 NJ columns
+  constexpr int STORES = MI * NJ * (OBF ? 2 : 4);  // instructions for a wave's part of a whole tile
+  static_assert(!AHEAD || STAGES == 2, "the hand-over waits for all loads");
   constexpr int OS = OBF ? 2 : 4, ER = OBF ? 16 : 8, EROW = 32 * NJ * OS, EBYTES = ER * EROW;
   __shared__ __attribute__((aligned(16))) unsigned char lds[STAGES * STAGE + NW * EBYTES];
 
@@ -425,6 +427,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     read_scales(0, sc);
   }
   int g = 0, landed = 0;  // landed: steps whose chunk is known to have arrived
+  bool stored = false;    // the wave's part of the last tile was whole
   for (int t = 0; t < my; ++t) {
     const int tile = first + t * G;
     const int64_t r0 = (int64_t)(tile % row_tiles) * BM + 32 * MI * wm;
@@ -446,7 +449,10 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
         // The chunk's last products run behind the hand-over to the next: its
         // loads have landed for every wave, every wave has read all of this
         // chunk, whose stage takes the loads of chunk g + STAGES.
-        wait_vmcnt<(STAGES - 2) * PER>();
+        // (Loads and stores are counted in the order of their issue: those
+        // loads are older than the last tile's stores, which may go on.)
+        if (c == 0 && stored) wait_vmcnt<STORES < 63 ? STORES : 63>();
+        else wait_vmcnt<0>();
         lds_barrier();
         read(g + 1, 0, f[0]);  // before the loads, which would hold up LDS
         read_scales(g + 1, sn);
@@ -489,6 +495,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
     // wave write to different banks, and leave in whole pieces of consecutive
     // columns.
     unsigned char* const mine = &lds[STAGES * STAGE + wave * EBYTES];
+    stored = r0 + 32 * MI <= p.rows && v0 + 32 * NJ <= p.V;  // no lane of the stores below is left out
     constexpr int PIECES = EROW / 16, HALF = PIECES / 2;  // of a row
     constexpr int SETS = ER / 8;                          // groups of 8 rows in an exchange
     auto turned = [](int q, int half) __attribute__((always_inline)) {
@@ -501,34 +508,43 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
       for (int x = 0; x < 4 / SETS; ++x) {
         const int64_t rb = r0 + 32 * i + ER * x;  // first row of the exchange
         if (rb >= p.rows) continue;
+        // Lanes' addresses are computed anew each time: kept over the products
+        // they go to scratch, and each reload waits for all stores before it.
+        int l = lane;
+        __asm__ volatile("" : "+v"(l));
+        if constexpr (AHEAD) {
+          // nor are sums that a later exchange takes read yet
+#pragma unroll
+          for (int k = i; k < MI; ++k)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) __asm__ volatile("" : "+a"(acc[k][j]));
+        }
 #pragma unroll
         for (int u = 0; u < SETS; ++u) {
-          const int lr = 8 * u + 4 * (lane >> 5);  // first of the lane's four rows
+          const int lr = 8 * u + 4 * (l >> 5);  // first of the lane's four rows
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
               const float y = acc[i][j][4 * (SETS * x + u) + e];
-              const int byte = (32 * j + (lane & 31)) * OS;
-              unsigned char* const at = mine + (lr + e) * EROW + 16 * turned(byte >> 4, lane >> 5) + (byte & 15);
+              const int byte = (32 * j + (l & 31)) * OS;
+              unsigned char* const at = mine + (lr + e) * EROW + 16 * turned(byte >> 4, l >> 5) + (byte & 15);
               if constexpr (OBF) *(uint16_t*)at = (uint16_t)(pack_bf16x2(y, 0.0f) & 0xFFFFu);
               else *(float*)at = y;
             }
         }
 #pragma unroll
         for (int h = 0; h < ER * PIECES / 64; ++h) {
-          const int pc = lane + 64 * h, lr = pc / PIECES, q = pc % PIECES;
+          const int pc = l + 64 * h, lr = pc / PIECES, q = pc % PIECES;
           const u32x4_t w = *(const u32x4_t*)(mine + lr * EROW + 16 * turned(q, lr >> 2 & 1));
           const int64_t n = rb + lr, v = v0 + q * (16 / OS);
-          if (n < p.rows && v < p.V) {
-            unsigned char* const dst = (unsigned char*)p.out + (n * p.V + v) * OS;
-            if (v + 16 / OS <= p.V) {
-              __builtin_nontemporal_store(w, (u32x4_any_t*)dst);
-            } else {
-              for (int e = 0; e < (int)(p.V - v); ++e) {
-                if constexpr (OBF) ((uint16_t*)dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-                else ((uint32_t*)dst)[e] = w[e];
-              }
+          unsigned char* const dst = (unsigned char*)p.out + (rb * p.V + v0) * OS + ((int64_t)lr * p.V + q * (16 / OS)) * OS;
+          if (stored || (n < p.rows && v + 16 / OS <= p.V)) {
+            __builtin_nontemporal_store(w, (u32x4_any_t*)dst);
+          } else if (n < p.rows && v < p.V) {
+            for (int e = 0; e < (int)(p.V - v); ++e) {
+              if constexpr (OBF) ((uint16_t*)dst)[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+              else ((uint32_t*)dst)[e] = w[e];
             }
           }
         }
@@ -554,28 +570,30 @@ hipError_t head_go(const Fp4HeadParams& p, bool obf, int groups, hipStream_t s) 
 }
 }  // namespace
 
-// The forms of the kernel, and what a round of their tiles over the CUs takes
-// (us at d = 5120, the one hidden size at which they were timed against each
-// other).  The form with the shortest sum of rounds is taken.  At V = 129280, in
-// us: 1 row 70 (32x128), 68 (32x256); 64 rows 134, 117 (32 rows), 95 (64x128), 81
-// (64x256); 128 rows 137 (64x256), 99 (128x256), 104 (192x256); 320 rows 239
-// (128x256), 195 (192x256), 170 (320x128), 163 (320x192), 200 (256x256); 2560
-// rows 1378, 1100, 1210, 1171, 1040.  37 rows of 2056 at V = 32003: 13.5
-// (32x128), 9.1 (64x128), 12.8 (64x256).
+// The forms of the kernel, and what their tiles over the CUs take: the first
+// round of them and every further one (us at d = 5120, the one hidden size at
+// which they were timed against each other).  The form with the shortest sum is
+// taken.  Kernel times at V = 129280, in us, bf16 logits from 128 rows on: 1 row
+// 70 (32x128), 68 (32x256); 64 rows 117 (32x128), 95 (64x128), 81 (64x256), 102
+// (128x256); 128 rows 137 (64x256), 99 (128x256), 107 (192x256), 102 (256x256); 256
+// rows 162 (128x256), 118 (256x256), 146 (320x192); 320 rows 218 (128x256), 184
+// (192x256), 188 (256x256), 167 (320x128), 155 (320x192); 640 rows 347, 321, 288,
+// 303, 278; 2560 rows 1366, 1094, 956, 1206, 1008.  37 rows of 2056 at V = 32003:
+// 13.5 (32x128), 9.1 (64x128), 12.8 (64x256).
 namespace {
 struct Form {
   int bm, bn;
-  float round;
+  float first, more;
 };
-constexpr Form kForms[] = {{32, 128, 17.5f},  {64, 128, 24.0f},  {64, 256, 40.0f}, {128, 256, 45.0f},
-                           {192, 256, 46.0f}, {256, 256, 52.0f}, {320, 128, 42.0f}, {320, 192, 54.0f}};
+constexpr Form kForms[] = {{32, 128, 17.5f, 17.5f}, {64, 128, 24.0f, 24.0f},  {64, 256, 40.0f, 40.0f},  {128, 256, 68.0f, 34.0f},
+                           {192, 256, 70.0f, 40.0f}, {256, 256, 62.0f, 49.0f}, {320, 128, 57.0f, 38.0f}, {320, 192, 70.0f, 46.0f}};
 int pick_form(int64_t rows, int64_t V, int num_cus) {
   int best = 0;
   double least = 0.0;
   for (int i = 0; i < (int)(sizeof(kForms) / sizeof(kForms[0])); ++i) {
     const Form& f = kForms[i];
     const int64_t tiles = ((rows + f.bm - 1) / f.bm) * ((V + f.bn - 1) / f.bn);
-    const double cost = (double)((tiles + num_cus - 1) / num_cus) * f.round;
+    const double cost = f.first + (double)((tiles + num_cus - 1) / num_cus - 1) * f.more;
     if (i == 0 || cost < least) {
       best = i;
       least = cost;
