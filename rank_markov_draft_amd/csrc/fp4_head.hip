@@ -265,10 +265,11 @@ __device__ __forceinline__ void load_lds4_at(const BufferWords& r, uint32_t off,
 // a row's blocks are read as zeros (2^-127), so that what of the head's next
 // row stands in a last chunk counts nothing, NaN scales included.
 //
-// AHEAD (tiles bound by the matrix cores): the fragments of a product are
-// read while the product before it runs, and the hand-over from chunk to
-// chunk (wait, barrier, first reads, the next loads one by one between
-// products) runs behind the chunk's last products.  The sums are pinned after
+// AHEAD (tiles bound by the matrix cores): fragments are read while earlier
+// products run, and the hand-over from chunk to chunk (its loads one by one
+// between products, then wait, barrier and first reads) runs behind the chunk's
+// last two steps; with all of it behind the last one, 2560 rows took 968 us
+// instead of 940.  The sums are pinned after
 // each step, or the compiler would move all of a chunk's products past the wait
 // for the next one's loads (at 2560 rows 9% of the time).
 // Otherwise (tiles bound by the head's stream) all of a chunk's fragments are
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
   static_assert((STAGES - 1) * PER < 64, "wait count");
   // a wave's part of the output on its way to memory: ER rows x 32 NJ columns
   constexpr int STORES = MI * NJ * (OBF ? 2 : 4);  // instructions for a wave's part of a whole tile
-  static_assert(!AHEAD || STAGES == 2, "the hand-over waits for all loads");
+  static_assert(!AHEAD || (STAGES == 2 && PER < 63), "the hand-over's wait counts");
   constexpr int OS = OBF ? 2 : 4, ER = OBF ? 16 : 8, EROW = 32 * NJ * OS, EBYTES = ER * EROW;
   __shared__ __attribute__((aligned(16))) unsigned char lds[STAGES * STAGE + NW * EBYTES];
 
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
   bind(0);
 #pragma unroll
   for (int g = 0; g < STAGES - (AHEAD ? 0 : 1); ++g) issue(g);
-  Frags f[AHEAD ? 2 : S];
+  Frags f[AHEAD ? 3 : S];
   Scales sc, sn;
   if constexpr (AHEAD) {
     wait_vmcnt<(STAGES - 1) * PER>();
@@ -440,31 +441,36 @@ __global__ __launch_bounds__(64 * WM * WN) void fp4_head_kernel(Fp4HeadParams p,
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     for (int c = 0; c < C; ++c, ++g) {
       if constexpr (AHEAD) {
+        // Fragments are read up to two steps ahead.  When step 3's have come to
+        // every wave, the chunk's stage takes the loads of chunk g + STAGES, one
+        // by one between step 2's products; the next chunk's have landed for
+        // every wave before step 3, behind whose products its first fragments
+        // and scales are read.
         read(g, 1, f[1]);
+        read(g, 2, f[2]);
         multiply(s0, f[0], sc);
-        read(g, 2, f[0]);
+        read(g, 3, f[0]);
         multiply(s1, f[1], sc);
-        read(g, 3, f[1]);
-        multiply(s2, f[0], sc);
-        // The chunk's last products run behind the hand-over to the next: its
-        // loads have landed for every wave, every wave has read all of this
-        // chunk, whose stage takes the loads of chunk g + STAGES.
-        // (Loads and stores are counted in the order of their issue: those
-        // loads are older than the last tile's stores, which may go on.)
-        if (c == 0 && stored) wait_vmcnt<STORES < 63 ? STORES : 63>();
-        else wait_vmcnt<0>();
         lds_barrier();
-        read(g + 1, 0, f[0]);  // before the loads, which would hold up LDS
-        read_scales(g + 1, sn);
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int q = 0; q < MI * NJ; ++q) {
-          product(s3, q, f[1], sc);
+          product(s2, q, f[2], sc);
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int l = q * PER / (MI * NJ); l < (q + 1) * PER / (MI * NJ); ++l) load(g + STAGES, l);
           __builtin_amdgcn_sched_barrier(0);
         }
+        // (Loads and stores are counted in the order of their issue: the next
+        // chunk's are older than these, and than the last tile's stores, which
+        // may go on.)
+        if (c == 0 && stored) wait_vmcnt<(STORES + PER < 63 ? STORES + PER : 63)>();
+        else wait_vmcnt<PER>();
+        lds_barrier();
+        read(g + 1, 0, f[1]);
+        read_scales(g + 1, sn);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(s3, f[0], sc);
+        f[0] = f[1];
         next();
         sc = sn;
       } else {
