@@ -581,18 +581,18 @@ hipError_t head_go(const Fp4HeadParams& p, bool obf, int groups, hipStream_t s) 
 // which they were timed against each other).  The form with the shortest sum is
 // taken.  Kernel times at V = 129280, in us, bf16 logits from 128 rows on: 1 row
 // 70 (32x128), 68 (32x256); 64 rows 117 (32x128), 95 (64x128), 81 (64x256), 102
-// (128x256); 128 rows 137 (64x256), 99 (128x256), 107 (192x256), 102 (256x256); 256
-// rows 162 (128x256), 118 (256x256), 146 (320x192); 320 rows 218 (128x256), 184
-// (192x256), 188 (256x256), 167 (320x128), 155 (320x192); 640 rows 347, 321, 288,
-// 303, 278; 2560 rows 1366, 1094, 956, 1206, 1008.  37 rows of 2056 at V = 32003:
+// (128x256); 128 rows 137 (64x256), 90 (128x256), 105 (192x256), 101 (256x256); 256
+// rows 152 (128x256), 109 (256x256), 134 (320x192); 320 rows 197 (128x256), 171
+// (192x256), 175 (256x256), 152 (320x128), 142 (320x192); 640 rows 326, 309, 273,
+// 281, 257; 2560 rows 1239, 1053, 934, 1103, 962.  37 rows of 2056 at V = 32003:
 // 13.5 (32x128), 9.1 (64x128), 12.8 (64x256).
 namespace {
 struct Form {
   int bm, bn;
   float first, more;
 };
-constexpr Form kForms[] = {{32, 128, 17.5f, 17.5f}, {64, 128, 24.0f, 24.0f},  {64, 256, 40.0f, 40.0f},  {128, 256, 68.0f, 34.0f},
-                           {192, 256, 70.0f, 40.0f}, {256, 256, 62.0f, 49.0f}, {320, 128, 57.0f, 38.0f}, {320, 192, 70.0f, 46.0f}};
+constexpr Form kForms[] = {{32, 128, 17.5f, 17.5f}, {64, 128, 24.0f, 24.0f},  {64, 256, 40.0f, 40.0f},  {128, 256, 62.0f, 31.0f},
+                           {192, 256, 69.0f, 37.0f}, {256, 256, 56.0f, 46.5f}, {320, 128, 42.0f, 35.0f}, {320, 192, 52.0f, 44.0f}};
 int pick_form(int64_t rows, int64_t V, int num_cus) {
   int best = 0;
   double least = 0.0;

@@ -25,12 +25,12 @@ def _gen(seed):
 
 
 # ------------------------------------------------------------ 4-bit head
-# on 256 CUs: tiles of 32 x 128, 64 x 128, 64 x 256, 128 x 256, 192 x 256, twice 256
-# x 256, 320 x 128 and 320 x 192; d ends in half a chunk, a third of its last
+# on 256 CUs: tiles of 32 x 128, 64 x 128, 64 x 256, 128 x 256, twice 320 x 192, 256
+# x 256, 320 x 128, again 320 x 192, and 192 x 256; d ends in half a chunk, a third of its last
 # group of blocks filled
 @pytest.mark.parametrize("odt", [F32, BF16])
 @pytest.mark.parametrize("rows,V", [(1, 70001), (40, 70001), (40, 129280), (70, 70001), (130, 70001), (200, 70001), (700, 70001),
-                                    (650, 6983), (300, 129280)])
+                                    (650, 6983), (300, 129280), (330, 129280)])
 def test_head_tiles(native, rows, V, odt):
     d = 556
     x = torch.randn(rows, d, **_gen(rows))
