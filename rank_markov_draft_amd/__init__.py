@@ -560,9 +560,9 @@ def quantize_blocks_fp4(x: torch.Tensor, *, out: torch.Tensor | None = None, sca
                               or t.data_ptr() % align):
             raise ValueError(f"{name} must be a contiguous uint8 tensor of shape {shape}, {align}-byte aligned")
     if out is None:
-        out = torch.empty(lead + (16 * n,), dtype=torch.uint8, device=x.device)
+        out = x.new_empty(lead + (16 * n,), dtype=torch.uint8)
     if scale_out is None:
-        scale_out = torch.empty(lead + (n,), dtype=torch.uint8, device=x.device)
+        scale_out = x.new_empty(lead + (n,), dtype=torch.uint8)
     xc = x.contiguous()
     rows = math.prod(lead)
     st = _call(x.device, _lib.load().dspark_markov_quantize_fp4, xc.data_ptr(), tag, rows, d, out.data_ptr(), scale_out.data_ptr())
@@ -582,7 +582,7 @@ def dequantize_blocks_fp4(codes: torch.Tensor, scales: torch.Tensor, size: int, 
         raise ValueError(f"scales must be uint8 {lead + (n,)}, got {scales.dtype} {tuple(scales.shape)}")
     _check_device(codes.device, None, scales=scales, out=out)
     if out is None:
-        out = torch.empty(lead + (size,), dtype=dtype, device=codes.device)
+        out = codes.new_empty(lead + (size,), dtype=dtype)
     elif tuple(out.shape) != lead + (size,) or out.dtype != dtype or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {dtype} tensor of shape {lead + (size,)}")
     tag = _dtype_tag(out)
@@ -617,7 +617,7 @@ def lm_head_logits_fp4(hidden_states: torch.Tensor, head_codes: torch.Tensor, he
     if out_dtype is None:
         out_dtype = torch.float32 if out is None else out.dtype
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
+        out = hidden_states.new_empty(shape, dtype=out_dtype)
     elif tuple(out.shape) != shape or out.dtype != out_dtype or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {out_dtype} tensor of shape {shape}")
     out_tag = _dtype_tag(out)
@@ -627,7 +627,7 @@ def lm_head_logits_fp4(hidden_states: torch.Tensor, head_codes: torch.Tensor, he
     h, hc, hs = hidden_states.contiguous(), _at(head_codes, 16), _at(head_scales, 4)
     if workspace is None:
         nbytes = int(_lib.load().dspark_markov_lm_head_fp4_workspace_bytes(rows, 1, d))
-        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+        buffer = hidden_states.new_empty(nbytes, dtype=torch.uint8)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
     st = _call(dev, _lib.load().dspark_markov_lm_head_fp4, h.data_ptr(), tag, d, hc.data_ptr(), hs.data_ptr(), rows, 1, V, out.data_ptr(),
@@ -888,12 +888,12 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
     lim = _lib.TokenLimits(*at, num[1], num[0], num[2], num[3])
     _check_device(dev, workspace, uniforms=uniforms)
     tag = _dtype_tag(logits)
-    tokens = torch.empty((B, M), dtype=torch.int64, device=dev)
-    probs = torch.empty((B, M), dtype=torch.float32, device=dev)
+    tokens = logits.new_empty((B, M), dtype=torch.int64)
+    probs = logits.new_empty((B, M), dtype=torch.float32)
     x, u = logits.contiguous(), uniforms.to(torch.float32).contiguous()
     if workspace is None:
         nbytes = int(_lib.load().dspark_markov_sample_filtered_workspace_bytes(B, M, V))
-        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+        buffer = logits.new_empty(nbytes, dtype=torch.uint8)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
     st = _call(dev, _lib.load().dspark_markov_sample_filtered, x.data_ptr(), tag, u.data_ptr(), lim, B, M, V, tokens.data_ptr(),
@@ -928,12 +928,12 @@ def distill_block_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_
     dev = logits.device
     _check_device(dev, workspace, teacher_ids=teacher_ids, teacher_logits=teacher_logits)
     tag, ttag = _dtype_tag(logits), _dtype_tag(teacher_logits)
-    loss = torch.empty((B, M), dtype=torch.float32, device=dev)
-    stats = torch.empty((B, M, 4), dtype=torch.float32, device=dev)
+    loss = logits.new_empty((B, M), dtype=torch.float32)
+    stats = logits.new_empty((B, M, 4), dtype=torch.float32)
     x, ids, t = logits.contiguous(), teacher_ids.to(torch.int64).contiguous(), teacher_logits.contiguous()
     if workspace is None:
         nbytes = int(_lib.load().dspark_markov_distill_workspace_bytes(B, M, V))
-        buffer = torch.empty(nbytes, dtype=torch.uint8, device=dev)  # needs no zero fill
+        buffer = logits.new_empty(nbytes, dtype=torch.uint8)  # needs no zero fill
     else:
         nbytes, buffer = workspace.nbytes, workspace.buffer
     st = _call(dev, _lib.load().dspark_markov_distill_block, x.data_ptr(), tag, ids.data_ptr(), t.data_ptr(), ttag, B, M, V, K, T,
