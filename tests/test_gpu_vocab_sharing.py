@@ -57,6 +57,32 @@ def test_one_workspace_in_turn(native):
             assert _same(call(ws), w)
 
 
+@pytest.mark.parametrize("T", [0.0, 0.8])
+@pytest.mark.parametrize("dtype,v", [(torch.bfloat16, 9008), (torch.float32, 9001)])
+def test_drafts_between_them(native, dtype, v, T):
+    """Drafts, with and without rules, on the workspace that the others have written."""
+    c = Case(50)
+    want = [c.head(), c.sample(), c.distill()]
+    w1, w2 = (0.1 * torch.randn(v, 64, **_gen(s)).to(dtype) for s in (51, 52))
+    base = torch.randn(B, M, v, **_gen(53)).to(dtype)
+    first = torch.randint(0, v, (B,), **_gen(54))
+    history = torch.randint(0, v, (B, 40), **_gen(55))
+    rep = torch.full((B,), 1.3, device="cuda")
+
+    def drafts(**kw):
+        return [*rmd.sample_block_tokens(base, first, w1, w2, temperature=T, seed=3, **kw),
+                *rmd.sample_block_tokens_processed(base, first, w1, w2, temperature=T, seed=3, history=history,
+                                                   repetition_penalty=rep, **kw)]
+
+    plain = drafts()
+    ws = rmd.Workspace(B, M, 9008, 64, sample=True, processed=True, fp4_hidden=D, distill=True, filtered=True)
+    for turn in range(3):
+        for call, w in zip((c.head, c.sample, c.distill), want):
+            assert _same(call(ws), w), turn
+            assert _same(drafts(workspace=ws), plain), turn
+    assert rmd.read_device_error(ws) == 0
+
+
 @pytest.mark.parametrize("name", ["head", "sample", "distill"])
 def test_graphs_share_a_workspace(native, name):
     ws = rmd.Workspace(B, M, V, 1, sample=False, fp4_hidden=D, distill=True, filtered=True)
