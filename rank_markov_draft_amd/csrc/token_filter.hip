@@ -9,8 +9,9 @@
 //
 // The borders decide tokens, and a row has up to V of them, so weights are
 // computed in 64 bits and, wherever sums of them are compared, summed as
-// integers of at least 32 and usually 45 bits below the largest weight: a sum
-// does not depend on its order, and atomics may form it.
+// integers: a sum does not depend on its order, and atomics may form it.  Their
+// unit is 2^-scale of the largest weight, as fine as 62 bits hold the row's sum
+// (Choice::scale).
 //
 // Two launches.  The first reads the rows once, all of the device sharing
 // them, and leaves the largest logit of every group of 128 columns (and the
@@ -299,8 +300,22 @@ __device__ __forceinline__ void sort_keys(Shared& s, int n) {
 __device__ __forceinline__ uint64_t order_key(uint32_t code, uint32_t i) { return ((uint64_t)~code << 32) | i; }
 __device__ __forceinline__ uint32_t key_code(uint64_t k) { return ~(uint32_t)(k >> 32); }
 
+// Rows of more columns than this take the WIDE form.  The scale of the other one
+// goes by V weights of one, so that what a sum of kept weights, which is at
+// least one, loses to its roundings is at most V 2^-(scale + 1): 2^-27 of it at
+// this size, but 1/8 at V = 2^30, where a tail of a tenth of the row vanished.
+// The scale of the WIDE form goes by the row: by its sum where that is known, by
+// top_k up to this number, else by 128 times the sum of the largest weights of
+// the groups that can hold a kept token.  A sum then loses at most V 2^-62 of
+// itself by the first, 2^-26 by the second, 2^-25 by the third (as the kept
+// weights sum to min(1, k / groups) of those largest ones or more).  Past 2^51
+// the integers take a conversion of six instructions: one token of 129280 columns
+// takes 17.7 us in this form, against 17.2, 2048 rows of 151936 730 against 726,
+// and 16 flat rows of 2^20 2.95 ms against 2.84.
+constexpr int64_t kNarrowColumns = 1 << 18;
+
 // A row on its way to a token.
-template <bool BF>
+template <bool BF, bool WIDE>
 struct Choice {
   const char* row;
   int64_t V;
@@ -315,6 +330,7 @@ struct Choice {
   // The mass of a token that passes min_p, else 0.
   __device__ __forceinline__ uint64_t mass(float x) const {
     const double w = exp2_32nds(((double)x - (double)m) * kappa, scale, s->table);
+    if constexpr (WIDE) return w >= min_p ? (uint64_t)__builtin_rint(w) : 0;
     // at most 2^51: the sum's mantissa is the rounded integer
     return w >= min_p ? __builtin_bit_cast(uint64_t, w + 0x1p52) & 0xFFFFFFFFFFFFFull : 0;
   }
@@ -783,7 +799,7 @@ struct Choice {
 // take two more passes over themselves: 2048 of them 500 us, 2.37 GB at 4.7 TB/s;
 // a row alone 69 us (62 at 1024 threads), all barriers and loads that wait for
 // each other.  With at most 128 candidates a row takes 12 us.
-template <bool BF>
+template <bool BF, bool WIDE>
 __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams p, int64_t r0) {
   __shared__ Shared s;
   fill_table(s.table);
@@ -793,17 +809,24 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
   const double* const sums = p.sums + n * G;
   const Limits lim = limits_of(p.limits, n / p.M, V);
   const float u = p.uniforms[n];
-  Choice<BF> c;
+  Choice<BF, WIDE> c;
   c.row = (const char*)p.logits + n * V * (BF ? 2 : 4);
   c.V = V;
   c.kappa = lim.kappa;
   c.s = &s;
-  {
+  auto scale_to = [&](int scale) __attribute__((always_inline)) {
+    c.scale = scale;
+    c.min_p = __builtin_ldexp(lim.min_p, scale);
+  };
+  // the scale at which a sum of weights below z, at least 1, is an integer below 2^62
+  auto scale_by = [&](double z) __attribute__((always_inline)) {
+    scale_to(62 - ((int)(__builtin_bit_cast(uint64_t, z) >> 52) - 1022));
+  };
+  if constexpr (!WIDE) {
     int bits = 0;
     while (((int64_t)1 << bits) < V) ++bits;
-    c.scale = 62 - bits < 51 ? 62 - bits : 51;
+    scale_to(62 - bits < 51 ? 62 - bits : 51);
   }
-  c.min_p = __builtin_ldexp(lim.min_p, c.scale);
   c.part = kPartBits;
   while (((V - 1) >> c.part) >= kParts) ++c.part;
   c.tops = tops;
@@ -921,6 +944,7 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
     for (int64_t g = g0; g < g1; ++g)
       if (tops[g] > kNone) t += sums[g] * weight64(value_of(tops[g]), m, c.kappa, s.table);
     block_scan(t, &z, s);
+    if constexpr (WIDE) scale_by(z);
     whole = (uint64_t)__builtin_rint(__builtin_ldexp(z, c.scale));
     // what weighs less than (1 - top_p) z / V reaches no more than 1 - top_p of
     // z with all its like (and a little less, for the roundings)
@@ -929,6 +953,17 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
     if (f > -3.0e38f) bound = max(bound, min(ordered_code(f), top));
   }
   c.bound = min(bound, top);
+  if constexpr (WIDE) {
+    if (!lim.full && lim.k <= kNarrowColumns) {
+      scale_by((double)lim.k);
+    } else if (!lim.full) {
+      double t = 0.0, z;
+      for (int64_t g = g0; g < g1; ++g)
+        if (tops[g] >= c.bound) t += weight64(value_of(tops[g]), m, c.kappa, s.table);
+      block_scan(t, &z, s);
+      scale_by(kFilterGroup * z);
+    }
+  }
 
   // ---- the groups that reach it, and their tokens, while they fit the list
   uint32_t mine = 0;
@@ -1011,7 +1046,7 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
       for (int h = 0; h < 2; ++h) meet(&befores[lane + 64 * h], n2[h]);
       if (lane == 0) meet(&sums2[0], all);
       __syncthreads();
-      const uint64_t target = Choice<BF>::part_up(whole ? whole : sums2[0], lim.top_p);
+      const uint64_t target = Choice<BF, WIDE>::part_up(whole ? whole : sums2[0], lim.top_p);
 #pragma unroll
       for (int h = 0; h < 2; ++h) w[h] = befores[lane + 64 * h] < target ? w[h] : 0;
     }
@@ -1027,7 +1062,7 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
     if (lane == 0) meet(&sums2[1], all);
     __syncthreads();
     z = sums2[1];
-    const uint64_t target = Choice<BF>::part_down(z, u);
+    const uint64_t target = Choice<BF, WIDE>::part_down(z, u);
     token = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -1041,11 +1076,11 @@ __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams
     for (int i = tid; i < kept; i += kThreads) s.mass[i] = c.mass_of(key_code(s.keys[i]));
     if (lim.nucleus) {
       uint64_t sum;
-      const uint64_t all = c.total(s.mass, kept), target = Choice<BF>::part_up(whole ? whole : all, lim.top_p);
+      const uint64_t all = c.total(s.mass, kept), target = Choice<BF, WIDE>::part_up(whole ? whole : all, lim.top_p);
       if (target <= all) kept = c.reach(s.mass, kept, 0, target, &sum) + 1;
     }
     z = c.total(s.mass, kept);
-    const uint64_t target = Choice<BF>::part_down(z, u);
+    const uint64_t target = Choice<BF, WIDE>::part_down(z, u);
     // by index: the key's halves change places, the lower one now the place in the list
     __syncthreads();
     uint64_t k[kPer];
@@ -1108,7 +1143,10 @@ hipError_t filter_go(const FilterParams& p, hipStream_t s) {
   });
   if (e != hipSuccess) return e;
   return by_rows(p.rows, 1, kThreads, [&](int64_t r, int64_t rows) {
-    hipLaunchKernelGGL(filter_choose_kernel<BF>, dim3((unsigned)rows), dim3(kThreads), 0, s, p, r);
+    if (p.V > kNarrowColumns)
+      hipLaunchKernelGGL((filter_choose_kernel<BF, true>), dim3((unsigned)rows), dim3(kThreads), 0, s, p, r);
+    else
+      hipLaunchKernelGGL((filter_choose_kernel<BF, false>), dim3((unsigned)rows), dim3(kThreads), 0, s, p, r);
   });
 }
 }  // namespace
