@@ -858,9 +858,10 @@ def sample_block_filtered(logits: torch.Tensor, uniforms: torch.Tensor, temperat
     or a tensor [B]; None (and a top_k of 0, a top_p of 1, a min_p of 0) is off.
     A temperature below 1e-5, or None, takes the first of the largest logits (so
     does a row whose largest is +inf or NaN).  A row with nothing above -inf gets token
-    -1 and probability 0.  Weights are computed in 64 bits, to 2^-42 of
-    themselves, and summed as 64-bit integers: a sum is within 2^-27 of itself
-    for V up to 2^18 and within 2^-25 beyond."""
+    -1 and probability 0.  Weights are computed in 64 bits, to 2^-48 of
+    themselves down to a thousandth of the largest, and summed as 64-bit
+    integers: a sum is within 2^-27 of itself for V up to 2^18 and within 2^-25
+    beyond."""
     B, M, V = _block(logits, None, "logits")
     if tuple(uniforms.shape) != (B, M) or not uniforms.is_floating_point():
         raise ValueError(f"uniforms must be float {(B, M)}, got {uniforms.dtype} {tuple(uniforms.shape)}")

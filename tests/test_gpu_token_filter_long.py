@@ -13,7 +13,7 @@ import rank_markov_draft_amd as rmd
 pytestmark = pytest.mark.gpu
 
 F32, BF16 = torch.float32, torch.bfloat16
-# the stated bound on a sum, and as much again for the weights' own 2^-42, the
+# the stated bound on a sum, and as much again for the weights' own 2^-48, the
 # uniform number's and the limits' parts of a sum (2^-40) many times over
 TOL = 2.0 ** -25 + 2.0 ** -38
 
