@@ -469,8 +469,8 @@ dspark_status_t dspark_markov_sample_block_processed(const void* base_logits, ds
  * 2^-48 of themselves down to a thousandth of the largest, and summed as 64-bit
  * integers: a sum of kept weights is within 2^-27 of itself for V up to 2^18 and
  * within 2^-25 beyond, so that a token or a border whose share of the sum lies that
- * close to u or to top_p may be the next one, and a probability is as good as that
- * and its rounding.
+ * close to u or to top_p may be the next one, a weight that close to min_p may fall
+ * to either side, and a probability is as good as its sum and its rounding.
  * A temperature below 1e-5 (or NaN) takes the first of the largest logits, and
  * so does a row whose largest is +inf or NaN (which ranks above +inf, as in
  * dspark_markov_sample_block).  Tokens with a logit of -inf are never drawn: a

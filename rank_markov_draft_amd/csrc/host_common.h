@@ -1,6 +1,6 @@
 // host_common.h -- host-side pieces shared by the translation units of the C
-// ABI (dspark_markov.hip, dspark_serving.hip): the workspace layout, size
-// arithmetic and argument checks.
+// ABI (dspark_markov.hip, dspark_serving.hip, dspark_vocab.hip): the workspace
+// layout, size arithmetic and argument checks.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -35,7 +35,10 @@ namespace host {
 //   data          from kDataOffset: the apply kernels' store sink, or the
 //                 sampling steps' per-(row, vocabulary slice) argmax keys
 //                 (B * ceil(V/128) words), or the backward's and the gated
-//                 head's scratch.
+//                 head's scratch, or the 8-bit and 4-bit heads' quantised
+//                 hidden states and scales, or the token tables of drafts under
+//                 rules, or the limits' group sums and maxima, or the
+//                 distillation's partial sums.
 constexpr size_t kControlBytes = 256;
 constexpr int64_t kChainMaxSteps = 16;
 constexpr size_t kChainAreaBytes =
@@ -104,7 +107,8 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-// Byte ranges that a call reads, for the overlap checks.
+// Byte ranges of a call, for the overlap checks: what it reads, and its outputs
+// too once its scratch is held against them.
 struct Ranges {
   const void* at[16];
   size_t bytes[16];

@@ -181,8 +181,9 @@ __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
 
 // ---------------------------------------------------------------- groups
 // A wave takes 512 columns of a row at a time, 16 lanes a group.  2048 fp32 rows
-// of 151936 with their sums take 255 us (4.9 TB/s, the vector units 0.94 busy with
-// 64-bit weights), 320 bf16 rows of 129280, a few with sums, 26 us, one row 4.6.
+// of 151936 with their sums take 263 us (4.7 TB/s, the vector units 0.96 busy with
+// 64-bit weights), 320 bf16 rows of 129280, a few with sums, 27 us, all 39, none
+// 16, one row 4.6.
 constexpr int kGroupThreads = 256, kTurns = 4;                          // turns of a wave
 constexpr int kGroupSlice = kGroupThreads / 64 * kTurns * 64 * kVec;   // columns of a workgroup
 
@@ -797,8 +798,9 @@ struct Choice {
 // A workgroup a row, two a CU (at 1024 threads 256 x 8 rows took 873 us instead of
 // 740).  Nucleus rows of 151936 fp32 logits with tens of thousands of kept tokens
 // take two more passes over themselves: 2048 of them 500 us, 2.37 GB at 4.7 TB/s;
-// a row alone 69 us (62 at 1024 threads), all barriers and loads that wait for
-// each other.  With at most 128 candidates a row takes 12 us.
+// a row alone 69 us (62 at 1024 threads), 97 of 129280 standard normal logits in
+// bf16, all barriers and loads that wait for each other.  With at most 128
+// candidates a row takes 12 us.
 template <bool BF, bool WIDE>
 __global__ __launch_bounds__(kThreads, 4) void filter_choose_kernel(FilterParams p, int64_t r0) {
   __shared__ Shared s;
